@@ -125,7 +125,7 @@ def _by_expert(idx, N, capacity):
     offsets = torch.cumsum(counts, 0) - counts
     pos = torch.empty_like(key)
     pos[order] = torch.arange(slots, device=idx.device)
-    inv = torch.where(key < N, pos, -1 - pos)
+    inv = torch.where(key < N, pos, -2 - pos)  # a slot without an expert: its zero row, below -1
     perm = torch.where(key[order] < N, order, -1)
     return offsets.int(), perm.int(), inv.int().reshape(idx.shape)
 
