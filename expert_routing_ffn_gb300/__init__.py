@@ -643,3 +643,8 @@ def moe_testing_wait_timeout(ws, stream=None):
 
 
 from .layer import DeviceLayer, LayerBuffers  # noqa: E402,F401
+
+
+from .train import (moe_combine_rows, moe_combine_rows_grad, moe_dispatch_rows, moe_dispatch_rows_grad,  # noqa: E402
+                    moe_experts_down, moe_experts_down_grad, moe_experts_path, moe_experts_up, moe_experts_up_grad,
+                    moe_gate_grad, moe_train_workspace_size)

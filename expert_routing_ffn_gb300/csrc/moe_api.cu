@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "train.h"
 #include "../../include/moe_testing.h"
 #include "tma.h"
 
@@ -239,6 +240,11 @@ moe_status prep_permute(const moe_dims* dims, const int32_t* final_idx, const in
 }
 
 }  // namespace
+
+namespace moe {
+moe_status cuda_failed(cudaError_t e, const char* what) { return record_cuda(e, what); }
+int device_sms() { return sm_count(); }
+}  // namespace moe
 
 extern "C" {
 

@@ -1,0 +1,165 @@
+// The router's gradient: from the gates of a token's slots back through the
+// (optional) renormalisation and the softmax to the logits, with the
+// load-balance loss.
+//   v_e  = sum of d gate over the token's slots on e  (renormalised gates:
+//          (dgate_s - sum_j dgate_j gate_j) / sum_j p_j)  +  c N f_e / T
+//   dl_e = p_e (v_e - sum_j p_j v_j)
+//   loss = c N sum_e f_e P_e,  f_e = slots on e / (T k),  P_e = mean_t p_te
+// T x N floats in and out: bytes for long batches, launch latency for short
+// ones.  A warp owns a token, a lane every 32nd expert.  f and P need the
+// whole batch first; their sums are taken by at most kGateParts blocks in
+// token order and added up by every block of the second launch, so no atomic
+// decides an order.  Without a balance term that first launch is left out.
+#include "common.cuh"
+#include "train.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+
+struct GateParams {
+    const float* prob; const int32_t* idx; const float* dgate;
+    int T, N, k, renorm, parts, rows_per_part;
+    float balance;
+    float *dlogits, *loss, *part;
+};
+
+// part[b][0][e] = slots on e, part[b][1][e] = sum of p_te, over block b's tokens
+__global__ void __launch_bounds__(kThreads) gate_load_kernel(const GateParams p) {
+    extern __shared__ float gsm[];
+    int* slots = reinterpret_cast<int*>(gsm);  // [N]
+    float* psum = gsm + p.N;                   // [kWarps][N]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < p.N; i += kThreads) slots[i] = 0;
+    __syncthreads();
+    grid_dep_wait();
+    const int64_t t0 = (int64_t)blockIdx.x * p.rows_per_part;
+    const int64_t t1 = min(t0 + p.rows_per_part, (int64_t)p.T);
+    for (int64_t i = t0 * p.k + tid; i < t1 * p.k; i += kThreads) {
+        const int e = p.idx[i];
+        if (e >= 0 && e < p.N) atomicAdd(&slots[e], 1);
+    }
+    for (int e = lane; e < p.N; e += 32) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        int64_t t = t0 + warp;
+        for (; t + 3 * kWarps < t1; t += 4 * kWarps)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) s[u] += p.prob[(t + u * kWarps) * p.N + e];
+        for (; t < t1; t += kWarps) s[0] += p.prob[t * p.N + e];
+        psum[warp * p.N + e] = (s[0] + s[1]) + (s[2] + s[3]);
+    }
+    __syncthreads();
+    float* out = p.part + (size_t)blockIdx.x * 2 * p.N;
+    for (int e = tid; e < p.N; e += kThreads) {
+        float s = 0.f;
+        for (int w = 0; w < kWarps; ++w) s += psum[w * p.N + e];
+        out[e] = (float)slots[e];  // below 2^24: exact
+        out[p.N + e] = s;
+    }
+    grid_dep_launch();
+}
+
+template <int NV>  // experts per lane
+__global__ void __launch_bounds__(kThreads) gate_grad_kernel(const GateParams p) {
+    extern __shared__ float gsm[];
+    float* load = gsm;            // [N] c N f_e / T
+    float* lterm = gsm + p.N;     // [N] f_e P_e
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dep_wait();
+    const bool bal = p.parts > 0;
+    if (bal) {
+        for (int e = tid; e < p.N; e += kThreads) {
+            float c = 0.f, s = 0.f;
+#pragma unroll 8
+            for (int b = 0; b < p.parts; ++b) {
+                c += __ldcg(p.part + (size_t)b * 2 * p.N + e);
+                s += __ldcg(p.part + (size_t)b * 2 * p.N + p.N + e);
+            }
+            const float f = c / ((float)p.T * (float)p.k);
+            load[e] = p.balance * (float)p.N / (float)p.T * f;
+            lterm[e] = f * (s / (float)p.T);
+        }
+        __syncthreads();
+    }
+    if (blockIdx.x == 0 && tid == 0 && p.loss) {
+        float l = 0.f;
+        if (bal)
+            for (int e = 0; e < p.N; ++e) l += lterm[e];
+        p.loss[0] = p.balance * (float)p.N * l;
+    }
+    for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < p.T; t += (int64_t)gridDim.x * kWarps) {
+        const float* row = p.prob + t * p.N;
+        int my_e = -1;
+        float my_d = 0.f;
+        if (lane < p.k) {
+            my_e = p.idx[t * p.k + lane];
+            if (my_e < 0 || my_e >= p.N) my_e = -1;
+            else my_d = p.dgate[t * p.k + lane];
+        }
+        float q[NV], v[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = i * 32 + lane;
+            q[i] = e < p.N ? row[e] : 0.f;
+            v[i] = bal && e < p.N ? load[e] : 0.f;
+        }
+        if (p.renorm) {
+            const float my_p = my_e >= 0 ? row[my_e] : 0.f;
+            const float total = warp_sum(my_p);
+            const float inv = total > 0.f ? 1.f / total : 0.f;
+            const float mean = warp_sum(my_d * (my_p * inv));
+            my_d = my_e >= 0 ? (my_d - mean) * inv : 0.f;
+        }
+        for (int s = 0; s < p.k; ++s) {
+            const int e = __shfl_sync(0xffffffffu, my_e, s);
+            const float dg = __shfl_sync(0xffffffffu, my_d, s);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (e == i * 32 + lane) v[i] += dg;
+        }
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) dot = fmaf(q[i], v[i], dot);
+        dot = warp_sum(dot);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (i * 32 + lane < p.N) p.dlogits[t * p.N + i * 32 + lane] = q[i] * (v[i] - dot);
+    }
+    grid_dep_launch();
+}
+
+}  // namespace
+
+cudaError_t launch_gate_grad(const GateGradArgs& a, cudaStream_t st, int* launches) {
+    GateParams p;
+    p.prob = a.prob; p.idx = a.idx; p.dgate = a.dgate;
+    p.T = a.T; p.N = a.N; p.k = a.k; p.renorm = a.renorm; p.balance = a.balance;
+    p.dlogits = a.dlogits; p.loss = a.loss; p.part = a.part;
+    p.parts = 0; p.rows_per_part = 0;
+    *launches = 1;
+    if (a.balance > 0.f) {
+        // 32 tokens a block at least: shorter batches have fewer blocks to add up
+        int parts = (a.T + 31) / 32;
+        if (parts > kGateParts) parts = kGateParts;
+        p.rows_per_part = (a.T + parts - 1) / parts;
+        p.parts = (a.T + p.rows_per_part - 1) / p.rows_per_part;
+        const size_t smem = (size_t)a.N * (1 + kWarps) * 4;
+        cudaError_t e = launch_pdl(gate_load_kernel, dim3(p.parts), dim3(kThreads), smem, st, p);
+        if (e != cudaSuccess) return e;
+        *launches = 2;
+    }
+    int64_t blocks = ((int64_t)a.T + kWarps - 1) / kWarps;
+    if (blocks > (int64_t)a.sms * 8) blocks = (int64_t)a.sms * 8;
+    const dim3 grid((unsigned)blocks);
+    const size_t smem = (size_t)a.N * 2 * 4;
+    const int nv = (a.N + 31) / 32;
+    return nv <= 1 ? launch_pdl(gate_grad_kernel<1>, grid, dim3(kThreads), smem, st, p)
+         : nv <= 2 ? launch_pdl(gate_grad_kernel<2>, grid, dim3(kThreads), smem, st, p)
+         : nv <= 4 ? launch_pdl(gate_grad_kernel<4>, grid, dim3(kThreads), smem, st, p)
+         : nv <= 8 ? launch_pdl(gate_grad_kernel<8>, grid, dim3(kThreads), smem, st, p)
+                   : launch_pdl(gate_grad_kernel<16>, grid, dim3(kThreads), smem, st, p);
+}
+
+}  // namespace moe
