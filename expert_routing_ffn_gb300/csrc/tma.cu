@@ -60,6 +60,27 @@ moe_status encode_f32_2d(void* out128, const void* base, uint64_t inner, uint64_
                      box_outer);
 }
 
+moe_status encode_3d(void* out128, bool bf16, const void* base, uint64_t inner, uint64_t middle, uint64_t outer,
+                     uint32_t box_inner, uint32_t box_middle) {
+    auto fn = encode_fn();
+    if (!fn) return MOE_ERR_CUDA;
+    const uint64_t row = inner * (bf16 ? 2 : 4);
+    if ((reinterpret_cast<uintptr_t>(base) & 15u) || (row & 15u)) return MOE_ERR_INVALID_ARG;
+    CUtensorMap m;
+    std::memset(&m, 0, sizeof(m));
+    const cuuint64_t dims[3] = {inner, middle, outer};
+    const cuuint64_t strides[2] = {row, row * middle};
+    const cuuint32_t box[3] = {box_inner, box_middle, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(&m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+                    const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return MOE_ERR_INVALID_ARG;
+    std::memcpy(out128, &m, sizeof(m));
+    return MOE_OK;
+}
+
 moe_status encode_expert_tmaps(ExpertEntry& E, int d) {
     // gate / up: K-major tiles of 128 channels x 64 hidden values
     for (int m = 0; m < 2; ++m)

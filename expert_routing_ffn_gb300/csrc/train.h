@@ -95,6 +95,7 @@ struct GroupedArgs {
     DevError* err;
     int sms;
 };
+bool grouped_tc_shapes(bool bf16, int d, int I);
 bool grouped_tc_usable(const GroupedArgs& a);
 cudaError_t launch_grouped_simt(const GroupedArgs& a, cudaStream_t st);
 cudaError_t launch_grouped_tc(const GroupedArgs& a, cudaStream_t st, int* launches);

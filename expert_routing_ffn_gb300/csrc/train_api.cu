@@ -87,7 +87,8 @@ GroupedArgs grouped(const moe_dims* D, TrainForm form, const int32_t* offsets, v
 
 moe_status run_grouped(const GroupedArgs& a, void* stream, const char* what) {
     int launches = 1;
-    const cudaError_t e = launch_grouped_simt(a, S(stream));
+    const cudaError_t e = grouped_tc_usable(a) ? launch_grouped_tc(a, S(stream), &launches)
+                                               : launch_grouped_simt(a, S(stream));
     if (e != cudaSuccess) return cuda_failed(e, what);
     note_launches(launches);
     return MOE_OK;
@@ -290,7 +291,7 @@ moe_status moe_experts_down_grad(const moe_dims* dims, const void* dy_perm, cons
 
 const char* moe_experts_path(const moe_dims* dims) {
     if (check_dims(dims) != MOE_OK) return "unsupported";
-    return "simt";
+    return grouped_tc_shapes(dims->wtype == MOE_DTYPE_BF16, dims->d, dims->I) ? "tc" : "simt";
 }
 
 }  // extern "C"

@@ -110,8 +110,8 @@ moe_status moe_gate_grad(const moe_dims* dims, const float* router_prob, const i
  *   g = x Wg_e^T, u = x Wu_e^T, h = SiLU(g) (.) u.
  *   x_perm [T*k, d]; w_gate, w_up [N, I, d]; g, u (both or neither NULL: kept
  *   for the gradient) and h: [T*k, I].  Tensor cores when wtype is bf16, d and
- *   I are multiples of 8 and the matrices are 16-byte aligned; CUDA cores in
- *   float32 arithmetic otherwise.  moe_experts_path names the choice. */
+ *   I are multiples of 8 from 64 on and every matrix is 16-byte aligned; CUDA
+ *   cores in float32 arithmetic otherwise.  moe_experts_path names the choice. */
 moe_status moe_experts_up(const moe_dims* dims, const void* x_perm, const int32_t* expert_offsets,
                           const void* w_gate, const void* w_up, void* g, void* u, void* h, void* ws,
                           size_t ws_bytes, void* stream);
