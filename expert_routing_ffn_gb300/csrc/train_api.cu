@@ -86,11 +86,12 @@ GroupedArgs grouped(const moe_dims* D, TrainForm form, const int32_t* offsets, v
 }
 
 moe_status run_grouped(const GroupedArgs& a, void* stream, const char* what) {
-    int launches = 1;
-    const cudaError_t e = grouped_tc_usable(a) ? launch_grouped_tc(a, S(stream), &launches)
-                                               : launch_grouped_simt(a, S(stream));
+    const bool tc = grouped_tc_usable(a), dw = a.form == kFormDw;
+    const cudaError_t e = !tc  ? launch_grouped_simt(a, S(stream))
+                          : dw ? launch_grouped_dw_tc(a, S(stream))
+                               : launch_grouped_rows_tc(a, S(stream));
     if (e != cudaSuccess) return cuda_failed(e, what);
-    note_launches(launches);
+    note_launches(tc && dw ? 2 : 1);
     return MOE_OK;
 }
 

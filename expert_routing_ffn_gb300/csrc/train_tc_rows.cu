@@ -1,0 +1,550 @@
+// The experts' products that give grouped rows, on the tensor cores (tcgen05,
+// accumulators in tensor memory), fed by TMA.  With x, h, dy, dg, du the
+// grouped rows and Wg, Wu, Wd [I, d] an expert's weights:
+//   Up    g = x Wg^T, u = x Wu^T       K = d; epilogue h = SiLU(g) u
+//   Down  y = h Wd                     K = I
+//   Dh    dh = dy Wd^T                 K = d; epilogue dg, du from g, u
+//   Dx    dx = dg Wg + du Wu           K = I twice, one accumulator
+//
+// The weights are the MMA's M side and the rows its N side: a tile is 256
+// weight rows (or columns) on a CTA pair (2-CTA MMA, 128 accumulator lanes in
+// each CTA) x up to 256 grouped rows.  N goes in steps of 32, so a segment's
+// rows are split into equal tiles and a ragged end costs at most 31 rows,
+// where rows on the M side cost up to 255: 384 rows an expert took 2 tiles of
+// 256 (DeepSeek-V2-Lite shape, 4096 tokens), a third of the MMA work wasted.
+// It also serves a decode-size batch, N = 32, as a pure stream of weights.
+//
+// The accumulator comes out transposed (a lane is a channel, a column a row of
+// the output).  tcgen05.ld in the 16x256b shape hands it out in the layout of
+// matrix fragments, and stmatrix with transposition writes it to shared memory
+// as rows of 64 channels (128 bytes, swizzled), whence TMA stores it.  In Up
+// a CTA's M side is 64 gate rows and 64 up rows; the warps that hold g and
+// those that hold u of the same channels swap half of their values through
+// shared memory, in fp32.  In Dh g and u come in by TMA and ldmatrix in the
+// same layout, and dg, du overwrite them.
+//
+// The tiles of all experts form one list (expert by expert, row tiles
+// innermost: a weight tile read by several of them comes from L2 after the
+// first), taken round robin by the resident pairs.
+//
+// Block: warp 0 issues the TMA loads, warp 1 the MMAs (one thread of the
+// pair's leader), warps 2-5 the epilogue, in panels of 32 rows through a ring
+// of buffers.  Accumulators are double-buffered.  Every wait is bounded.
+#include <cuda.h>
+
+#include <array>
+#include <cstring>
+#include <mutex>
+#include <vector>
+
+#include "common.cuh"
+#include "tma.h"
+#include "train.h"
+#include "train_tc.cuh"
+
+namespace moe {
+
+namespace {
+
+using namespace train;
+
+constexpr int kThreads = 192, kEpiThreads = 128;
+constexpr int kMaxN = 256;     // rows of a tile, at most
+constexpr int kStepN = 32;     // granularity of N on a CTA pair
+constexpr int kPanel = 32;     // rows per epilogue panel
+constexpr uint32_t kBK = kTcBK;
+constexpr uint32_t kStageA = 128 * kBK * 2, kStageB = kMaxN / 2 * kBK * 2, kStage = kStageA + kStageB;
+constexpr uint32_t kBox = kPanel * 128;  // 32 rows x 64 channels
+
+template <int FORM>
+struct Cfg {
+    static constexpr bool kNT = FORM == kFormUp || FORM == kFormDh;  // weights K-major
+    static constexpr int kChannels = FORM == kFormUp ? 64 : 128;     // output channels of one CTA
+    static constexpr int kBoxes = FORM == kFormUp ? 3 : FORM == kFormDh ? 4 : 2;  // boxes of a panel
+    static constexpr int kBuffers = 3;
+    static constexpr int kStages = FORM == kFormDh || FORM == kFormUp ? 5 : 6;
+    static constexpr uint32_t kPanels = kStages * kStage;  // epilogue buffers
+    static constexpr uint32_t kSwap = kPanels + kBuffers * kBoxes * kBox;  // Up: 2 x 64 bytes a thread
+    static constexpr uint32_t kTables = kSwap + (FORM == kFormUp ? 2 * kEpiThreads * 64 : 0);
+    static constexpr uint32_t kBars = kTables + 2 * ((kTrainMaxExperts + 1) * 4 + 15) / 16 * 16;
+    static constexpr uint32_t kSmem = kBars + (2 * kStages + 5 + kBuffers) * 8 + 16;
+    static_assert(kSmem <= 232448, "227 KB of shared memory per block");
+};
+
+struct RowsParams {
+    CUtensorMap a[2];         // weights
+    CUtensorMap b[2][kMaxN / 32];  // rows [M, K] in boxes of 16, 32, .. 128 rows
+    CUtensorMap in[2];        // Dh: g, u
+    CUtensorMap o[3];         // outputs (boxes of 32 rows x 64 channels)
+    __nv_bfloat16* out[3];
+    const int32_t* offsets;
+    int M, N, d, I;
+    DevError* err;
+};
+
+// 1 / (1 + e^-g) with the fast exponential and division (a few ulp in fp32;
+// the results are rounded to bf16).  e^-g overflows to infinity for very
+// negative g and 1 / (1 + inf) = 0, the limit.
+__device__ __forceinline__ float fast_sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+
+__device__ __forceinline__ uint32_t pack_f(uint32_t lo, uint32_t hi) {
+    return pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
+}
+
+struct Tile {
+    int e, row0, rows, c0;  // expert, first row, rows of the tile (1..256), first channel of the pair
+};
+__device__ __forceinline__ int row_tiles(int rows) { return (rows + kMaxN - 1) / kMaxN; }
+// rows of a tile when `rows` are split into equal tiles: a multiple of 32
+__device__ __forceinline__ int tile_rows(int rows) {
+    const int n = row_tiles(rows);
+    return ((rows + n - 1) / n + kStepN - 1) / kStepN * kStepN;
+}
+
+template <int FORM>
+__device__ __forceinline__ Tile decode(int N, const int* first, const int* row_s, int t) {
+    int lo = 0, hi = N;
+    while (hi - lo > 1) {  // the last expert whose tiles start at or before t
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    const int r0 = row_s[lo], rows = row_s[lo + 1] - r0, mts = row_tiles(rows), per = tile_rows(rows);
+    const int local = t - first[lo], m = local % mts;
+    Tile x;
+    x.e = lo;
+    x.row0 = r0 + m * per;
+    x.rows = min(per, rows - m * per);
+    x.c0 = local / mts * 2 * Cfg<FORM>::kChannels;
+    return x;
+}
+
+template <int FORM>
+__global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_constant__ RowsParams p) {
+    using C = Cfg<FORM>;
+    constexpr int kS = C::kStages, kNB = C::kBuffers;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    int* first = reinterpret_cast<int*>(smem + C::kTables);
+    int* row_s = first + kTrainMaxExperts + 1;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBars);
+    uint64_t *empty = full + kS, *tfull = empty + kS, *tempty = tfull + 2, *drain = tempty + 2, *pfull = drain + 1;
+    uint32_t* tmem_s = reinterpret_cast<uint32_t*>(pfull + kNB);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_s + 1);
+
+    grid_dep_wait();  // the previous kernels' outputs; no tensor memory is taken before it
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = smem_u32(smem);
+    const uint32_t rank = cluster_rank();
+    const bool leader = rank == 0;
+    const int unit = (int)(blockIdx.x >> 1), n_units = (int)(gridDim.x >> 1);
+    const int n_cols = C::kNT ? p.I : p.d;                   // channels of the output
+    const int K = C::kNT ? p.d : p.I;
+    const int nk1 = (K + (int)kBK - 1) / (int)kBK, nk = FORM == kFormDx ? 2 * nk1 : nk1;
+
+    // rows before each expert (never beyond M, never backwards), tiles before each expert
+    for (int e = tid; e <= p.N; e += kThreads) row_s[e] = min(max(p.offsets[e], 0), p.M);
+    if (tid == 32) {
+        for (int s = 0; s < kS; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], 8);  // an arrival per epilogue warp of both CTAs
+        }
+        mbar_init(drain, 1);
+        for (int b = 0; b < kNB; ++b) mbar_init(&pfull[b], 1);
+        fence_mbar_init();
+        *abort_flag = 0;
+        if (base & 1023u) {  // the swizzled tiles need it
+            set_error(p.err, MOE_ERR_CAPACITY, 1023);
+            *abort_flag = 1;
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const int cts = (n_cols + 2 * C::kChannels - 1) / (2 * C::kChannels);
+        int carry = 0;
+        for (int b = 0; b < p.N; b += 32) {
+            const int e = b + lane;
+            const int v = e < p.N ? row_tiles(max(row_s[e + 1] - row_s[e], 0)) * cts : 0;
+            int inc = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += x;
+            }
+            if (e < p.N) first[e] = carry + inc - v;
+            carry += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) first[p.N] = carry;
+    }
+    if (warp == 1) tmem_alloc<true>(tmem_s);
+    {  // rows of no expert
+        const int64_t v0 = (int64_t)row_s[p.N] * n_cols / 8, v1 = (int64_t)p.M * n_cols / 8;
+        for (int64_t v = v0 + (int64_t)blockIdx.x * kThreads + tid; v < v1; v += (int64_t)gridDim.x * kThreads)
+            for (int o = 0; o < 3; ++o)
+                if (p.out[o]) reinterpret_cast<uint4*>(p.out[o])[v] = make_uint4(0, 0, 0, 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the peer's barriers are ready before any arrival from here
+    tc_fence_after();
+    const uint32_t tmem = *tmem_s;
+    const int n_tiles = first[p.N];
+
+    if (warp == 0) {
+        // ---------------- loads (each CTA its own stages, on the leader's barrier)
+        if (lane == 0) {
+            int it = 0;
+            for (int t = unit; t < n_tiles && !*abort_flag; t += n_units) {
+                const Tile x = decode<FORM>(p.N, first, row_s, t);
+                const int half = (x.rows + kStepN - 1) / kStepN * kStepN / 2;  // rows staged by each CTA
+                const int brow = x.row0 + (int)rank * half;
+                const int ch = x.c0 + (int)rank * C::kChannels;
+                for (int kb = 0; kb < nk; ++kb, ++it) {
+                    const int st = it % kS;
+                    if (!wait<true>(&empty[st], ((it / kS) & 1) ^ 1, abort_flag, p.err, 1)) break;
+                    const uint32_t ad = base + st * kStage, bd = ad + kStageA;
+                    const uint32_t bar = leader_address(&full[st]);
+                    if (leader) mbar_arrive_expect_tx(&full[st], 2 * (kStageA + (uint32_t)half * 128));
+                    const int part = FORM == kFormDx && kb >= nk1;
+                    const int k0 = (kb - part * nk1) * (int)kBK;
+                    if constexpr (FORM == kFormUp) {
+                        load_3d<true>(ad, &p.a[0], k0, ch, x.e, bar);
+                        load_3d<true>(ad + 8192, &p.a[1], k0, ch, x.e, bar);
+                    } else if constexpr (FORM == kFormDh) {
+                        load_3d<true>(ad, &p.a[0], k0, ch, x.e, bar);
+                    } else {
+                        load_3d<true>(ad, &p.a[part], ch, k0, x.e, bar);
+                        load_3d<true>(ad + 8192, &p.a[part], ch + 64, k0, x.e, bar);
+                    }
+                    load_2d<true>(bd, &p.b[part][half / 16 - 1], k0, brow, bar);
+                }
+            }
+            // the leader's MMAs have consumed this CTA's last stages before it may leave
+            for (int k = it > kS ? it - kS : 0; k < it; ++k)
+                (void)wait<true>(&empty[k % kS], (k / kS) & 1, abort_flag, p.err, 2, false);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMAs (the pair's leader)
+        if (lane == 0 && leader) {
+            int it = 0, local = 0;
+            for (int t = unit; t < n_tiles; t += n_units, ++local) {
+                if (*abort_flag) break;
+                const Tile x = decode<FORM>(p.N, first, row_s, t);
+                const uint32_t idesc = tc_idesc(256, (x.rows + kStepN - 1) / kStepN * kStepN, 0, C::kNT ? 0 : 1);
+                const int ab = local & 1;
+                if (!wait<true>(&tempty[ab], ((local >> 1) & 1) ^ 1, abort_flag, p.err, 3)) break;
+                tc_fence_after();
+                bool ok = true;
+                for (int kb = 0; kb < nk; ++kb, ++it) {
+                    const int st = it % kS;
+                    if (!wait<true>(&full[st], (it / kS) & 1, abort_flag, p.err, 4)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t ad = base + st * kStage, bd = ad + kStageA;
+#pragma unroll
+                    for (int kk = 0; kk < (int)kBK / 16; ++kk) {
+                        // K-major: 16 values = 32 bytes along the swizzled row; MN-major: 16 rows of
+                        // 128 bytes, the next 64 channels 8 KB on
+                        const uint64_t da = C::kNT ? smem_desc(ad + kk * 32, 16, 1024) : smem_desc(ad + kk * 2048, 8192, 1024);
+                        mma<true>(tmem + ab * kMaxN, da, smem_desc(bd + kk * 32, 16, 1024), idesc, (kb | kk) ? 1u : 0u);
+                    }
+                    commit<true>(&empty[st]);
+                }
+                if (!ok) break;
+                commit<true>(&tfull[ab]);
+            }
+            // every MMA issued here is done before tensor memory is released
+            commit_local<true>(drain);
+            (void)wait<true>(drain, 0, abort_flag, p.err, 6, false);
+        }
+    } else {
+        // ---------------- epilogue: warps 2..5, warp w on tensor-memory lanes 32 (w % 4) ...
+        const int quarter = warp & 3, etid = tid - 64;
+        const bool boss = etid == 0;  // issues this CTA's output stores (and Dh's input loads)
+        const uint32_t panels = base + C::kPanels;
+        const uint32_t free0 = leader_address(&tempty[0]), free1 = leader_address(&tempty[1]);
+        // stmatrix / ldmatrix: lanes 8j .. 8j + 7 address matrix j, a row of 16 bytes each
+        const int mj = lane >> 3, mr = lane & 7;
+        // this warp's 32 channels: the box and the first 16-byte chunk in its rows
+        const int my_box = quarter >> 1, my_chunk = (quarter & 1) * 4;
+        int local = 0, pn = 0;
+        uint32_t in_phase = 0;  // Dh: parity of each buffer's input barrier
+        // Dh: g and u of 32 rows from q0 on into buffer `buf`
+        auto load_inputs = [&](const Tile& x, int ch, int q0, int buf) {
+            const uint32_t dst = panels + buf * C::kBoxes * kBox, bar = smem_u32(&pfull[buf]);
+            const int n_box = ch + 64 < n_cols ? 2 : 1;
+            mbar_arrive_expect_tx(&pfull[buf], 2 * n_box * kBox);
+            for (int j = 0; j < n_box; ++j) {
+                load_2d<false>(dst + j * kBox, &p.in[0], ch + j * 64, x.row0 + q0, bar);
+                load_2d<false>(dst + (2 + j) * kBox, &p.in[1], ch + j * 64, x.row0 + q0, bar);
+            }
+        };
+        for (int t = unit; t < n_tiles; t += n_units, ++local) {
+            const Tile x = decode<FORM>(p.N, first, row_s, t);
+            const int ch = x.c0 + (int)rank * C::kChannels;
+            const bool any = ch < n_cols;  // this CTA's channels lie in the output
+            if (FORM == kFormDh && any && boss) {  // the first panel's inputs, beside the tile's MMAs
+                stores_read<kNB - 1>();
+                load_inputs(x, ch, 0, pn % kNB);
+            }
+            const int ab = local & 1;
+            bool ok = true;
+            if (lane == 0) ok = wait<true>(&tfull[ab], (local >> 1) & 1, abort_flag, p.err, 5);
+            // the four warps share barriers: they leave together
+            const bool stop = bar_any(1, kEpiThreads, !ok || *abort_flag);
+            tc_fence_after();
+            const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + ab * kMaxN;
+            if (any) {
+#pragma unroll 1
+                for (int q0 = 0; q0 < x.rows; q0 += kPanel, ++pn) {
+                    const uint32_t buf = panels + (pn % kNB) * C::kBoxes * kBox;
+                    if (FORM == kFormDh && boss && q0 + kPanel < x.rows) {
+                        stores_read<1>();
+                        load_inputs(x, ch, q0 + kPanel, (pn + 1) % kNB);
+                    }
+                    uint32_t lo[16], hi[16];  // lanes 0-15 and 16-31 of the warp's quarter
+                    tmem_ld_16x32(taddr + q0, lo);
+                    tmem_ld_16x32(taddr + (16u << 16) + q0, hi);
+                    tmem_ld_wait();
+                    if constexpr (FORM == kFormUp) {
+                        // warps of quarters 0, 1 hold g and those of 2, 3 hold u of the same channels, at the
+                        // same registers.  Each pair of warps swaps 16 rows' values for the other 16's, in
+                        // fp32, and forms h of the rows it then has both of.
+                        const bool is_u = quarter >= 2;
+                        float4* mine = reinterpret_cast<float4*>(smem + C::kSwap + (pn & 1) * kEpiThreads * 64) + etid;
+                        const float4* theirs = mine + ((warp ^ 6) - warp) * 32;
+                        // g gives away rows 16-31 (blocks 2, 3), u rows 0-15
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t* l = is_u ? lo + 4 * i : lo + 8 + 4 * i;
+                            const uint32_t* h = is_u ? hi + 4 * i : hi + 8 + 4 * i;
+                            mine[(2 * i) * kEpiThreads] = make_float4(__uint_as_float(l[0]), __uint_as_float(l[1]),
+                                                                      __uint_as_float(l[2]), __uint_as_float(l[3]));
+                            mine[(2 * i + 1) * kEpiThreads] = make_float4(__uint_as_float(h[0]), __uint_as_float(h[1]),
+                                                                          __uint_as_float(h[2]), __uint_as_float(h[3]));
+                        }
+                        const uint32_t at = buf + mr * 128 + (((my_chunk + mj) ^ mr) << 4);
+                        if (p.out[0]) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                stmatrix_x4_trans(at + (is_u ? kBox : 0) + i * 1024, pack_f(lo[4 * i], lo[4 * i + 1]),
+                                                  pack_f(lo[4 * i + 2], lo[4 * i + 3]), pack_f(hi[4 * i], hi[4 * i + 1]),
+                                                  pack_f(hi[4 * i + 2], hi[4 * i + 3]));
+                        }
+                        bar_sync(2 + (quarter & 1), 64);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {
+                                const float4 o = theirs[(2 * i + z) * kEpiThreads];
+                                const uint32_t* m = z ? (is_u ? hi + 8 + 4 * i : hi + 4 * i) : (is_u ? lo + 8 + 4 * i : lo + 4 * i);
+                                const float of[4] = {o.x, o.y, o.z, o.w};
+                                float v[4];
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const float mf = __uint_as_float(m[q]);
+                                    const float g = is_u ? of[q] : mf, u = is_u ? mf : of[q];
+                                    v[q] = g * fast_sigmoid(g) * u;
+                                }
+                                w[2 * z] = pack_bf16x2(v[0], v[1]);
+                                w[2 * z + 1] = pack_bf16x2(v[2], v[3]);
+                            }
+                            stmatrix_x4_trans(at + 2 * kBox + ((is_u ? 2 : 0) + i) * 1024, w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+                        const uint32_t at = buf + my_box * kBox + mr * 128 + (((my_chunk + mj) ^ mr) << 4);
+                        if constexpr (FORM == kFormDh) {
+                            if (lane == 0)
+                                (void)wait<false>(&pfull[pn % kNB], (in_phase >> (pn % kNB)) & 1, abort_flag, p.err, 7, false);
+                            __syncwarp();
+                            in_phase ^= 1u << (pn % kNB);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {  // 8 rows, 32 channels
+                            const uint32_t* h[4] = {lo + 4 * i, lo + 4 * i + 2, hi + 4 * i, hi + 4 * i + 2};
+                            if constexpr (FORM == kFormDh) {
+                                uint32_t g[4], u[4], a[4], b[4];
+                                ldmatrix_x4_trans(at + i * 1024, g[0], g[1], g[2], g[3]);
+                                ldmatrix_x4_trans(at + 2 * kBox + i * 1024, u[0], u[1], u[2], u[3]);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    float da[2], db[2];
+#pragma unroll
+                                    for (int z = 0; z < 2; ++z) {
+                                        const float gf = z ? bf16_hi(g[j]) : bf16_lo(g[j]);
+                                        const float uf = z ? bf16_hi(u[j]) : bf16_lo(u[j]);
+                                        const float dh = __uint_as_float(h[j][z]), s = fast_sigmoid(gf);
+                                        da[z] = dh * uf * s * (1.f + gf * (1.f - s));
+                                        db[z] = dh * gf * s;
+                                    }
+                                    a[j] = pack_bf16x2(da[0], da[1]);
+                                    b[j] = pack_bf16x2(db[0], db[1]);
+                                }
+                                stmatrix_x4_trans(at + i * 1024, a[0], a[1], a[2], a[3]);
+                                stmatrix_x4_trans(at + 2 * kBox + i * 1024, b[0], b[1], b[2], b[3]);
+                            } else {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    w[j] = pack_bf16x2(__uint_as_float(h[j][0]), __uint_as_float(h[j][1]));
+                                stmatrix_x4_trans(at + i * 1024, w[0], w[1], w[2], w[3]);
+                            }
+                        }
+                    }
+                    fence_proxy_async();
+                    // the next panel's buffer is free once the store that last used it has read it
+                    if (FORM != kFormDh && boss) stores_read<kNB - 2>();
+                    bar_sync(1, kEpiThreads);
+                    // box b of the buffer: which output, and its first channel
+                    auto out_of = [&](int b) { return FORM == kFormUp ? b : FORM == kFormDh ? b >> 1 : 0; };
+                    auto col_of = [&](int b) { return ch + (FORM == kFormUp ? 0 : (b & 1) * 64); };
+                    const int n_rows = x.rows - q0;
+                    if (n_rows >= kPanel) {
+                        if (boss) {
+#pragma unroll
+                            for (int b = 0; b < C::kBoxes; ++b)
+                                if (p.out[out_of(b)] && col_of(b) < n_cols)
+                                    store_2d(&p.o[out_of(b)], col_of(b), x.row0 + q0, buf + b * kBox);
+                        }
+                    } else {  // the rows after these are another expert's
+                        for (int c = etid; c < C::kBoxes * n_rows * 8; c += kEpiThreads) {
+                            const int b = c / (n_rows * 8), r = c / 8 % n_rows, q = c & 7;
+                            const int col = col_of(b) + q * 8;
+                            if (p.out[out_of(b)] && col < n_cols)
+                                *reinterpret_cast<uint4*>(p.out[out_of(b)] + (int64_t)(x.row0 + q0 + r) * n_cols + col) =
+                                    *reinterpret_cast<const uint4*>(smem + (buf - base) + b * kBox + r * 128 + ((q ^ (r & 7)) << 4));
+                        }
+                    }
+                    if (boss) stores_commit();  // a group per panel, empty or not
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (!leader) arrive_cluster(ab ? free1 : free0);
+                else mbar_arrive(&tempty[ab]);
+            }
+            if (stop) break;
+        }
+        // the buffers stay until the stores have read them, and the outputs are
+        // complete when the grid ends
+        if (boss) stores_done();
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    // the leader's MMAs, which read the peer's shared memory and write its
+    // tensor memory, are done before either CTA frees or leaves
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 1) tmem_free<true>(tmem);
+    grid_dep_launch();
+}
+
+// ---------------------------------------------------------------- host
+
+template <int FORM>
+cudaError_t launch_form(const RowsParams& p, int64_t units, int sms, cudaStream_t st) {
+    auto kern = grouped_rows_kernel<FORM>;
+    constexpr uint32_t kSmem = Cfg<FORM>::kSmem;
+    cudaError_t e = allow_max_smem(kern);
+    if (e != cudaSuccess) return e;
+    int most = 0;
+    e = resident_pairs(reinterpret_cast<const void*>(kern), kThreads, kSmem, sms, &most);
+    if (e != cudaSuccess) return e;
+    if (most <= 0) return cudaErrorInvalidConfiguration;
+    if (units > most) units = most;
+    return note_launch(reinterpret_cast<const void*>(kern), kThreads, kSmem,
+                       launch_units(kern, p, (int)units, true, kThreads, kSmem, st));
+}
+
+}  // namespace
+
+bool grouped_tc_shapes(bool bf16, int d, int I) {
+    // rows on 16-byte boundaries; below 64 a K step or a box is mostly padding
+    return bf16 && d % 8 == 0 && I % 8 == 0 && d >= 64 && I >= 64;
+}
+
+bool grouped_tc_usable(const GroupedArgs& a) {
+    if (!grouped_tc_shapes(a.bf16, a.d, a.I) || a.M == 0) return false;
+    for (const void* q : {a.a0, a.a1, a.b0, a.b1, a.g, a.u, (const void*)a.o0, (const void*)a.o1, (const void*)a.o2})
+        if (reinterpret_cast<uintptr_t>(q) & 15u) return false;
+    return true;
+}
+
+cudaError_t resident_pairs(const void* kernel, int threads, uint32_t smem, int sms, int* pairs) {
+    static std::mutex mu;
+    static std::vector<std::array<int64_t, 3>> done;  // kernel, device, pairs
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    for (const auto& x : done)
+        if (x[0] == (int64_t)reinterpret_cast<uintptr_t>(kernel) && x[1] == dev) { *pairs = (int)x[2]; return cudaSuccess; }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sms & ~1);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    *pairs = n < sms / 2 ? n : sms / 2;
+    done.push_back({(int64_t)reinterpret_cast<uintptr_t>(kernel), dev, *pairs});
+    return cudaSuccess;
+}
+
+cudaError_t launch_grouped_rows_tc(const GroupedArgs& a, cudaStream_t st) {
+    RowsParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.offsets = a.offsets; p.err = a.err;
+    p.M = a.M; p.N = a.N; p.d = a.d; p.I = a.I;
+    const bool nt = a.form == kFormUp || a.form == kFormDh;
+    const uint64_t d = (uint64_t)a.d, I = (uint64_t)a.I, M = (uint64_t)a.M;
+    const uint64_t K = nt ? d : I, cols = nt ? I : d;
+    const int pair_channels = a.form == kFormUp ? 128 : 256;
+    bool ok = true;
+    const void* rows[2] = {a.a0, a.a1};
+    const void* weights[2] = {a.b0, a.b1};
+    const void* in[2] = {a.g, a.u};
+    void* outs[3] = {a.o0, a.o1, a.o2};
+    auto rows_map = [&](CUtensorMap* m, const void* base, uint64_t width, uint32_t box_rows) {
+        ok = ok && encode_bf16_2d(m, base, width, M, width * 2, 64, box_rows) == MOE_OK;
+    };
+    for (int i = 0; i < 2; ++i) {
+        // a box height for every half of a tile that can occur (a tile has at most M rows)
+        if (rows[i])
+            for (int h = 0; h < kMaxN / 32 && h * 32 < a.M; ++h) rows_map(&p.b[i][h], rows[i], K, (h + 1) * 16);
+        // K-major weights in boxes of the rows that a CTA takes of one matrix, MN-major in 64 x 64
+        if (weights[i])
+            ok = ok && encode_3d(&p.a[i], true, weights[i], d, I, (uint64_t)a.N, 64, a.form == kFormDh ? 128 : 64) == MOE_OK;
+        if (in[i]) rows_map(&p.in[i], in[i], cols, kPanel);
+    }
+    for (int i = 0; i < 3; ++i) {
+        p.out[i] = static_cast<__nv_bfloat16*>(outs[i]);
+        if (outs[i]) rows_map(&p.o[i], outs[i], cols, kPanel);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    const int64_t col_tiles = ((int64_t)cols + pair_channels - 1) / pair_channels;
+    const int64_t units = ((int64_t)a.M / kMaxN + (a.N < a.M ? a.N : a.M)) * col_tiles;
+    switch (a.form) {
+        case kFormUp: return launch_form<kFormUp>(p, units, a.sms, st);
+        case kFormDown: return launch_form<kFormDown>(p, units, a.sms, st);
+        case kFormDh: return launch_form<kFormDh>(p, units, a.sms, st);
+        case kFormDx: return launch_form<kFormDx>(p, units, a.sms, st);
+        case kFormDw: break;
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace moe
