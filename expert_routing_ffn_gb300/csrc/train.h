@@ -103,16 +103,16 @@ cudaError_t launch_grouped_simt(const GroupedArgs& a, cudaStream_t st);
 // tensor cores: the forms that give rows (one launch), and Dw (two)
 cudaError_t launch_grouped_rows_tc(const GroupedArgs& a, cudaStream_t st);
 cudaError_t launch_grouped_dw_tc(const GroupedArgs& a, cudaStream_t st);
-// CTA pairs of a kernel that can be resident at once, at most sms / 2
-cudaError_t resident_pairs(const void* kernel, int threads, uint32_t smem, int sms, int* pairs);
+// clusters of `size` CTAs of a kernel that can be resident at once
+cudaError_t resident_clusters(const void* kernel, int size, int threads, uint32_t smem, int sms, int* clusters);
 
-// A persistent launch of `units` CTAs, or CTA pairs (clusters of two), behind
-// the previous kernel of the stream.
+// A persistent launch of `units` clusters of `size` CTAs behind the previous
+// kernel of the stream.
 template <typename P>
-inline cudaError_t launch_units(void (*kern)(P), const std::remove_const_t<P>& p, int units, bool pair, int threads,
+inline cudaError_t launch_units(void (*kern)(P), const std::remove_const_t<P>& p, int units, int size, int threads,
                                 uint32_t smem, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units < 1 ? 1 : units) * (pair ? 2 : 1));
+    cfg.gridDim = dim3((unsigned)(units < 1 ? 1 : units) * (unsigned)size);
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -120,11 +120,11 @@ inline cudaError_t launch_units(void (*kern)(P), const std::remove_const_t<P>& p
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.x = (unsigned)size;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pair ? 2 : 1;
+    cfg.numAttrs = size > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 

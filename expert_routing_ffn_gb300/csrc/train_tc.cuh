@@ -19,7 +19,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 __device__ __forceinline__ uint32_t leader_address(const void* bar) {
     uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(bar)), "r"(cluster_rank() & ~1u));
     return a;
 }
 __device__ __forceinline__ void cluster_sync() {
@@ -38,14 +38,18 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
     return ok != 0;
 }
 
-// Bounded wait; PAIR: cluster-scope acquire (the peer CTA signals the barrier).
 template <bool PAIR>
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, DevError* err,
-                                     int where, bool honor_abort = true) {
-    if constexpr (!PAIR) return tc_wait(bar, parity, abort_flag, err, where, honor_abort);
+__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
+    return PAIR ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+}
+// The rest of a wait whose first try failed: gives up when another role has
+// aborted (honor_abort) or after the clock budget (records MOE_ERR_TIMEOUT).
+template <bool PAIR>
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, DevError* err,
+                                       int where, bool honor_abort) {
     const long long t0 = clock64();
     for (uint32_t i = 0;; ++i) {
-        if (try_wait_cluster(bar, parity)) return true;
+        if (try_wait<PAIR>(bar, parity)) return true;
         if ((i & 63) == 63) {
             if (honor_abort && *abort_flag) return false;
             if (clock64() - t0 > kTcWaitCycles) {
@@ -55,6 +59,15 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
             }
         }
     }
+}
+// Bounded wait; PAIR: cluster-scope acquire (another CTA signals the barrier).
+// The thread that issues the MMAs waits once per 64 values of K, some 400
+// cycles of MMAs: the common case is one instruction and a branch.
+template <bool PAIR>
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, DevError* err,
+                                     int where, bool honor_abort = true) {
+    if (try_wait<PAIR>(bar, parity)) return true;
+    return wait_slow<PAIR>(bar, parity, abort_flag, err, where, honor_abort);
 }
 
 // ---------------------------------------------------------------- loads, stores
@@ -84,6 +97,15 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const void* map, int c0, i
             " [%0], [%1, {%2, %3, %4}], [%5];"
             ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
 }
+// A pair's CTA loads a tile into the same place of every CTA in `mask`; each
+// of them signals its own pair's leader.
+__device__ __forceinline__ void load_2d_multicast(uint32_t dst, const void* map, int c0, int c1, uint32_t bar,
+                                                  uint16_t mask) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;"
+        ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar), "h"(mask) : "memory");
+}
 __device__ __forceinline__ void store_2d(const void* map, int c0, int c1, uint32_t src) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
                  ::"l"(map), "r"(c0), "r"(c1), "r"(src) : "memory");
@@ -108,6 +130,10 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
 }
 
 // ---------------------------------------------------------------- MMA
+// A shared-memory matrix descriptor advanced by `bytes` (a multiple of 16):
+// the address field is its low 14 bits, and no operand crosses 256 KB.
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
+
 template <bool PAIR>
 __device__ __forceinline__ void mma(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
     if constexpr (PAIR)
@@ -125,6 +151,12 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
             ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
     else tc_commit(bar);
+}
+// arrive on `bar` of the cluster's CTAs in `mask`
+__device__ __forceinline__ void commit_mask(uint64_t* bar, uint16_t mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(smem_u32(bar)), "h"(mask) : "memory");
 }
 // the same, on this CTA's barrier alone
 template <bool PAIR>

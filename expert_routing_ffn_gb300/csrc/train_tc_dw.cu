@@ -3,23 +3,26 @@
 // [M, d]: x, or dy), one or two a in a launch.  tcgen05, accumulators in
 // tensor memory, fed by TMA.
 //
-// A tile is 128 channels x 256 columns of one dW, or 256 x 256 on a CTA pair
-// with the 2-CTA MMA where each CTA stages half of either operand.  The rows
-// are the K axis, so both operands are MN-major as they lie in memory.  They
+// The channels of all a form strips of 128; a tile is two strips x 256 columns
+// on a CTA pair (2-CTA MMA), a strip each, where each CTA stages its strip and
+// half of the columns.  (Two strips of different a share a tile at the seam:
+// I = 1408 is 11 strips, and dWg and dWu together 11 tiles.)  The rows are the
+// K axis, so both operands are MN-major as they lie in memory.  They
 // are summed, so a step that ran past the segment would add the next expert's
 // rows: each expert has tensor maps of its own whose row count ends with its
 // segment (map kernel), and TMA fills the rest of the last step with zeros.
 // Every dW is written once, those of experts without rows as zeros, so at the
 // sizes of a training step (a few hundred rows an expert) the store of dW
-// costs as much as the MMAs: the epilogue has four 4 KB boxes a warp, so that
-// its stores queue up instead of waiting for one another.
+// costs as much as the MMAs: eight epilogue warps, two to a quarter of the
+// accumulator's lanes, with two 4 KB boxes each, so that stores queue up
+// instead of waiting for one another.
 //
-// Tiles are taken round robin by the resident CTAs (pairs), experts with most
-// rows first, so that the units end together when the load is skewed.
+// Tiles are taken round robin by the resident pairs, experts with most rows
+// first, so that the pairs end together when the load is skewed.
 //
-// Block: warp 0 issues the TMA loads, warp 1 the MMAs (one thread), warps 2-5
-// drain the accumulators (a thread owns a channel), double-buffered.  Every
-// wait is bounded.
+// Block: warp 0 issues the TMA loads, warp 1 the MMAs (one thread of the
+// pair's leader), warps 2-9 drain the accumulators (a thread owns a channel),
+// double-buffered.  Every wait is bounded.
 #include <cuda.h>
 
 #include <cstring>
@@ -36,24 +39,17 @@ namespace {
 
 using namespace train;
 
-constexpr int kBM = 128, kBN = 256, kThreads = 192;
-constexpr int kBoxesPerWarp = 4;
+constexpr int kStrip = 128, kBN = 256, kEpiWarps = 8, kThreads = 64 + 32 * kEpiWarps;
+constexpr int kBoxesPerWarp = 2;
 constexpr uint32_t kBK = kTcBK;
-constexpr uint32_t kStageA = kBM * kBK * 2;  // 16 KB
+constexpr uint32_t kStageA = kStrip * kBK * 2, kStageB = kBN / 2 * kBK * 2, kStage = kStageA + kStageB;
 constexpr uint32_t kBox = 32 * 128;          // 32 channels x 128 bytes
 constexpr int kMapsPerExpert = 3;            // a0, a1, b
-
-template <bool PAIR>
-struct Cfg {
-    static constexpr int kStages = PAIR ? 5 : 3;
-    static constexpr uint32_t kStageB = (PAIR ? kBN / 2 : kBN) * kBK * 2;
-    static constexpr uint32_t kStage = kStageA + kStageB;
-    static constexpr uint32_t kBoxes = kStages * kStage;
-    static constexpr uint32_t kTable = kBoxes + 4 * kBoxesPerWarp * kBox;  // experts by rows, packed with their row counts
-    static constexpr uint32_t kBars = kTable + (kTrainMaxExperts * 4 + 15) / 16 * 16;
-    static constexpr uint32_t kSmem = kBars + (2 * kStages + 5) * 8 + 16;
-    static_assert(kSmem <= 232448, "227 KB of shared memory per block");
-};
+constexpr int kS = 5;                        // stages
+constexpr uint32_t kBoxes = kS * kStage, kTable = kBoxes + kEpiWarps * kBoxesPerWarp * kBox;  // table: rank -> expert
+constexpr uint32_t kBars = kTable + kTrainMaxExperts * 4;
+constexpr uint32_t kSmem = kBars + (2 * kS + 5) * 8 + 16;
+static_assert(kSmem <= 232448, "227 KB of shared memory per block");
 
 struct DwParams {
     CUtensorMap o[2];
@@ -64,17 +60,14 @@ struct DwParams {
 };
 
 struct Tile {
-    int e, rows, m0, n0, mat;
+    int e, rows, strip, n0;  // expert, its rows, the pair's first strip, first column
 };
 
-template <bool PAIR, bool F32>
+template <bool F32>
 __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_constant__ DwParams p) {
-    using C = Cfg<PAIR>;
-    constexpr int kS = C::kStages;
-    constexpr int kRows = PAIR ? 2 * kBM : kBM;
     extern __shared__ __align__(1024) unsigned char smem[];
-    int* order = reinterpret_cast<int*>(smem + C::kTable);  // rank -> expert
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBars);
+    int* order = reinterpret_cast<int*>(smem + kTable);  // rank -> expert
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBars);
     uint64_t *empty = full + kS, *tfull = empty + kS, *tempty = tfull + 2, *drain = tempty + 2;
     uint32_t* tmem_s = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_s + 1);
@@ -82,11 +75,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
     grid_dep_wait();  // the previous kernels' outputs; no tensor memory is taken before it
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = smem_u32(smem);
-    const uint32_t rank = PAIR ? cluster_rank() : 0;
+    const uint32_t rank = cluster_rank();
     const bool leader = rank == 0;
-    const int unit = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
-    const int n_units = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
-    const int row_off = (int)rank * kBM;
+    const int unit = (int)(blockIdx.x >> 1), n_units = (int)(gridDim.x >> 1);
 
     auto rows_of = [&](int e) {
         const int r0 = min(max(p.offsets[e], 0), p.M);
@@ -113,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], PAIR ? 8 : 4);  // an arrival per epilogue warp (of both CTAs)
+            mbar_init(&tempty[b], 2 * kEpiWarps);  // an arrival per epilogue warp of both CTAs
         }
         mbar_init(drain, 1);
         fence_mbar_init();
@@ -123,28 +114,31 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
             *abort_flag = 1;
         }
     }
-    if (warp == 1) tmem_alloc<PAIR>(tmem_s);
+    if (warp == 1) tmem_alloc<true>(tmem_s);
     fence_proxy_async();  // the row counts' shared memory becomes a stage that TMA writes
     tc_fence_before();
     __syncthreads();
-    if constexpr (PAIR) cluster_sync();  // the peer's barriers are ready before any arrival from here
+    cluster_sync();  // the peer's barriers are ready before any arrival from here
     tc_fence_after();
     const uint32_t tmem = *tmem_s;
-    const int mts = (p.I + kRows - 1) / kRows, nts = (p.d + kBN - 1) / kBN;
-    const int per = mts * nts * p.n_mat, n_tiles = per * p.N;
-    // channel tiles innermost: a column tile of b is read by consecutive units
+    const int strips = (p.I + kStrip - 1) / kStrip;  // of one a
+    const int mts = (strips * p.n_mat + 1) / 2, per = mts * ((p.d + kBN - 1) / kBN), n_tiles = per * p.N;
+    // strips innermost: a column tile of b is read by consecutive pairs
     auto decode = [&](int t) {
         Tile x;
-        const int place = t / per;
-        int local = t - place * per;
+        const int place = t / per, local = t - place * per;
         x.e = order[place];
         x.rows = rows_of(x.e);
-        x.mat = local / (mts * nts);
-        local -= x.mat * mts * nts;
         x.n0 = local / mts;
-        x.m0 = (local - x.n0 * mts) * kRows;
+        x.strip = (local - x.n0 * mts) * 2;
         x.n0 *= kBN;
         return x;
+    };
+    // this CTA's strip of a tile: which a, and its first channel (past I: no such strip)
+    auto strip_of = [&](const Tile& x, int& mat, int& m0) {
+        const int q = x.strip + (int)rank;
+        mat = q >= strips && p.n_mat > 1;
+        m0 = (q - (mat ? strips : 0)) * kStrip;
     };
 
     if (warp == 0) {
@@ -158,65 +152,67 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
                     for (int m = 0; m < kMapsPerExpert; ++m) map_acquire(emaps + m * 128);
                     last_e = x.e;
                 }
+                int mat, m0;
+                strip_of(x, mat, m0);
                 for (int k0 = 0; k0 < x.rows; k0 += (int)kBK, ++it) {
                     const int st = it % kS;
-                    if (!wait<PAIR>(&empty[st], ((it / kS) & 1) ^ 1, abort_flag, p.err, 1)) break;
-                    const uint32_t ad = base + st * C::kStage, bd = ad + kStageA;
-                    const uint32_t bar = PAIR ? leader_address(&full[st]) : smem_u32(&full[st]);
-                    if (leader) mbar_arrive_expect_tx(&full[st], (PAIR ? 2 : 1) * C::kStage);
+                    if (!wait<true>(&empty[st], ((it / kS) & 1) ^ 1, abort_flag, p.err, 1)) break;
+                    const uint32_t ad = base + st * kStage, bd = ad + kStageA;
+                    const uint32_t bar = leader_address(&full[st]);
+                    if (leader) mbar_arrive_expect_tx(&full[st], 2 * kStage);
 #pragma unroll
-                    for (int j = 0; j < kBM / 64; ++j)
-                        load_2d<PAIR>(ad + j * 8192, emaps + x.mat * 128, x.m0 + row_off + j * 64, k0, bar);
+                    for (int j = 0; j < 2; ++j) load_2d<true>(ad + j * 8192, emaps + mat * 128, m0 + j * 64, k0, bar);
 #pragma unroll
-                    for (int j = 0; j < (PAIR ? 2 : 4); ++j)
-                        load_2d<PAIR>(bd + j * 8192, emaps + 2 * 128, x.n0 + (int)rank * 128 + j * 64, k0, bar);
+                    for (int j = 0; j < 2; ++j)
+                        load_2d<true>(bd + j * 8192, emaps + 2 * 128, x.n0 + (int)rank * 128 + j * 64, k0, bar);
                 }
             }
-            // the last stages' loads have landed (a pair: and were consumed by the
-            // leader's MMAs) before the block may leave
-            for (int k = it > kS ? it - kS : 0; k < it; ++k) {
-                if constexpr (PAIR) (void)wait<true>(&empty[k % kS], (k / kS) & 1, abort_flag, p.err, 2, false);
-                else (void)wait<false>(&full[k % kS], (k / kS) & 1, abort_flag, p.err, 2, false);
-            }
+            // the leader's MMAs have consumed this CTA's last stages before it may leave
+            for (int k = it > kS ? it - kS : 0; k < it; ++k)
+                (void)wait<true>(&empty[k % kS], (k / kS) & 1, abort_flag, p.err, 2, false);
         }
     } else if (warp == 1) {
         // ---------------- MMAs (the leader of a pair)
         if (lane == 0 && leader) {
-            constexpr uint32_t idesc = tc_idesc(PAIR ? 2 * kBM : kBM, kBN, 1, 1);
-            int it = 0, local = 0;
+            constexpr uint32_t idesc = tc_idesc(2 * kStrip, kBN, 1, 1);
+            // 16 rows of 128 bytes a step, the next 64 channels or columns 8 KB on
+            const uint64_t da0 = smem_desc(base, 8192, 1024), db0 = smem_desc(base + kStageA, 8192, 1024);
+            int st = 0, local = 0;
+            uint32_t phase = 0;
             for (int t = unit; t < n_tiles; t += n_units, ++local) {
                 if (*abort_flag) break;
                 const int rows = decode(t).rows;
                 const int ab = local & 1;
-                if (!wait<PAIR>(&tempty[ab], ((local >> 1) & 1) ^ 1, abort_flag, p.err, 3)) break;
+                const uint32_t acc = tmem + ab * kBN;
+                if (!wait<true>(&tempty[ab], ((local >> 1) & 1) ^ 1, abort_flag, p.err, 3)) break;
                 tc_fence_after();
                 bool ok = true;
-                for (int k0 = 0; k0 < rows; k0 += (int)kBK, ++it) {
-                    const int st = it % kS;
-                    if (!wait<PAIR>(&full[st], (it / kS) & 1, abort_flag, p.err, 4)) { ok = false; break; }
+                for (int k0 = 0; k0 < rows; k0 += (int)kBK) {
+                    if (!wait<true>(&full[st], phase, abort_flag, p.err, 4)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t ad = base + st * C::kStage, bd = ad + kStageA;
-                    // 16 rows of 128 bytes a step, the next 64 channels or columns 8 KB on;
+                    const uint64_t da = desc_at(da0, st * kStage), db = desc_at(db0, st * kStage);
                     // 16-row steps without a row of the segment are left out
-                    const int steps = min((int)kBK / 16, (rows - k0 + 15) / 16);
-                    for (int kk = 0; kk < steps; ++kk)
-                        mma<PAIR>(tmem + ab * kBN, smem_desc(ad + kk * 2048, 8192, 1024), smem_desc(bd + kk * 2048, 8192, 1024),
-                                  idesc, (k0 | kk) ? 1u : 0u);
-                    commit<PAIR>(&empty[st]);
+#pragma unroll
+                    for (int kk = 0; kk < (int)kBK / 16; ++kk)
+                        if (kk == 0 || k0 + kk * 16 < rows)
+                            mma<true>(acc, desc_at(da, kk * 2048), desc_at(db, kk * 2048), idesc, (k0 | kk) ? 1u : 0u);
+                    commit<true>(&empty[st]);
+                    if (++st == kS) { st = 0; phase ^= 1; }
                 }
                 if (!ok) break;
-                commit<PAIR>(&tfull[ab]);
+                commit<true>(&tfull[ab]);
             }
             // every MMA issued here is done before tensor memory is released
-            commit_local<PAIR>(drain);
-            (void)wait<PAIR>(drain, 0, abort_flag, p.err, 6, false);
+            commit_local<true>(drain);
+            (void)wait<true>(drain, 0, abort_flag, p.err, 6, false);
         }
     } else {
-        // ---------------- epilogue: warps 2..5, a thread owns a channel of dW
-        const int quarter = warp & 3;
-        const uint32_t boxes = base + C::kBoxes + quarter * kBoxesPerWarp * kBox;
+        // ---------------- epilogue: a thread owns a channel of dW, two warps share a quarter of
+        // the lanes and take every other box of columns
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t boxes = base + kBoxes + (warp - 2) * kBoxesPerWarp * kBox;
         const uint32_t sw = lane & 7;  // 128-byte swizzle: chunk j of row i at chunk j ^ (i & 7)
-        const uint32_t free0 = PAIR ? leader_address(&tempty[0]) : 0, free1 = PAIR ? leader_address(&tempty[1]) : 0;
+        const uint32_t free0 = leader_address(&tempty[0]), free1 = leader_address(&tempty[1]);
         int local = 0, pn = 0;
         constexpr int kW = F32 ? 32 : 64;  // columns of a box
         for (int t = unit; t < n_tiles; t += n_units, ++local) {
@@ -224,14 +220,16 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
             const Tile x = decode(t);
             const int ab = local & 1;
             bool ok = true;
-            if (lane == 0) ok = wait<PAIR>(&tfull[ab], (local >> 1) & 1, abort_flag, p.err, 5);
+            if (lane == 0) ok = wait<true>(&tfull[ab], (local >> 1) & 1, abort_flag, p.err, 5);
             if (!__shfl_sync(0xffffffffu, ok, 0)) break;
             tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + ab * kBN;
-            const int m = x.m0 + row_off + quarter * 32;  // this warp's first channel
+            int mat, m;
+            strip_of(x, mat, m);
+            m += quarter * 32;  // this warp's first channel
             if (m < p.I && !(p.accumulate && x.rows == 0)) {
 #pragma unroll 1
-                for (int c = 0; c < kBN && x.n0 + c < p.d; c += kW, ++pn) {
+                for (int c = half * kW; c < kBN && x.n0 + c < p.d; c += 2 * kW, ++pn) {
                     const uint32_t box = boxes + (pn % kBoxesPerWarp) * kBox;
                     if (lane == 0) stores_read<kBoxesPerWarp - 1>();  // the store that last used this box
                     __syncwarp();
@@ -256,8 +254,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
                     fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) {
-                        if (F32 && p.accumulate) add_3d(&p.o[x.mat], x.n0 + c, m, x.e, box);
-                        else store_3d(&p.o[x.mat], x.n0 + c, m, x.e, box);
+                        if (F32 && p.accumulate) add_3d(&p.o[mat], x.n0 + c, m, x.e, box);
+                        else store_3d(&p.o[mat], x.n0 + c, m, x.e, box);
                         stores_commit();
                     }
                 }
@@ -265,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (PAIR && !leader) arrive_cluster(ab ? free1 : free0);
+                if (!leader) arrive_cluster(ab ? free1 : free0);
                 else mbar_arrive(&tempty[ab]);
             }
         }
@@ -279,9 +277,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
     __syncthreads();
     // the leader's MMAs, which read the peer's shared memory and write its
     // tensor memory, are done before either CTA frees or leaves
-    if constexpr (PAIR) cluster_sync();
+    cluster_sync();
     tc_fence_after();
-    if (warp == 1) tmem_free<PAIR>(tmem);
+    if (warp == 1) tmem_free<true>(tmem);
     grid_dep_launch();
 }
 
@@ -317,20 +315,20 @@ __global__ void __launch_bounds__(128) expert_maps_kernel(const __grid_constant_
     grid_dep_launch();
 }
 
-template <bool PAIR, bool F32>
-cudaError_t launch_dw(const DwParams& p, int64_t units, int sms, cudaStream_t st) {
-    auto kern = grouped_dw_kernel<PAIR, F32>;
+template <bool F32>
+cudaError_t launch_dw(const DwParams& p, int sms, cudaStream_t st) {
+    auto kern = grouped_dw_kernel<F32>;
     cudaError_t e = allow_max_smem(kern);
     if (e != cudaSuccess) return e;
-    int most = sms;
-    if constexpr (PAIR) {
-        e = resident_pairs(reinterpret_cast<const void*>(kern), kThreads, Cfg<true>::kSmem, sms, &most);
-        if (e != cudaSuccess) return e;
-        if (most <= 0) return cudaErrorInvalidConfiguration;
-    }
+    int most = 0;
+    e = resident_clusters(reinterpret_cast<const void*>(kern), 2, kThreads, kSmem, sms, &most);
+    if (e != cudaSuccess) return e;
+    if (most <= 0) return cudaErrorInvalidConfiguration;
+    const int64_t strips = (p.I + kStrip - 1) / kStrip;
+    int64_t units = p.N * ((strips * p.n_mat + 1) / 2) * ((p.d + kBN - 1) / kBN);
     if (units > most) units = most;
-    return note_launch(reinterpret_cast<const void*>(kern), kThreads, Cfg<PAIR>::kSmem,
-                       launch_units(kern, p, (int)units, PAIR, kThreads, Cfg<PAIR>::kSmem, st));
+    return note_launch(reinterpret_cast<const void*>(kern), kThreads, kSmem,
+                       launch_units(kern, p, (int)units, 2, kThreads, kSmem, st));
 }
 
 }  // namespace
@@ -358,12 +356,7 @@ cudaError_t launch_grouped_dw_tc(const GroupedArgs& a, cudaStream_t st) {
             return cudaErrorInvalidValue;
     cudaError_t e = launch_pdl(expert_maps_kernel, dim3((a.N + 3) / 4), dim3(128), 0, st, mp);
     if (e != cudaSuccess) return e;
-    // a pair's 256 channels, unless the expert has less
-    const bool pair = a.I >= 2 * kBM;
-    const int tile_rows = pair ? 2 * kBM : kBM;
-    const int64_t units = (int64_t)a.N * p.n_mat * ((a.I + tile_rows - 1) / tile_rows) * ((a.d + kBN - 1) / kBN);
-    if (pair) return a.out_f32 ? launch_dw<true, true>(p, units, a.sms, st) : launch_dw<true, false>(p, units, a.sms, st);
-    return a.out_f32 ? launch_dw<false, true>(p, units, a.sms, st) : launch_dw<false, false>(p, units, a.sms, st);
+    return a.out_f32 ? launch_dw<true>(p, a.sms, st) : launch_dw<false>(p, a.sms, st);
 }
 
 }  // namespace moe

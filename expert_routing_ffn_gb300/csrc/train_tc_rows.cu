@@ -48,32 +48,37 @@ namespace {
 
 using namespace train;
 
-constexpr int kThreads = 192, kEpiThreads = 128;
-constexpr int kMaxN = 256;     // rows of a tile, at most
+constexpr int kGroups = 2, kGroupThreads = 128;  // epilogue: two groups of four warps
+constexpr int kThreads = 64 + kGroups * kGroupThreads;
 constexpr int kStepN = 32;     // granularity of N on a CTA pair
 constexpr int kPanel = 32;     // rows per epilogue panel
+constexpr int kBuffers = 2;    // panel buffers of each group
 constexpr uint32_t kBK = kTcBK;
-constexpr uint32_t kStageA = 128 * kBK * 2, kStageB = kMaxN / 2 * kBK * 2, kStage = kStageA + kStageB;
+constexpr uint32_t kStageA = 128 * kBK * 2;
 constexpr uint32_t kBox = kPanel * 128;  // 32 rows x 64 channels
+constexpr int kBoxHeights = 8;
 
-template <int FORM>
+// MAXN: the most rows of a tile.
+template <int FORM, int MAXN>
 struct Cfg {
     static constexpr bool kNT = FORM == kFormUp || FORM == kFormDh;  // weights K-major
     static constexpr int kChannels = FORM == kFormUp ? 64 : 128;     // output channels of one CTA
     static constexpr int kBoxes = FORM == kFormUp ? 3 : FORM == kFormDh ? 4 : 2;  // boxes of a panel
-    static constexpr int kBuffers = 3;
-    static constexpr int kStages = FORM == kFormDh || FORM == kFormUp ? 5 : 6;
-    static constexpr uint32_t kPanels = kStages * kStage;  // epilogue buffers
-    static constexpr uint32_t kSwap = kPanels + kBuffers * kBoxes * kBox;  // Up: 2 x 64 bytes a thread
-    static constexpr uint32_t kTables = kSwap + (FORM == kFormUp ? 2 * kEpiThreads * 64 : 0);
-    static constexpr uint32_t kBars = kTables + 2 * ((kTrainMaxExperts + 1) * 4 + 15) / 16 * 16;
-    static constexpr uint32_t kSmem = kBars + (2 * kStages + 5 + kBuffers) * 8 + 16;
+    static constexpr uint32_t kStage = kStageA + MAXN / 2 * kBK * 2;
+    static constexpr uint32_t kBuffer = kBoxes * kBox;
+    static constexpr uint32_t kSwap = FORM == kFormUp ? kGroupThreads * 64 : 0;  // a group's room to swap values
+    static constexpr uint32_t kEpi = kGroups * (kBuffers * kBuffer + kSwap);
+    static constexpr int kStages = (int)((224 * 1024 - kEpi) / kStage);
+    static constexpr uint32_t kPanels = (kStages * kStage + 1023) / 1024 * 1024;  // epilogue buffers
+    static constexpr uint32_t kTable = kPanels + kEpi;
+    static constexpr uint32_t kBars = kTable + ((kTrainMaxExperts + 1) * 4 + 15) / 16 * 16;
+    static constexpr uint32_t kSmem = kBars + (2 * kStages + 5 + kGroups * kBuffers) * 8 + 16;
     static_assert(kSmem <= 232448, "227 KB of shared memory per block");
 };
 
 struct RowsParams {
     CUtensorMap a[2];         // weights
-    CUtensorMap b[2][kMaxN / 32];  // rows [M, K] in boxes of 16, 32, .. 128 rows
+    CUtensorMap b[2][kBoxHeights];  // rows [M, K] in boxes of 16, 32, .. 128 rows
     CUtensorMap in[2];        // Dh: g, u
     CUtensorMap o[3];         // outputs (boxes of 32 rows x 64 channels)
     __nv_bfloat16* out[3];
@@ -92,43 +97,68 @@ __device__ __forceinline__ uint32_t pack_f(uint32_t lo, uint32_t hi) {
 }
 
 struct Tile {
-    int e, row0, rows, c0;  // expert, first row, rows of the tile (1..256), first channel of the pair
+    int e, row0, rows, c0;  // expert, first row, rows of the tile, first channel of the pair
 };
-__device__ __forceinline__ int row_tiles(int rows) { return (rows + kMaxN - 1) / kMaxN; }
-// rows of a tile when `rows` are split into equal tiles: a multiple of 32
-__device__ __forceinline__ int tile_rows(int rows) {
-    const int n = row_tiles(rows);
-    return ((rows + n - 1) / n + kStepN - 1) / kStepN * kStepN;
+
+// The rows of a segment are cut into units of 32 (the last one ragged), the
+// units into as few tiles of at most MAXN rows as possible, of sizes that
+// differ by one unit at most.
+template <int MAXN>
+__device__ __forceinline__ int row_tiles(int rows) { return (rows + MAXN - 1) / MAXN; }
+
+// Where the units' whole rounds end, the tiles left over are fewer than the
+// units: each is cut into `cut` parts of its rows, so that the last round is
+// as short as it can be with one part a unit (its weights come from L2 then).
+struct Schedule {
+    int whole, cut, total;  // tiles of whole rounds, parts of a later tile, list entries
+};
+__device__ __forceinline__ Schedule schedule(int n_tiles, int n_units) {
+    Schedule s;
+    const int left = n_tiles % n_units;
+    s.whole = n_tiles - left;
+    s.cut = left > 0 ? n_units / left : 1;
+    if (s.cut > 8) s.cut = 8;
+    s.total = s.whole + left * s.cut;
+    return s;
 }
 
-template <int FORM>
-__device__ __forceinline__ Tile decode(int N, const int* first, const int* row_s, int t) {
-    int lo = 0, hi = N;
+// List entry t; rows = 0 for a part that its tile is too short for.
+template <int FORM, int MAXN>
+__device__ __forceinline__ Tile decode(const RowsParams& p, const int* first, const Schedule& sc, int t) {
+    int part = 0, cut = 1;
+    if (t >= sc.whole) {
+        cut = sc.cut;
+        part = (t - sc.whole) % cut;
+        t = sc.whole + (t - sc.whole) / cut;
+    }
+    int lo = 0, hi = p.N;
     while (hi - lo > 1) {  // the last expert whose tiles start at or before t
         const int mid = (lo + hi) >> 1;
         if (first[mid] <= t) lo = mid;
         else hi = mid;
     }
-    const int r0 = row_s[lo], rows = row_s[lo + 1] - r0, mts = row_tiles(rows), per = tile_rows(rows);
-    const int local = t - first[lo], m = local % mts;
+    const int r0 = min(max(p.offsets[lo], 0), p.M), rows = min(max(p.offsets[lo + 1], 0), p.M) - r0;
+    const int mts = row_tiles<MAXN>(rows), units = (rows + kStepN - 1) / kStepN;
+    const int local = t - first[lo], c = local / mts, m = local - c * mts;
+    const int u0 = m * units / mts, nu = (m + 1) * units / mts - u0;  // this tile's units
+    const int a = u0 + part * nu / cut, b = u0 + (part + 1) * nu / cut;
     Tile x;
     x.e = lo;
-    x.row0 = r0 + m * per;
-    x.rows = min(per, rows - m * per);
-    x.c0 = local / mts * 2 * Cfg<FORM>::kChannels;
+    x.row0 = r0 + a * kStepN;
+    x.rows = min(b * kStepN, rows) - a * kStepN;
+    x.c0 = c * 2 * Cfg<FORM, MAXN>::kChannels;
     return x;
 }
 
-template <int FORM>
+template <int FORM, int MAXN>
 __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_constant__ RowsParams p) {
-    using C = Cfg<FORM>;
-    constexpr int kS = C::kStages, kNB = C::kBuffers;
+    using C = Cfg<FORM, MAXN>;
+    constexpr int kS = C::kStages;
     extern __shared__ __align__(1024) unsigned char smem[];
-    int* first = reinterpret_cast<int*>(smem + C::kTables);
-    int* row_s = first + kTrainMaxExperts + 1;
+    int* first = reinterpret_cast<int*>(smem + C::kTable);  // tiles before each expert
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBars);
     uint64_t *empty = full + kS, *tfull = empty + kS, *tempty = tfull + 2, *drain = tempty + 2, *pfull = drain + 1;
-    uint32_t* tmem_s = reinterpret_cast<uint32_t*>(pfull + kNB);
+    uint32_t* tmem_s = reinterpret_cast<uint32_t*>(pfull + kGroups * kBuffers);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_s + 1);
 
     grid_dep_wait();  // the previous kernels' outputs; no tensor memory is taken before it
@@ -141,8 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
     const int K = C::kNT ? p.d : p.I;
     const int nk1 = (K + (int)kBK - 1) / (int)kBK, nk = FORM == kFormDx ? 2 * nk1 : nk1;
 
-    // rows before each expert (never beyond M, never backwards), tiles before each expert
-    for (int e = tid; e <= p.N; e += kThreads) row_s[e] = min(max(p.offsets[e], 0), p.M);
+    auto row_at = [&](int e) { return min(max(p.offsets[e], 0), p.M); };
     if (tid == 32) {
         for (int s = 0; s < kS; ++s) {
             mbar_init(&full[s], 1);
@@ -150,10 +179,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], 8);  // an arrival per epilogue warp of both CTAs
+            mbar_init(&tempty[b], 2 * kGroups * 4);  // an arrival per epilogue warp of both CTAs
         }
         mbar_init(drain, 1);
-        for (int b = 0; b < kNB; ++b) mbar_init(&pfull[b], 1);
+        for (int b = 0; b < kGroups * kBuffers; ++b) mbar_init(&pfull[b], 1);
         fence_mbar_init();
         *abort_flag = 0;
         if (base & 1023u) {  // the swizzled tiles need it
@@ -161,13 +190,12 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
             *abort_flag = 1;
         }
     }
-    __syncthreads();
     if (warp == 0) {
         const int cts = (n_cols + 2 * C::kChannels - 1) / (2 * C::kChannels);
         int carry = 0;
         for (int b = 0; b < p.N; b += 32) {
             const int e = b + lane;
-            const int v = e < p.N ? row_tiles(max(row_s[e + 1] - row_s[e], 0)) * cts : 0;
+            const int v = e < p.N ? row_tiles<MAXN>(max(row_at(e + 1) - row_at(e), 0)) * cts : 0;
             int inc = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -181,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
     }
     if (warp == 1) tmem_alloc<true>(tmem_s);
     {  // rows of no expert
-        const int64_t v0 = (int64_t)row_s[p.N] * n_cols / 8, v1 = (int64_t)p.M * n_cols / 8;
+        const int64_t v0 = (int64_t)row_at(p.N) * n_cols / 8, v1 = (int64_t)p.M * n_cols / 8;
         for (int64_t v = v0 + (int64_t)blockIdx.x * kThreads + tid; v < v1; v += (int64_t)gridDim.x * kThreads)
             for (int o = 0; o < 3; ++o)
                 if (p.out[o]) reinterpret_cast<uint4*>(p.out[o])[v] = make_uint4(0, 0, 0, 0);
@@ -191,21 +219,22 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
     cluster_sync();  // the peer's barriers are ready before any arrival from here
     tc_fence_after();
     const uint32_t tmem = *tmem_s;
-    const int n_tiles = first[p.N];
+    const Schedule sc = schedule(first[p.N], n_units);
 
     if (warp == 0) {
         // ---------------- loads (each CTA its own stages, on the leader's barrier)
         if (lane == 0) {
             int it = 0;
-            for (int t = unit; t < n_tiles && !*abort_flag; t += n_units) {
-                const Tile x = decode<FORM>(p.N, first, row_s, t);
+            for (int t = unit; t < sc.total && !*abort_flag; t += n_units) {
+                const Tile x = decode<FORM, MAXN>(p, first, sc, t);
+                if (x.rows <= 0) continue;
                 const int half = (x.rows + kStepN - 1) / kStepN * kStepN / 2;  // rows staged by each CTA
                 const int brow = x.row0 + (int)rank * half;
                 const int ch = x.c0 + (int)rank * C::kChannels;
                 for (int kb = 0; kb < nk; ++kb, ++it) {
                     const int st = it % kS;
                     if (!wait<true>(&empty[st], ((it / kS) & 1) ^ 1, abort_flag, p.err, 1)) break;
-                    const uint32_t ad = base + st * kStage, bd = ad + kStageA;
+                    const uint32_t ad = base + st * C::kStage, bd = ad + kStageA;
                     const uint32_t bar = leader_address(&full[st]);
                     if (leader) mbar_arrive_expect_tx(&full[st], 2 * (kStageA + (uint32_t)half * 128));
                     const int part = FORM == kFormDx && kb >= nk1;
@@ -229,41 +258,49 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
     } else if (warp == 1) {
         // ---------------- MMAs (the pair's leader)
         if (lane == 0 && leader) {
-            int it = 0, local = 0;
-            for (int t = unit; t < n_tiles; t += n_units, ++local) {
+            // K-major: 16 values = 32 bytes along the swizzled row; MN-major: 16 rows of 128 bytes,
+            // the next 64 channels 8 KB on
+            const uint64_t da0 = C::kNT ? smem_desc(base, 16, 1024) : smem_desc(base, 8192, 1024);
+            const uint64_t db0 = smem_desc(base + kStageA, 16, 1024);
+            constexpr uint32_t kStepA = C::kNT ? 32 : 2048, kStepB = 32;
+            int st = 0, local = 0;
+            uint32_t phase = 0;
+            for (int t = unit; t < sc.total; t += n_units) {
                 if (*abort_flag) break;
-                const Tile x = decode<FORM>(p.N, first, row_s, t);
+                const Tile x = decode<FORM, MAXN>(p, first, sc, t);
+                if (x.rows <= 0) continue;
                 const uint32_t idesc = tc_idesc(256, (x.rows + kStepN - 1) / kStepN * kStepN, 0, C::kNT ? 0 : 1);
                 const int ab = local & 1;
+                const uint32_t acc = tmem + ab * 256;
                 if (!wait<true>(&tempty[ab], ((local >> 1) & 1) ^ 1, abort_flag, p.err, 3)) break;
                 tc_fence_after();
                 bool ok = true;
-                for (int kb = 0; kb < nk; ++kb, ++it) {
-                    const int st = it % kS;
-                    if (!wait<true>(&full[st], (it / kS) & 1, abort_flag, p.err, 4)) { ok = false; break; }
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!wait<true>(&full[st], phase, abort_flag, p.err, 4)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t ad = base + st * kStage, bd = ad + kStageA;
+                    const uint64_t da = desc_at(da0, st * C::kStage), db = desc_at(db0, st * C::kStage);
 #pragma unroll
-                    for (int kk = 0; kk < (int)kBK / 16; ++kk) {
-                        // K-major: 16 values = 32 bytes along the swizzled row; MN-major: 16 rows of
-                        // 128 bytes, the next 64 channels 8 KB on
-                        const uint64_t da = C::kNT ? smem_desc(ad + kk * 32, 16, 1024) : smem_desc(ad + kk * 2048, 8192, 1024);
-                        mma<true>(tmem + ab * kMaxN, da, smem_desc(bd + kk * 32, 16, 1024), idesc, (kb | kk) ? 1u : 0u);
-                    }
+                    for (int kk = 0; kk < (int)kBK / 16; ++kk)
+                        mma<true>(acc, desc_at(da, kk * kStepA), desc_at(db, kk * kStepB), idesc, (kb | kk) ? 1u : 0u);
                     commit<true>(&empty[st]);
+                    if (++st == kS) { st = 0; phase ^= 1; }
                 }
                 if (!ok) break;
                 commit<true>(&tfull[ab]);
+                ++local;
             }
             // every MMA issued here is done before tensor memory is released
             commit_local<true>(drain);
             (void)wait<true>(drain, 0, abort_flag, p.err, 6, false);
         }
     } else {
-        // ---------------- epilogue: warps 2..5, warp w on tensor-memory lanes 32 (w % 4) ...
-        const int quarter = warp & 3, etid = tid - 64;
-        const bool boss = etid == 0;  // issues this CTA's output stores (and Dh's input loads)
-        const uint32_t panels = base + C::kPanels;
+        // ---------------- epilogue: warp w on tensor-memory lanes 32 (w % 4) ..; a group of four
+        // warps takes every other panel, with buffers and a barrier of its own
+        const int quarter = warp & 3, group = (warp - 2) >> 2, etid = (tid - 64) & (kGroupThreads - 1);
+        const int bar_id = 1 + group;
+        const bool boss = etid == 0;  // issues the group's output stores (and Dh's input loads)
+        const uint32_t panels = base + C::kPanels + group * kBuffers * C::kBuffer;
+        uint64_t* const in_bar = pfull + group * kBuffers;
         const uint32_t free0 = leader_address(&tempty[0]), free1 = leader_address(&tempty[1]);
         // stmatrix / ldmatrix: lanes 8j .. 8j + 7 address matrix j, a row of 16 bytes each
         const int mj = lane >> 3, mr = lane & 7;
@@ -271,38 +308,40 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
         const int my_box = quarter >> 1, my_chunk = (quarter & 1) * 4;
         int local = 0, pn = 0;
         uint32_t in_phase = 0;  // Dh: parity of each buffer's input barrier
-        // Dh: g and u of 32 rows from q0 on into buffer `buf`
-        auto load_inputs = [&](const Tile& x, int ch, int q0, int buf) {
-            const uint32_t dst = panels + buf * C::kBoxes * kBox, bar = smem_u32(&pfull[buf]);
+        // Dh: g and u of 32 rows from q0 on into buffer `b`
+        auto load_inputs = [&](const Tile& x, int ch, int q0, int b) {
+            const uint32_t dst = panels + b * C::kBuffer, bar = smem_u32(&in_bar[b]);
             const int n_box = ch + 64 < n_cols ? 2 : 1;
-            mbar_arrive_expect_tx(&pfull[buf], 2 * n_box * kBox);
+            mbar_arrive_expect_tx(&in_bar[b], 2 * n_box * kBox);
             for (int j = 0; j < n_box; ++j) {
                 load_2d<false>(dst + j * kBox, &p.in[0], ch + j * 64, x.row0 + q0, bar);
                 load_2d<false>(dst + (2 + j) * kBox, &p.in[1], ch + j * 64, x.row0 + q0, bar);
             }
         };
-        for (int t = unit; t < n_tiles; t += n_units, ++local) {
-            const Tile x = decode<FORM>(p.N, first, row_s, t);
+        for (int t = unit; t < sc.total; t += n_units) {
+            const Tile x = decode<FORM, MAXN>(p, first, sc, t);
+            if (x.rows <= 0) continue;
             const int ch = x.c0 + (int)rank * C::kChannels;
-            const bool any = ch < n_cols;  // this CTA's channels lie in the output
+            const bool any = ch < n_cols && group * kPanel < x.rows;  // this group has a panel of this CTA's channels
             if (FORM == kFormDh && any && boss) {  // the first panel's inputs, beside the tile's MMAs
-                stores_read<kNB - 1>();
-                load_inputs(x, ch, 0, pn % kNB);
+                stores_read<kBuffers - 1>();
+                load_inputs(x, ch, group * kPanel, pn % kBuffers);
             }
             const int ab = local & 1;
             bool ok = true;
             if (lane == 0) ok = wait<true>(&tfull[ab], (local >> 1) & 1, abort_flag, p.err, 5);
             // the four warps share barriers: they leave together
-            const bool stop = bar_any(1, kEpiThreads, !ok || *abort_flag);
+            const bool stop = bar_any(bar_id, kGroupThreads, !ok || *abort_flag);
+            ++local;
             tc_fence_after();
-            const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + ab * kMaxN;
+            const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + ab * 256;
             if (any) {
 #pragma unroll 1
-                for (int q0 = 0; q0 < x.rows; q0 += kPanel, ++pn) {
-                    const uint32_t buf = panels + (pn % kNB) * C::kBoxes * kBox;
-                    if (FORM == kFormDh && boss && q0 + kPanel < x.rows) {
-                        stores_read<1>();
-                        load_inputs(x, ch, q0 + kPanel, (pn + 1) % kNB);
+                for (int q0 = group * kPanel; q0 < x.rows; q0 += kGroups * kPanel, ++pn) {
+                    const uint32_t buf = panels + (pn % kBuffers) * C::kBuffer;
+                    if (FORM == kFormDh && boss && q0 + kGroups * kPanel < x.rows) {
+                        stores_read<0>();  // the last panel's store has left the other buffer
+                        load_inputs(x, ch, q0 + kGroups * kPanel, (pn + 1) % kBuffers);
                     }
                     uint32_t lo[16], hi[16];  // lanes 0-15 and 16-31 of the warp's quarter
                     tmem_ld_16x32(taddr + q0, lo);
@@ -313,16 +352,17 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
                         // same registers.  Each pair of warps swaps 16 rows' values for the other 16's, in
                         // fp32, and forms h of the rows it then has both of.
                         const bool is_u = quarter >= 2;
-                        float4* mine = reinterpret_cast<float4*>(smem + C::kSwap + (pn & 1) * kEpiThreads * 64) + etid;
-                        const float4* theirs = mine + ((warp ^ 6) - warp) * 32;
+                        float4* mine = reinterpret_cast<float4*>(smem + C::kPanels + kGroups * kBuffers * C::kBuffer +
+                                                                 group * C::kSwap) + etid;
+                        const float4* theirs = mine + (((etid >> 5) ^ 2) - (etid >> 5)) * 32;
                         // g gives away rows 16-31 (blocks 2, 3), u rows 0-15
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const uint32_t* l = is_u ? lo + 4 * i : lo + 8 + 4 * i;
                             const uint32_t* h = is_u ? hi + 4 * i : hi + 8 + 4 * i;
-                            mine[(2 * i) * kEpiThreads] = make_float4(__uint_as_float(l[0]), __uint_as_float(l[1]),
+                            mine[(2 * i) * kGroupThreads] = make_float4(__uint_as_float(l[0]), __uint_as_float(l[1]),
                                                                       __uint_as_float(l[2]), __uint_as_float(l[3]));
-                            mine[(2 * i + 1) * kEpiThreads] = make_float4(__uint_as_float(h[0]), __uint_as_float(h[1]),
+                            mine[(2 * i + 1) * kGroupThreads] = make_float4(__uint_as_float(h[0]), __uint_as_float(h[1]),
                                                                           __uint_as_float(h[2]), __uint_as_float(h[3]));
                         }
                         const uint32_t at = buf + mr * 128 + (((my_chunk + mj) ^ mr) << 4);
@@ -333,13 +373,13 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
                                                   pack_f(lo[4 * i + 2], lo[4 * i + 3]), pack_f(hi[4 * i], hi[4 * i + 1]),
                                                   pack_f(hi[4 * i + 2], hi[4 * i + 3]));
                         }
-                        bar_sync(2 + (quarter & 1), 64);
+                        bar_sync(3 + group * 2 + (quarter & 1), 64);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             uint32_t w[4];
 #pragma unroll
                             for (int z = 0; z < 2; ++z) {
-                                const float4 o = theirs[(2 * i + z) * kEpiThreads];
+                                const float4 o = theirs[(2 * i + z) * kGroupThreads];
                                 const uint32_t* m = z ? (is_u ? hi + 8 + 4 * i : hi + 4 * i) : (is_u ? lo + 8 + 4 * i : lo + 4 * i);
                                 const float of[4] = {o.x, o.y, o.z, o.w};
                                 float v[4];
@@ -358,9 +398,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
                         const uint32_t at = buf + my_box * kBox + mr * 128 + (((my_chunk + mj) ^ mr) << 4);
                         if constexpr (FORM == kFormDh) {
                             if (lane == 0)
-                                (void)wait<false>(&pfull[pn % kNB], (in_phase >> (pn % kNB)) & 1, abort_flag, p.err, 7, false);
+                                (void)wait<false>(&in_bar[pn % kBuffers], (in_phase >> (pn % kBuffers)) & 1, abort_flag, p.err, 7, false);
                             __syncwarp();
-                            in_phase ^= 1u << (pn % kNB);
+                            in_phase ^= 1u << (pn % kBuffers);
                         }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {  // 8 rows, 32 channels
@@ -396,8 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
                     }
                     fence_proxy_async();
                     // the next panel's buffer is free once the store that last used it has read it
-                    if (FORM != kFormDh && boss) stores_read<kNB - 2>();
-                    bar_sync(1, kEpiThreads);
+                    if (FORM != kFormDh && boss) stores_read<kBuffers - 2>();
+                    bar_sync(bar_id, kGroupThreads);
                     // box b of the buffer: which output, and its first channel
                     auto out_of = [&](int b) { return FORM == kFormUp ? b : FORM == kFormDh ? b >> 1 : 0; };
                     auto col_of = [&](int b) { return ch + (FORM == kFormUp ? 0 : (b & 1) * 64); };
@@ -410,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
                                     store_2d(&p.o[out_of(b)], col_of(b), x.row0 + q0, buf + b * kBox);
                         }
                     } else {  // the rows after these are another expert's
-                        for (int c = etid; c < C::kBoxes * n_rows * 8; c += kEpiThreads) {
+                        for (int c = etid; c < C::kBoxes * n_rows * 8; c += kGroupThreads) {
                             const int b = c / (n_rows * 8), r = c / 8 % n_rows, q = c & 7;
                             const int col = col_of(b) + q * 8;
                             if (p.out[out_of(b)] && col < n_cols)
@@ -447,19 +487,24 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
 
 // ---------------------------------------------------------------- host
 
-template <int FORM>
+template <int FORM, int MAXN>
 cudaError_t launch_form(const RowsParams& p, int64_t units, int sms, cudaStream_t st) {
-    auto kern = grouped_rows_kernel<FORM>;
-    constexpr uint32_t kSmem = Cfg<FORM>::kSmem;
+    auto kern = grouped_rows_kernel<FORM, MAXN>;
+    constexpr uint32_t kSmem = Cfg<FORM, MAXN>::kSmem;
     cudaError_t e = allow_max_smem(kern);
     if (e != cudaSuccess) return e;
     int most = 0;
-    e = resident_pairs(reinterpret_cast<const void*>(kern), kThreads, kSmem, sms, &most);
+    e = resident_clusters(reinterpret_cast<const void*>(kern), 2, kThreads, kSmem, sms, &most);
     if (e != cudaSuccess) return e;
     if (most <= 0) return cudaErrorInvalidConfiguration;
     if (units > most) units = most;
     return note_launch(reinterpret_cast<const void*>(kern), kThreads, kSmem,
-                       launch_units(kern, p, (int)units, true, kThreads, kSmem, st));
+                       launch_units(kern, p, (int)units, 2, kThreads, kSmem, st));
+}
+
+template <int FORM>
+cudaError_t launch_rows(const RowsParams& p, bool few, int64_t units, int sms, cudaStream_t st) {
+    return few ? launch_form<FORM, 64>(p, units, sms, st) : launch_form<FORM, 256>(p, units, sms, st);
 }
 
 }  // namespace
@@ -476,22 +521,22 @@ bool grouped_tc_usable(const GroupedArgs& a) {
     return true;
 }
 
-cudaError_t resident_pairs(const void* kernel, int threads, uint32_t smem, int sms, int* pairs) {
+cudaError_t resident_clusters(const void* kernel, int size, int threads, uint32_t smem, int sms, int* clusters) {
     static std::mutex mu;
-    static std::vector<std::array<int64_t, 3>> done;  // kernel, device, pairs
+    static std::vector<std::array<int64_t, 3>> done;  // kernel, device, clusters
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mu);
     for (const auto& x : done)
-        if (x[0] == (int64_t)reinterpret_cast<uintptr_t>(kernel) && x[1] == dev) { *pairs = (int)x[2]; return cudaSuccess; }
+        if (x[0] == (int64_t)reinterpret_cast<uintptr_t>(kernel) && x[1] == dev) { *clusters = (int)x[2]; return cudaSuccess; }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(sms & ~1);
+    cfg.gridDim = dim3(sms / size * size);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = size;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -499,8 +544,8 @@ cudaError_t resident_pairs(const void* kernel, int threads, uint32_t smem, int s
     int n = 0;
     e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
     if (e != cudaSuccess) return e;
-    *pairs = n < sms / 2 ? n : sms / 2;
-    done.push_back({(int64_t)reinterpret_cast<uintptr_t>(kernel), dev, *pairs});
+    *clusters = n < sms / size ? n : sms / size;
+    done.push_back({(int64_t)reinterpret_cast<uintptr_t>(kernel), dev, *clusters});
     return cudaSuccess;
 }
 
@@ -512,7 +557,13 @@ cudaError_t launch_grouped_rows_tc(const GroupedArgs& a, cudaStream_t st) {
     const bool nt = a.form == kFormUp || a.form == kFormDh;
     const uint64_t d = (uint64_t)a.d, I = (uint64_t)a.I, M = (uint64_t)a.M;
     const uint64_t K = nt ? d : I, cols = nt ? I : d;
-    const int pair_channels = a.form == kFormUp ? 128 : 256;
+#ifdef MOE_FEW
+    const bool few = MOE_FEW;
+#else
+    const bool few = (long long)a.M <= 24LL * a.N;
+#endif
+    const int max_n = few ? 64 : 256;
+    const int span = a.form == kFormUp ? 128 : 256;
     bool ok = true;
     const void* rows[2] = {a.a0, a.a1};
     const void* weights[2] = {a.b0, a.b1};
@@ -522,9 +573,9 @@ cudaError_t launch_grouped_rows_tc(const GroupedArgs& a, cudaStream_t st) {
         ok = ok && encode_bf16_2d(m, base, width, M, width * 2, 64, box_rows) == MOE_OK;
     };
     for (int i = 0; i < 2; ++i) {
-        // a box height for every half of a tile that can occur (a tile has at most M rows)
+        // a box height for every part of a tile that can occur (a tile has at most M rows, rounded up to 32)
         if (rows[i])
-            for (int h = 0; h < kMaxN / 32 && h * 32 < a.M; ++h) rows_map(&p.b[i][h], rows[i], K, (h + 1) * 16);
+            for (int h = 0; h < max_n / kStepN && h * kStepN < a.M; ++h) rows_map(&p.b[i][h], rows[i], K, (h + 1) * 16);
         // K-major weights in boxes of the rows that a CTA takes of one matrix, MN-major in 64 x 64
         if (weights[i])
             ok = ok && encode_3d(&p.a[i], true, weights[i], d, I, (uint64_t)a.N, 64, a.form == kFormDh ? 128 : 64) == MOE_OK;
@@ -535,13 +586,14 @@ cudaError_t launch_grouped_rows_tc(const GroupedArgs& a, cudaStream_t st) {
         if (outs[i]) rows_map(&p.o[i], outs[i], cols, kPanel);
     }
     if (!ok) return cudaErrorInvalidValue;
-    const int64_t col_tiles = ((int64_t)cols + pair_channels - 1) / pair_channels;
-    const int64_t units = ((int64_t)a.M / kMaxN + (a.N < a.M ? a.N : a.M)) * col_tiles;
+    const int64_t col_tiles = ((int64_t)cols + span - 1) / span;
+    // an upper bound of the tiles, each cut into up to eight parts where there are few
+    const int64_t units = ((int64_t)a.M / max_n + (a.N < a.M ? a.N : a.M)) * col_tiles * 8;
     switch (a.form) {
-        case kFormUp: return launch_form<kFormUp>(p, units, a.sms, st);
-        case kFormDown: return launch_form<kFormDown>(p, units, a.sms, st);
-        case kFormDh: return launch_form<kFormDh>(p, units, a.sms, st);
-        case kFormDx: return launch_form<kFormDx>(p, units, a.sms, st);
+        case kFormUp: return launch_rows<kFormUp>(p, few, units, a.sms, st);
+        case kFormDown: return launch_rows<kFormDown>(p, few, units, a.sms, st);
+        case kFormDh: return launch_rows<kFormDh>(p, few, units, a.sms, st);
+        case kFormDx: return launch_rows<kFormDx>(p, few, units, a.sms, st);
         case kFormDw: break;
     }
     return cudaErrorInvalidValue;
