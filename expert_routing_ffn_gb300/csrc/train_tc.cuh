@@ -130,6 +130,18 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
 }
 
 // ---------------------------------------------------------------- MMA
+// One lane of a converged warp.  The warp that issues MMAs runs its loop with
+// all lanes and picks one for the issue alone: the loop's addresses and
+// descriptors are then uniform, and an MMA takes them from uniform registers.
+// From a branch of a single lane they had to be moved there one by one, some
+// 100 cycles an MMA: 625 cycles per 64 values of K whatever N was, where a
+// 256 x 256 tile's MMAs take 512.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+
 // A shared-memory matrix descriptor advanced by `bytes` (a multiple of 16):
 // the address field is its low 14 bits, and no operand crosses 256 KB.
 __device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }

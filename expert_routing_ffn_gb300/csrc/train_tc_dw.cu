@@ -142,68 +142,81 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
     };
 
     if (warp == 0) {
-        // ---------------- loads (each CTA its own stages)
-        if (lane == 0) {
-            int it = 0, last_e = -1;
-            for (int t = unit; t < n_tiles && !*abort_flag; t += n_units) {
-                const Tile x = decode(t);
-                const unsigned char* emaps = p.maps + (size_t)x.e * kMapsPerExpert * 128;
-                if (x.e != last_e && x.rows > 0) {
-                    for (int m = 0; m < kMapsPerExpert; ++m) map_acquire(emaps + m * 128);
-                    last_e = x.e;
-                }
-                int mat, m0;
-                strip_of(x, mat, m0);
-                for (int k0 = 0; k0 < x.rows; k0 += (int)kBK, ++it) {
-                    const int st = it % kS;
-                    if (!wait<true>(&empty[st], ((it / kS) & 1) ^ 1, abort_flag, p.err, 1)) break;
-                    const uint32_t ad = base + st * kStage, bd = ad + kStageA;
-                    const uint32_t bar = leader_address(&full[st]);
+        // ---------------- loads (each CTA its own stages, on the leader's barrier)
+        const uint32_t full0 = leader_address(&full[0]);
+        int st = 0, it = 0, last_e = -1;
+        uint32_t phase = 1;
+        for (int t = unit; t < n_tiles; t += n_units) {
+            if (__any_sync(0xffffffffu, *abort_flag)) break;
+            const Tile x = decode(t);
+            int mat, m0;
+            strip_of(x, mat, m0);
+            const int rows = __shfl_sync(0xffffffffu, x.rows, 0), e = __shfl_sync(0xffffffffu, x.e, 0);
+            mat = __shfl_sync(0xffffffffu, mat, 0);
+            m0 = __shfl_sync(0xffffffffu, m0, 0);
+            const int n0 = __shfl_sync(0xffffffffu, x.n0, 0) + (int)rank * 128;
+            const unsigned char* emaps = p.maps + (size_t)e * kMapsPerExpert * 128;
+            if (e != last_e && rows > 0) {  // by every lane: any may be the one that issues the copies
+                for (int m = 0; m < kMapsPerExpert; ++m) map_acquire(emaps + m * 128);
+                last_e = e;
+            }
+            for (int k0 = 0; k0 < rows; k0 += (int)kBK, ++it) {
+                // a wait that gives up raises the abort flag, which ends the later ones
+                (void)wait<true>(&empty[st], phase, abort_flag, p.err, 1);
+                __syncwarp();
+                if (elect_one()) {
+                    const uint32_t ad = base + st * kStage, bd = ad + kStageA, bar = full0 + st * 8;
                     if (leader) mbar_arrive_expect_tx(&full[st], 2 * kStage);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) load_2d<true>(ad + j * 8192, emaps + mat * 128, m0 + j * 64, k0, bar);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        load_2d<true>(bd + j * 8192, emaps + 2 * 128, x.n0 + (int)rank * 128 + j * 64, k0, bar);
+                    for (int j = 0; j < 2; ++j) load_2d<true>(bd + j * 8192, emaps + 2 * 128, n0 + j * 64, k0, bar);
                 }
+                __syncwarp();
+                if (++st == kS) { st = 0; phase ^= 1; }
             }
-            // the leader's MMAs have consumed this CTA's last stages before it may leave
-            for (int k = it > kS ? it - kS : 0; k < it; ++k)
-                (void)wait<true>(&empty[k % kS], (k / kS) & 1, abort_flag, p.err, 2, false);
         }
+        // the leader's MMAs have consumed this CTA's last stages before it may leave
+        for (int k = it > kS ? it - kS : 0; k < it; ++k)
+            (void)wait<true>(&empty[k % kS], (k / kS) & 1, abort_flag, p.err, 2, false);
     } else if (warp == 1) {
         // ---------------- MMAs (the leader of a pair)
-        if (lane == 0 && leader) {
+        if (leader) {
             constexpr uint32_t idesc = tc_idesc(2 * kStrip, kBN, 1, 1);
             // 16 rows of 128 bytes a step, the next 64 channels or columns 8 KB on
             const uint64_t da0 = smem_desc(base, 8192, 1024), db0 = smem_desc(base + kStageA, 8192, 1024);
             int st = 0, local = 0;
             uint32_t phase = 0;
             for (int t = unit; t < n_tiles; t += n_units, ++local) {
-                if (*abort_flag) break;
-                const int rows = decode(t).rows;
+                if (__any_sync(0xffffffffu, *abort_flag)) break;
+                const int rows = __shfl_sync(0xffffffffu, decode(t).rows, 0);
                 const int ab = local & 1;
                 const uint32_t acc = tmem + ab * kBN;
-                if (!wait<true>(&tempty[ab], ((local >> 1) & 1) ^ 1, abort_flag, p.err, 3)) break;
+                // a wait that gives up raises the abort flag, which ends the later ones
+                (void)wait<true>(&tempty[ab], ((local >> 1) & 1) ^ 1, abort_flag, p.err, 3);
                 tc_fence_after();
-                bool ok = true;
                 for (int k0 = 0; k0 < rows; k0 += (int)kBK) {
-                    if (!wait<true>(&full[st], phase, abort_flag, p.err, 4)) { ok = false; break; }
+                    (void)wait<true>(&full[st], phase, abort_flag, p.err, 4);
                     tc_fence_after();
-                    const uint64_t da = desc_at(da0, st * kStage), db = desc_at(db0, st * kStage);
-                    // 16-row steps without a row of the segment are left out
+                    __syncwarp();
+                    if (elect_one()) {
+                        const uint64_t da = desc_at(da0, st * kStage), db = desc_at(db0, st * kStage);
+                        // 16-row steps without a row of the segment are left out
 #pragma unroll
-                    for (int kk = 0; kk < (int)kBK / 16; ++kk)
-                        if (kk == 0 || k0 + kk * 16 < rows)
-                            mma<true>(acc, desc_at(da, kk * 2048), desc_at(db, kk * 2048), idesc, (k0 | kk) ? 1u : 0u);
-                    commit<true>(&empty[st]);
+                        for (int kk = 0; kk < (int)kBK / 16; ++kk)
+                            if (kk == 0 || k0 + kk * 16 < rows)
+                                mma<true>(acc, desc_at(da, kk * 2048), desc_at(db, kk * 2048), idesc, (k0 | kk) ? 1u : 0u);
+                        commit<true>(&empty[st]);
+                    }
+                    __syncwarp();
                     if (++st == kS) { st = 0; phase ^= 1; }
                 }
-                if (!ok) break;
-                commit<true>(&tfull[ab]);
+                if (elect_one()) commit<true>(&tfull[ab]);
+                __syncwarp();
             }
             // every MMA issued here is done before tensor memory is released
-            commit_local<true>(drain);
+            if (elect_one()) commit_local<true>(drain);
+            __syncwarp();
             (void)wait<true>(drain, 0, abort_flag, p.err, 6, false);
         }
     } else {

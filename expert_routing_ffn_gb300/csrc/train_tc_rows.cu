@@ -223,41 +223,48 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
 
     if (warp == 0) {
         // ---------------- loads (each CTA its own stages, on the leader's barrier)
-        if (lane == 0) {
-            int it = 0;
-            for (int t = unit; t < sc.total && !*abort_flag; t += n_units) {
-                const Tile x = decode<FORM, MAXN>(p, first, sc, t);
-                if (x.rows <= 0) continue;
-                const int half = (x.rows + kStepN - 1) / kStepN * kStepN / 2;  // rows staged by each CTA
-                const int brow = x.row0 + (int)rank * half;
-                const int ch = x.c0 + (int)rank * C::kChannels;
-                for (int kb = 0; kb < nk; ++kb, ++it) {
-                    const int st = it % kS;
-                    if (!wait<true>(&empty[st], ((it / kS) & 1) ^ 1, abort_flag, p.err, 1)) break;
-                    const uint32_t ad = base + st * C::kStage, bd = ad + kStageA;
-                    const uint32_t bar = leader_address(&full[st]);
-                    if (leader) mbar_arrive_expect_tx(&full[st], 2 * (kStageA + (uint32_t)half * 128));
+        const uint32_t full0 = leader_address(&full[0]);
+        int st = 0, it = 0;
+        uint32_t phase = 1;
+        for (int t = unit; t < sc.total; t += n_units) {
+            if (__any_sync(0xffffffffu, *abort_flag)) break;
+            const Tile x = decode<FORM, MAXN>(p, first, sc, t);
+            const int rows = __shfl_sync(0xffffffffu, x.rows, 0), e = __shfl_sync(0xffffffffu, x.e, 0);
+            if (rows <= 0) continue;
+            const int half = (rows + kStepN - 1) / kStepN * kStepN / 2;  // rows staged by each CTA
+            const int brow = __shfl_sync(0xffffffffu, x.row0, 0) + (int)rank * half;
+            const int ch = __shfl_sync(0xffffffffu, x.c0, 0) + (int)rank * C::kChannels;
+            const uint32_t bytes = 2 * (kStageA + (uint32_t)half * 128);
+            for (int kb = 0; kb < nk; ++kb, ++it) {
+                // a wait that gives up raises the abort flag, which ends the later ones
+                (void)wait<true>(&empty[st], phase, abort_flag, p.err, 1);
+                __syncwarp();
+                if (elect_one()) {
+                    const uint32_t ad = base + st * C::kStage, bd = ad + kStageA, bar = full0 + st * 8;
+                    if (leader) mbar_arrive_expect_tx(&full[st], bytes);
                     const int part = FORM == kFormDx && kb >= nk1;
                     const int k0 = (kb - part * nk1) * (int)kBK;
                     if constexpr (FORM == kFormUp) {
-                        load_3d<true>(ad, &p.a[0], k0, ch, x.e, bar);
-                        load_3d<true>(ad + 8192, &p.a[1], k0, ch, x.e, bar);
+                        load_3d<true>(ad, &p.a[0], k0, ch, e, bar);
+                        load_3d<true>(ad + 8192, &p.a[1], k0, ch, e, bar);
                     } else if constexpr (FORM == kFormDh) {
-                        load_3d<true>(ad, &p.a[0], k0, ch, x.e, bar);
+                        load_3d<true>(ad, &p.a[0], k0, ch, e, bar);
                     } else {
-                        load_3d<true>(ad, &p.a[part], ch, k0, x.e, bar);
-                        load_3d<true>(ad + 8192, &p.a[part], ch + 64, k0, x.e, bar);
+                        load_3d<true>(ad, &p.a[part], ch, k0, e, bar);
+                        load_3d<true>(ad + 8192, &p.a[part], ch + 64, k0, e, bar);
                     }
                     load_2d<true>(bd, &p.b[part][half / 16 - 1], k0, brow, bar);
                 }
+                __syncwarp();
+                if (++st == kS) { st = 0; phase ^= 1; }
             }
-            // the leader's MMAs have consumed this CTA's last stages before it may leave
-            for (int k = it > kS ? it - kS : 0; k < it; ++k)
-                (void)wait<true>(&empty[k % kS], (k / kS) & 1, abort_flag, p.err, 2, false);
         }
+        // the leader's MMAs have consumed this CTA's last stages before it may leave
+        for (int k = it > kS ? it - kS : 0; k < it; ++k)
+            (void)wait<true>(&empty[k % kS], (k / kS) & 1, abort_flag, p.err, 2, false);
     } else if (warp == 1) {
         // ---------------- MMAs (the pair's leader)
-        if (lane == 0 && leader) {
+        if (leader) {
             // K-major: 16 values = 32 bytes along the swizzled row; MN-major: 16 rows of 128 bytes,
             // the next 64 channels 8 KB on
             const uint64_t da0 = C::kNT ? smem_desc(base, 16, 1024) : smem_desc(base, 8192, 1024);
@@ -266,31 +273,36 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
             int st = 0, local = 0;
             uint32_t phase = 0;
             for (int t = unit; t < sc.total; t += n_units) {
-                if (*abort_flag) break;
+                if (__any_sync(0xffffffffu, *abort_flag)) break;
                 const Tile x = decode<FORM, MAXN>(p, first, sc, t);
-                if (x.rows <= 0) continue;
-                const uint32_t idesc = tc_idesc(256, (x.rows + kStepN - 1) / kStepN * kStepN, 0, C::kNT ? 0 : 1);
+                const int rows = __shfl_sync(0xffffffffu, x.rows, 0);
+                if (rows <= 0) continue;
+                const uint32_t idesc = tc_idesc(256, (rows + kStepN - 1) / kStepN * kStepN, 0, C::kNT ? 0 : 1);
                 const int ab = local & 1;
                 const uint32_t acc = tmem + ab * 256;
-                if (!wait<true>(&tempty[ab], ((local >> 1) & 1) ^ 1, abort_flag, p.err, 3)) break;
+                // a wait that gives up raises the abort flag, which ends the later ones
+                (void)wait<true>(&tempty[ab], ((local >> 1) & 1) ^ 1, abort_flag, p.err, 3);
                 tc_fence_after();
-                bool ok = true;
                 for (int kb = 0; kb < nk; ++kb) {
-                    if (!wait<true>(&full[st], phase, abort_flag, p.err, 4)) { ok = false; break; }
+                    (void)wait<true>(&full[st], phase, abort_flag, p.err, 4);
                     tc_fence_after();
-                    const uint64_t da = desc_at(da0, st * C::kStage), db = desc_at(db0, st * C::kStage);
+                    __syncwarp();
+                    if (elect_one()) {
+                        const uint64_t da = desc_at(da0, st * C::kStage), db = desc_at(db0, st * C::kStage);
 #pragma unroll
-                    for (int kk = 0; kk < (int)kBK / 16; ++kk)
-                        mma<true>(acc, desc_at(da, kk * kStepA), desc_at(db, kk * kStepB), idesc, (kb | kk) ? 1u : 0u);
-                    commit<true>(&empty[st]);
+                        for (int kk = 0; kk < (int)kBK / 16; ++kk)
+                            mma<true>(acc, desc_at(da, kk * kStepA), desc_at(db, kk * kStepB), idesc, (kb | kk) ? 1u : 0u);
+                        commit<true>(&empty[st]);
+                        if (kb + 1 == nk) commit<true>(&tfull[ab]);
+                    }
+                    __syncwarp();
                     if (++st == kS) { st = 0; phase ^= 1; }
                 }
-                if (!ok) break;
-                commit<true>(&tfull[ab]);
                 ++local;
             }
             // every MMA issued here is done before tensor memory is released
-            commit_local<true>(drain);
+            if (elect_one()) commit_local<true>(drain);
+            __syncwarp();
             (void)wait<true>(drain, 0, abort_flag, p.err, 6, false);
         }
     } else {
