@@ -25,8 +25,12 @@ __device__ __forceinline__ uint32_t leader_address(const void* bar) {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Arrive on another CTA's barrier.  What it tells the other CTA is that tensor
+// memory has been read (ordered by the tcgen05 fence before it), so it carries
+// no cluster-scope release: that one waited for the thread's stores under way,
+// some 3000 cycles a tile in the weight-gradient kernel.
 __device__ __forceinline__ void arrive_cluster(uint32_t bar_cl) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cl) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cl) : "memory");
 }
 __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
@@ -114,6 +118,10 @@ __device__ __forceinline__ void store_3d(const void* map, int c0, int c1, int c2
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
                  ::"l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(src) : "memory");
 }
+// `bytes` (a multiple of 16) of shared memory to 16-byte aligned global memory
+__device__ __forceinline__ void store_bulk(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
 // global += shared, fp32
 __device__ __forceinline__ void add_3d(const void* map, int c0, int c1, int c2, uint32_t src) {
     asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
@@ -194,9 +202,9 @@ __device__ __forceinline__ void tmem_free(uint32_t base) {
     else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(base));
 }
 
-// 32 consecutive accumulator columns of this thread's tensor-memory lane
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
-    uint32_t r[32];
+// 32 consecutive accumulator columns of this thread's tensor-memory lane; the
+// values are there after tmem_ld_wait
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
         "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -206,9 +214,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
           "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
           "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // 16 tensor-memory lanes x 32 columns: four 16 x 8 blocks in the fragment
@@ -255,6 +260,7 @@ __device__ __forceinline__ void map_replace(void* map, uint64_t address, uint32_
     asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;" ::"l"(map), "r"(rows) : "memory");
 }
 __device__ __forceinline__ void map_release() { asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory"); }
+__device__ __forceinline__ void map_prefetch(const void* map) { asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory"); }
 __device__ __forceinline__ void map_acquire(const void* map) {
     asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
 }

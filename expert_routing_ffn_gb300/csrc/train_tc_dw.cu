@@ -11,17 +11,18 @@
 // are summed, so a step that ran past the segment would add the next expert's
 // rows: each expert has tensor maps of its own whose row count ends with its
 // segment (map kernel), and TMA fills the rest of the last step with zeros.
-// Every dW is written once, those of experts without rows as zeros, so at the
-// sizes of a training step (a few hundred rows an expert) the store of dW
-// costs as much as the MMAs: eight epilogue warps, two to a quarter of the
-// accumulator's lanes, with two 4 KB boxes each, so that stores queue up
-// instead of waiting for one another.
+// Every dW is written once, so at the sizes of a training step (a few hundred
+// rows an expert) storing it costs as much as the MMAs.  Eight epilogue warps,
+// two to a quarter of the accumulator's lanes, take their part of a tile out
+// of tensor memory in one go and give the accumulator back before they convert
+// and store.  An expert without rows has no tiles: its dW is filled with zeros
+// in contiguous pieces at the end.
 //
 // Tiles are taken round robin by the resident pairs, experts with most rows
 // first, so that the pairs end together when the load is skewed.
 //
-// Block: warp 0 issues the TMA loads, warp 1 the MMAs (one thread of the
-// pair's leader), warps 2-9 drain the accumulators (a thread owns a channel),
+// Block: warp 0 issues the TMA loads, warp 1 the MMAs (of the pair's leader),
+// warps 2-9 the epilogue (a thread owns a channel).  Accumulators are
 // double-buffered.  Every wait is bounded.
 #include <cuda.h>
 
@@ -47,26 +48,66 @@ constexpr uint32_t kBox = 32 * 128;          // 32 channels x 128 bytes
 constexpr int kMapsPerExpert = 3;            // a0, a1, b
 constexpr int kS = 5;                        // stages
 constexpr uint32_t kBoxes = kS * kStage, kTable = kBoxes + kEpiWarps * kBoxesPerWarp * kBox;  // table: rank -> expert
-constexpr uint32_t kBars = kTable + kTrainMaxExperts * 4;
+constexpr uint32_t kBars = kTable + kTrainMaxExperts * 4 + 16;
 constexpr uint32_t kSmem = kBars + (2 * kS + 5) * 8 + 16;
 static_assert(kSmem <= 232448, "227 KB of shared memory per block");
 
 struct DwParams {
     CUtensorMap o[2];
+    unsigned char* out[2];
     const unsigned char* maps;  // [N][kMapsPerExpert] tensor maps
     const int32_t* offsets;
     int M, N, d, I, n_mat, accumulate;
     DevError* err;
 };
 
-struct Tile {
+// The tiles of one pair in order: expert by expert (order[] of falling rows,
+// those without rows left out), strips outermost, column tiles innermost: the
+// rows of dW that consecutive pairs write at a time are contiguous.
+struct Walk {
     int e, rows, strip, n0;  // expert, its rows, the pair's first strip, first column
+    int place, n_live, mt, nt, mts, nts, d_place, d_mt, d_nt;
+
+    __device__ __forceinline__ bool more() const { return place < n_live; }
+    __device__ __forceinline__ void set(const DwParams& p, const int* order, bool new_expert) {
+        strip = 2 * mt;
+        n0 = nt * kBN;
+        if (new_expert && place < n_live) {
+            e = order[place];
+            const int r0 = min(max(p.offsets[e], 0), p.M);
+            rows = max(min(max(p.offsets[e + 1], 0), p.M) - r0, 0);
+        }
+    }
+    __device__ __forceinline__ Walk(const DwParams& p, const int* order, int live, int unit, int n_units) {
+        mts = ((p.I + kStrip - 1) / kStrip * p.n_mat + 1) / 2;
+        nts = (p.d + kBN - 1) / kBN;
+        n_live = live;
+        const int per = mts * nts;
+        place = unit / per;
+        mt = unit % per / nts;
+        nt = unit % nts;
+        d_place = n_units / per;
+        d_mt = n_units % per / nts;
+        d_nt = n_units % nts;
+        e = rows = 0;
+        set(p, order, true);
+    }
+    __device__ __forceinline__ void next(const DwParams& p, const int* order) {
+        const int was = place;
+        nt += d_nt;
+        mt += d_mt;
+        place += d_place;
+        if (nt >= nts) { nt -= nts; ++mt; }
+        if (mt >= mts) { mt -= mts; ++place; }
+        set(p, order, place != was);
+    }
 };
 
 template <bool F32>
 __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_constant__ DwParams p) {
     extern __shared__ __align__(1024) unsigned char smem[];
     int* order = reinterpret_cast<int*>(smem + kTable);  // rank -> expert
+    int* live_s = order + kTrainMaxExperts;               // experts with rows
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBars);
     uint64_t *empty = full + kS, *tfull = empty + kS, *tempty = tfull + 2, *drain = tempty + 2;
     uint32_t* tmem_s = reinterpret_cast<uint32_t*>(drain + 1);
@@ -86,6 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
     {  // experts in order of falling row count (the lower index first among equals)
         int* rows_s = reinterpret_cast<int*>(smem);  // the stages are not in use yet
         for (int e = tid; e < p.N; e += kThreads) rows_s[e] = rows_of(e);
+        if (tid == 0) *live_s = 0;
         __syncthreads();
         for (int e = tid; e < p.N; e += kThreads) {
             const int r = rows_s[e];
@@ -95,6 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
                 place += q > r || (q == r && f < e);
             }
             order[place] = e;
+            if (r > 0) atomicMax(live_s, place + 1);
         }
     }
     if (tid == 32) {
@@ -121,21 +164,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
     cluster_sync();  // the peer's barriers are ready before any arrival from here
     tc_fence_after();
     const uint32_t tmem = *tmem_s;
+    const int live = *live_s;
     const int strips = (p.I + kStrip - 1) / kStrip;  // of one a
-    const int mts = (strips * p.n_mat + 1) / 2, per = mts * ((p.d + kBN - 1) / kBN), n_tiles = per * p.N;
-    // strips innermost: a column tile of b is read by consecutive pairs
-    auto decode = [&](int t) {
-        Tile x;
-        const int place = t / per, local = t - place * per;
-        x.e = order[place];
-        x.rows = rows_of(x.e);
-        x.n0 = local / mts;
-        x.strip = (local - x.n0 * mts) * 2;
-        x.n0 *= kBN;
-        return x;
-    };
     // this CTA's strip of a tile: which a, and its first channel (past I: no such strip)
-    auto strip_of = [&](const Tile& x, int& mat, int& m0) {
+    auto strip_of = [&](const Walk& x, int& mat, int& m0) {
         const int q = x.strip + (int)rank;
         mat = q >= strips && p.n_mat > 1;
         m0 = (q - (mat ? strips : 0)) * kStrip;
@@ -144,22 +176,22 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
     if (warp == 0) {
         // ---------------- loads (each CTA its own stages, on the leader's barrier)
         const uint32_t full0 = leader_address(&full[0]);
-        int st = 0, it = 0, last_e = -1;
+        int st = 0, it = 0;
         uint32_t phase = 1;
-        for (int t = unit; t < n_tiles; t += n_units) {
+        for (int i = lane; i < p.N * kMapsPerExpert; i += 32) map_acquire(p.maps + (size_t)i * 128);
+        __syncwarp();
+        for (Walk x(p, order, live, unit, n_units); x.more(); x.next(p, order)) {
             if (__any_sync(0xffffffffu, *abort_flag)) break;
-            const Tile x = decode(t);
             int mat, m0;
             strip_of(x, mat, m0);
             const int rows = __shfl_sync(0xffffffffu, x.rows, 0), e = __shfl_sync(0xffffffffu, x.e, 0);
-            mat = __shfl_sync(0xffffffffu, mat, 0);
-            m0 = __shfl_sync(0xffffffffu, m0, 0);
-            const int n0 = __shfl_sync(0xffffffffu, x.n0, 0) + (int)rank * 128;
+            const int n0 = x.n0 + (int)rank * 128;
             const unsigned char* emaps = p.maps + (size_t)e * kMapsPerExpert * 128;
-            if (e != last_e && rows > 0) {  // by every lane: any may be the one that issues the copies
-                for (int m = 0; m < kMapsPerExpert; ++m) map_acquire(emaps + m * 128);
-                last_e = e;
-            }
+            Walk nx = x;
+            nx.next(p, order);
+            if (nx.more() && nx.e != x.e && lane < kMapsPerExpert)
+                map_prefetch(p.maps + ((size_t)nx.e * kMapsPerExpert + lane) * 128);
+            __syncwarp();
             for (int k0 = 0; k0 < rows; k0 += (int)kBK, ++it) {
                 // a wait that gives up raises the abort flag, which ends the later ones
                 (void)wait<true>(&empty[st], phase, abort_flag, p.err, 1);
@@ -187,9 +219,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
             const uint64_t da0 = smem_desc(base, 8192, 1024), db0 = smem_desc(base + kStageA, 8192, 1024);
             int st = 0, local = 0;
             uint32_t phase = 0;
-            for (int t = unit; t < n_tiles; t += n_units, ++local) {
+            for (Walk x(p, order, live, unit, n_units); x.more(); x.next(p, order), ++local) {
                 if (__any_sync(0xffffffffu, *abort_flag)) break;
-                const int rows = __shfl_sync(0xffffffffu, decode(t).rows, 0);
+                const int rows = __shfl_sync(0xffffffffu, x.rows, 0);
                 const int ab = local & 1;
                 const uint32_t acc = tmem + ab * kBN;
                 // a wait that gives up raises the abort flag, which ends the later ones
@@ -221,63 +253,79 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
         }
     } else {
         // ---------------- epilogue: a thread owns a channel of dW, two warps share a quarter of
-        // the lanes and take every other box of columns
+        // the lanes, 128 columns each
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const uint32_t boxes = base + kBoxes + (warp - 2) * kBoxesPerWarp * kBox;
         const uint32_t sw = lane & 7;  // 128-byte swizzle: chunk j of row i at chunk j ^ (i & 7)
         const uint32_t free0 = leader_address(&tempty[0]), free1 = leader_address(&tempty[1]);
-        int local = 0, pn = 0;
+        int local = 0;
         constexpr int kW = F32 ? 32 : 64;  // columns of a box
-        for (int t = unit; t < n_tiles; t += n_units, ++local) {
-            if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
-            const Tile x = decode(t);
+        for (Walk x(p, order, live, unit, n_units); x.more(); x.next(p, order), ++local) {
+            if (__any_sync(0xffffffffu, *abort_flag)) break;
             const int ab = local & 1;
-            bool ok = true;
-            if (lane == 0) ok = wait<true>(&tfull[ab], (local >> 1) & 1, abort_flag, p.err, 5);
-            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-            tc_fence_after();
-            const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + ab * kBN;
             int mat, m;
             strip_of(x, mat, m);
             m += quarter * 32;  // this warp's first channel
-            if (m < p.I && !(p.accumulate && x.rows == 0)) {
-#pragma unroll 1
-                for (int c = half * kW; c < kBN && x.n0 + c < p.d; c += 2 * kW, ++pn) {
-                    const uint32_t box = boxes + (pn % kBoxesPerWarp) * kBox;
-                    if (lane == 0) stores_read<kBoxesPerWarp - 1>();  // the store that last used this box
-                    __syncwarp();
+            (void)wait<true>(&tfull[ab], (local >> 1) & 1, abort_flag, p.err, 5);
+            tc_fence_after();
+            __syncwarp();
+            const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + ab * kBN + half * 128;
+            uint32_t v[128];
 #pragma unroll
-                    for (int hh = 0; hh < kW / 32; ++hh) {
-                        float v[32];
-                        if (x.rows > 0) tmem_ld32(taddr + c + hh * 32, v);
-                        else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = 0.f;
-                        }
-                        // 64 bytes (32 bf16 values, or 16 of 32 floats) a half of the box's row
-#pragma unroll
-                        for (int q = 0; q < (F32 ? 8 : 4); ++q) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                w[i] = F32 ? __float_as_uint(v[q * 4 + i]) : pack_bf16x2(v[q * 8 + 2 * i], v[q * 8 + 2 * i + 1]);
-                            st_shared16(box + lane * 128 + ((((uint32_t)(hh * 4 + q)) ^ sw) << 4), w[0], w[1], w[2], w[3]);
-                        }
-                    }
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (F32 && p.accumulate) add_3d(&p.o[mat], x.n0 + c, m, x.e, box);
-                        else store_3d(&p.o[mat], x.n0 + c, m, x.e, box);
-                        stores_commit();
-                    }
-                }
-            }
+            for (int i = 0; i < 4; ++i) tmem_ld32(taddr + i * 32, v + i * 32);
+            tmem_ld_wait();
+            // the accumulator is free
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
                 if (!leader) arrive_cluster(ab ? free1 : free0);
                 else mbar_arrive(&tempty[ab]);
+            }
+            if (m >= p.I) continue;
+            // a box at a time: one is filled while the store of the other drains
+#pragma unroll
+            for (int r = 0; r < 128 / kW; ++r) {
+                const uint32_t box = boxes + (r & 1) * kBox;
+                if (lane == 0) stores_read<1>();
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {  // 16 bytes
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = F32 ? v[r * kW + q * 4 + i]
+                                   : pack_bf16x2(__uint_as_float(v[r * kW + q * 8 + 2 * i]),
+                                                 __uint_as_float(v[r * kW + q * 8 + 2 * i + 1]));
+                    st_shared16(box + lane * 128 + (((uint32_t)q ^ sw) << 4), w[0], w[1], w[2], w[3]);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                const int col = x.n0 + half * 128 + r * kW;
+                if (lane == 0) {
+                    if (col >= p.d) {
+                    } else if (F32 && p.accumulate) add_3d(&p.o[mat], col, m, x.e, box);
+                    else store_3d(&p.o[mat], col, m, x.e, box);
+                    stores_commit();
+                }
+            }
+        }
+        // zeros for the experts without rows, in contiguous pieces of this warp's boxes
+        if (!p.accumulate && live < p.N) {
+            constexpr uint32_t kPiece = kBoxesPerWarp * kBox;
+            if (lane == 0) stores_read<0>();
+            __syncwarp();
+            for (uint32_t i = lane * 16; i < kPiece; i += 512) st_shared16(boxes + i, 0, 0, 0, 0);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                const uint64_t bytes = (uint64_t)p.I * p.d * (F32 ? 4 : 2), pieces = (bytes + kPiece - 1) / kPiece;
+                const uint64_t n = pieces * (uint64_t)(p.N - live) * p.n_mat;
+                for (uint64_t c = (uint64_t)blockIdx.x * kEpiWarps + (warp - 2); c < n; c += (uint64_t)gridDim.x * kEpiWarps) {
+                    const uint64_t which = c / pieces, at = (c - which * pieces) * kPiece;
+                    unsigned char* o = p.out[which % p.n_mat] + (uint64_t)order[live + which / p.n_mat] * bytes + at;
+                    store_bulk(o, boxes, (uint32_t)min((uint64_t)kPiece, bytes - at));
+                    stores_commit();
+                }
             }
         }
         // the boxes stay until the stores have read them, and the outputs are
@@ -364,6 +412,8 @@ cudaError_t launch_grouped_dw_tc(const GroupedArgs& a, cudaStream_t st) {
         mp.row_bytes[i] = (int64_t)cols * 2;
     }
     mp.maps = a.maps; mp.offsets = a.offsets; mp.M = a.M; mp.N = a.N;
+    p.out[0] = static_cast<unsigned char*>(a.o0);
+    p.out[1] = static_cast<unsigned char*>(a.o1);
     for (int i = 0; i < p.n_mat; ++i)
         if (encode_3d(&p.o[i], !a.out_f32, i ? a.o1 : a.o0, d, I, (uint64_t)a.N, a.out_f32 ? 32 : 64, 32) != MOE_OK)
             return cudaErrorInvalidValue;
