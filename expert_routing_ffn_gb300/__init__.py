@@ -169,6 +169,8 @@ _PROTOS = {
 def lib():
     """Load libmoe_gb300.so (built by build.py / __graft_entry__.build())."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -223,13 +225,8 @@ def wdtype(dims: moe_dims):
 
 def make_dims(T, d, N, k, I, n_shared=0, I_shared=0, r=0, delta_max=None, wtype="bf16",
               renorm_topk=0) -> moe_dims:
-    D = moe_dims()
-    D.T, D.d, D.N, D.k, D.I = T, d, N, k, I
-    D.n_shared, D.I_shared, D.r = n_shared, I_shared, r
-    D.delta_max = N - k if delta_max is None else delta_max
-    D.wtype = MOE_DTYPE_BF16 if wtype in ("bf16", MOE_DTYPE_BF16) else MOE_DTYPE_F32
-    D.renorm_topk = renorm_topk
-    return D
+    return moe_dims(T, d, N, k, I, n_shared, I_shared, r, N - k if delta_max is None else delta_max,
+                    MOE_DTYPE_BF16 if wtype in ("bf16", MOE_DTYPE_BF16) else MOE_DTYPE_F32, renorm_topk)
 
 
 def moe_launch_total() -> int:

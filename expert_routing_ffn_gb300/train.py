@@ -40,11 +40,8 @@ _F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
 _WTYPE = {MOE_DTYPE_F32: torch.float32, MOE_DTYPE_BF16: torch.bfloat16}
 
 
-def _buf(t, dtype, numel, name, optional=False):
-    """Address of a contiguous CUDA tensor of at least numel elements (None -> None if optional)."""
+def _refuse(t, dtype, numel, name):
     if t is None:
-        if optional:
-            return None
         raise ValueError(f"{name} is required")
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -52,29 +49,44 @@ def _buf(t, dtype, numel, name, optional=False):
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.numel() < numel:
-        raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
-    return t.data_ptr()
+    raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
+
+
+def _buf(t, dtype, numel, name, optional=False):
+    """Address of a contiguous CUDA tensor of at least numel elements (None -> None if optional)."""
+    try:
+        if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= numel:
+            return t.data_ptr()
+    except AttributeError:
+        if t is None and optional:
+            return None
+    _refuse(t, dtype, numel, name)
 
 
 def _rows(t, dtype, T, d, name, optional=False):
     """Address and row stride of token rows [T, d] (contiguous columns)."""
-    if t is None:
-        if optional:
-            return None, 0
-        raise ValueError(f"{name} is required")
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.dim() != 2 or t.shape[0] < T or t.shape[1] != d:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs [{T}, {d}]")
-    if d > 1 and t.stride(1) != 1:
+    if t is None and optional:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype:
+        _refuse(t, dtype, T * d, name)
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < T or shape[1] != d:
+        raise ValueError(f"{name} has shape {tuple(shape)}, needs [{T}, {d}]")
+    ld, inner = t.stride()
+    if inner != 1 and d > 1:
         raise ValueError(f"{name} must have contiguous columns")
-    ld = t.stride(0) if T > 1 else d
+    if T <= 1:
+        ld = d
     if ld < d:
         raise ValueError(f"{name} has a row stride of {ld}, below its {d} columns")
     return t.data_ptr(), ld
+
+
+def _queue(t, stream):
+    """The stream of a call: the given one, or the current one of the device of tensor t."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _stream(stream)
 
 
 def _grad_type(dims, a, b, names, numel):
@@ -109,7 +121,7 @@ def moe_dispatch_rows(dims, x, expert_idx, capacity, x_perm, expert_offsets, per
         C.byref(dims), px, ldx, _buf(expert_idx, _I32, slots, "expert_idx"), int(capacity),
         _buf(x_perm, wt, slots * d, "x_perm"), _buf(expert_offsets, _I32, dims.N + 1, "expert_offsets"),
         _buf(perm, _I32, slots, "perm"), _buf(inv_perm, _I32, slots, "inv_perm"),
-        _buf(ws, _U8, 0, "ws"), ws.numel(), _stream(stream)), "moe_dispatch_rows")
+        _buf(ws, _U8, 0, "ws"), ws.numel(), _queue(x, stream)), "moe_dispatch_rows")
 
 
 def moe_dispatch_rows_grad(dims, dx_perm, inv_perm, add, dx, stream=None):
@@ -119,7 +131,7 @@ def moe_dispatch_rows_grad(dims, dx_perm, inv_perm, add, dx, stream=None):
     pdx, lddx = _rows(dx, wt, T, d, "dx")
     _check(lib().moe_dispatch_rows_grad(
         C.byref(dims), _buf(dx_perm, wt, slots * d, "dx_perm"), _buf(inv_perm, _I32, slots, "inv_perm"), padd, ldadd,
-        pdx, lddx, _stream(stream)), "moe_dispatch_rows_grad")
+        pdx, lddx, _queue(dx_perm, stream)), "moe_dispatch_rows_grad")
 
 
 def moe_combine_rows(dims, y_perm, gate, inv_perm, add, out, stream=None):
@@ -129,7 +141,7 @@ def moe_combine_rows(dims, y_perm, gate, inv_perm, add, out, stream=None):
     pout, ldout = _rows(out, wt, T, d, "out")
     _check(lib().moe_combine_rows(
         C.byref(dims), _buf(y_perm, wt, slots * d, "y_perm"), _buf(gate, _F32, slots, "gate", True),
-        _buf(inv_perm, _I32, slots, "inv_perm"), padd, ldadd, pout, ldout, _stream(stream)), "moe_combine_rows")
+        _buf(inv_perm, _I32, slots, "inv_perm"), padd, ldadd, pout, ldout, _queue(y_perm, stream)), "moe_combine_rows")
 
 
 def moe_combine_rows_grad(dims, dout, y_perm, gate, inv_perm, dy_perm, dgate, stream=None):
@@ -140,7 +152,7 @@ def moe_combine_rows_grad(dims, dout, y_perm, gate, inv_perm, dy_perm, dgate, st
         C.byref(dims), pd, ldd, _buf(y_perm, wt, slots * d, "y_perm", dgate is None),
         _buf(gate, _F32, slots, "gate", True), _buf(inv_perm, _I32, slots, "inv_perm"),
         _buf(dy_perm, wt, slots * d, "dy_perm", True), _buf(dgate, _F32, slots, "dgate", True),
-        _stream(stream)), "moe_combine_rows_grad")
+        _queue(dout, stream)), "moe_combine_rows_grad")
 
 
 def moe_gate_grad(dims, router_prob, topk_idx, dgate, balance, dlogits, balance_loss, ws, stream=None):
@@ -149,7 +161,7 @@ def moe_gate_grad(dims, router_prob, topk_idx, dgate, balance, dlogits, balance_
     _check(lib().moe_gate_grad(
         C.byref(dims), _buf(router_prob, _F32, T * N, "router_prob"), _buf(topk_idx, _I32, slots, "topk_idx"),
         _buf(dgate, _F32, slots, "dgate"), float(balance), _buf(dlogits, _F32, T * N, "dlogits"),
-        _buf(balance_loss, _F32, 1, "balance_loss", True), _buf(ws, _U8, 0, "ws"), ws.numel(), _stream(stream)),
+        _buf(balance_loss, _F32, 1, "balance_loss", True), _buf(ws, _U8, 0, "ws"), ws.numel(), _queue(router_prob, stream)),
         "moe_gate_grad")
 
 
@@ -161,7 +173,7 @@ def moe_experts_up(dims, x_perm, expert_offsets, w_gate, w_up, g, u, h, ws, stre
         C.byref(dims), _buf(x_perm, wt, slots * d, "x_perm"), _buf(expert_offsets, _I32, dims.N + 1, "expert_offsets"),
         _buf(w_gate, wt, nw, "w_gate"), _buf(w_up, wt, nw, "w_up"), _buf(g, wt, slots * I, "g", True),
         _buf(u, wt, slots * I, "u", True), _buf(h, wt, slots * I, "h"), _buf(ws, _U8, 0, "ws"), ws.numel(),
-        _stream(stream)), "moe_experts_up")
+        _queue(x_perm, stream)), "moe_experts_up")
 
 
 def moe_experts_up_grad(dims, dg, du, x_perm, expert_offsets, w_gate, w_up, dx_perm, dw_gate, dw_up, accumulate, ws,
@@ -177,7 +189,7 @@ def moe_experts_up_grad(dims, dg, du, x_perm, expert_offsets, w_gate, w_up, dx_p
         _buf(x_perm, wt, slots * d, "x_perm", pg is None), _buf(expert_offsets, _I32, dims.N + 1, "expert_offsets"),
         _buf(w_gate, wt, nw, "w_gate", dx_perm is None), _buf(w_up, wt, nw, "w_up", dx_perm is None),
         _buf(dx_perm, wt, slots * d, "dx_perm", True), pg, pu, gtype, int(bool(accumulate)),
-        _buf(ws, _U8, 0, "ws"), ws.numel(), _stream(stream)), "moe_experts_up_grad")
+        _buf(ws, _U8, 0, "ws"), ws.numel(), _queue(dg, stream)), "moe_experts_up_grad")
 
 
 def moe_experts_down(dims, h, expert_offsets, w_down, y_perm, ws, stream=None):
@@ -186,7 +198,7 @@ def moe_experts_down(dims, h, expert_offsets, w_down, y_perm, ws, stream=None):
     _check(lib().moe_experts_down(
         C.byref(dims), _buf(h, wt, slots * I, "h"), _buf(expert_offsets, _I32, dims.N + 1, "expert_offsets"),
         _buf(w_down, wt, dims.N * I * d, "w_down"), _buf(y_perm, wt, slots * d, "y_perm"), _buf(ws, _U8, 0, "ws"),
-        ws.numel(), _stream(stream)), "moe_experts_down")
+        ws.numel(), _queue(h, stream)), "moe_experts_down")
 
 
 def moe_experts_down_grad(dims, dy_perm, h, g, u, expert_offsets, w_down, dg, du, dw_down, accumulate, ws, stream=None):
@@ -201,4 +213,4 @@ def moe_experts_down_grad(dims, dy_perm, h, g, u, expert_offsets, w_down, dg, du
         _buf(g, wt, slots * I, "g", skip), _buf(u, wt, slots * I, "u", skip),
         _buf(expert_offsets, _I32, dims.N + 1, "expert_offsets"), _buf(w_down, wt, nw, "w_down", skip),
         _buf(dg, wt, slots * I, "dg", True), _buf(du, wt, slots * I, "du", True), pw, gtype, int(bool(accumulate)),
-        _buf(ws, _U8, 0, "ws"), ws.numel(), _stream(stream)), "moe_experts_down_grad")
+        _buf(ws, _U8, 0, "ws"), ws.numel(), _queue(dy_perm, stream)), "moe_experts_down_grad")
