@@ -23,17 +23,14 @@ constexpr int kTrainMaxSlots = 1 << 24;
 constexpr size_t kTrainMaxWs = 16u << 20;
 
 // ---------------------------------------------------------------- token rows
-// Slots per block of the dispatch: the slots of whole tokens.  Larger chunks
-// for long batches keep the table of counts (chunks x experts) short.
-constexpr int kDispChunk = 1024, kDispChunkLong = 4096, kDispLongSlots = 1 << 16;
-inline int dispatch_chunk_tokens(int T, int k) {
-    const int slots = (long long)T * k > kDispLongSlots ? kDispChunkLong : kDispChunk;
-    const int t = slots / k;
-    return t < T ? t : (T > 0 ? T : 1);
-}
-inline int dispatch_chunks(int T, int k) {
-    const int t = dispatch_chunk_tokens(T, k);
-    return (T + t - 1) / t;
+// Batches of up to kDispAlone slots are sorted in one launch, each block
+// counting all slots; longer ones have a counting launch first, a block per
+// span of whole tokens, about kDispSpan slots.
+constexpr int kDispAlone = 1 << 14, kDispSpan = 1 << 12;
+inline int dispatch_span_tokens(int T, int k) { return (long long)T * k <= kDispAlone ? (T > 0 ? T : 1) : kDispSpan / k; }
+inline int dispatch_spans(int T, int k) {
+    const int t = dispatch_span_tokens(T, k);
+    return T > 0 ? (T + t - 1) / t : 1;
 }
 
 struct DispatchArgs {
@@ -42,7 +39,7 @@ struct DispatchArgs {
     int T, N, k, capacity;
     int64_t row_bytes;
     void* x_perm; int32_t *offsets, *perm, *inv;
-    int32_t* counts;  // workspace: chunks x (N + 1)
+    int32_t* counts;  // workspace: spans x (N + 1)
     int sms;
     DevError* err;
 };
@@ -66,7 +63,7 @@ struct CombineRowsGradArgs {
 cudaError_t launch_combine_rows_grad(const CombineRowsGradArgs& a, cudaStream_t st);
 
 // ---------------------------------------------------------------- router
-constexpr int kGateParts = 64;  // blocks of the load and probability sums
+constexpr int kGateParts = 128;  // blocks of the load and probability sums
 struct GateGradArgs {
     const float* prob; const int32_t* idx; const float* dgate;
     int T, N, k, renorm; float balance;

@@ -49,7 +49,7 @@ TrainWs train_ws(const moe_dims& D) {
     L.err = 0;
     const size_t o = align_up(sizeof(DevError), kAlign);
     L.counts = L.part = L.maps = o;
-    const size_t counts = (size_t)dispatch_chunks(D.T, D.k) * (D.N + 1) * 4;
+    const size_t counts = (size_t)dispatch_spans(D.T, D.k) * (D.N + 1) * 4;
     const size_t part = (size_t)kGateParts * 2 * D.N * 4;
     const size_t maps = (size_t)D.N * 3 * 128;
     size_t most = counts > part ? counts : part;

@@ -5,8 +5,9 @@
 //          (dgate_s - sum_j dgate_j gate_j) / sum_j p_j)  +  c N f_e / T
 //   dl_e = p_e (v_e - sum_j p_j v_j)
 //   loss = c N sum_e f_e P_e,  f_e = slots on e / (T k),  P_e = mean_t p_te
-// T x N floats in and out: bytes for long batches, launch latency for short
-// ones.  A warp owns a token, a lane every 32nd expert.  f and P need the
+// T x N floats in and out: latency decides at every size (16384 tokens of 40
+// experts, 6 MB: 14 us in two launches).  A warp owns a token, up to four at a
+// time so that their loads are in flight together, a lane every 32nd expert.  f and P need the
 // whole batch first; their sums are taken by at most kGateParts blocks in
 // token order and added up by every block of the second launch, so no atomic
 // decides an order.  Without a balance term that first launch is left out.
@@ -70,12 +71,27 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(const GateParams p)
     grid_dep_wait();
     const bool bal = p.parts > 0;
     if (bal) {
-        for (int e = tid; e < p.N; e += kThreads) {
+        // the parts in kSlices runs, a run a thread, then the runs in order
+        constexpr int kSlices = 8;
+        float* run = gsm + 2 * p.N;  // [kSlices][2][N]
+        for (int i = tid; i < kSlices * p.N; i += kThreads) {
+            const int q = i / p.N, e = i - q * p.N;
             float c = 0.f, s = 0.f;
 #pragma unroll 8
-            for (int b = 0; b < p.parts; ++b) {
+            for (int b = q; b < p.parts; b += kSlices) {
                 c += __ldcg(p.part + (size_t)b * 2 * p.N + e);
                 s += __ldcg(p.part + (size_t)b * 2 * p.N + p.N + e);
+            }
+            run[(q * 2) * p.N + e] = c;
+            run[(q * 2 + 1) * p.N + e] = s;
+        }
+        __syncthreads();
+        for (int e = tid; e < p.N; e += kThreads) {
+            float c = 0.f, s = 0.f;
+#pragma unroll
+            for (int q = 0; q < kSlices; ++q) {
+                c += run[(q * 2) * p.N + e];
+                s += run[(q * 2 + 1) * p.N + e];
             }
             const float f = c / ((float)p.T * (float)p.k);
             load[e] = p.balance * (float)p.N / (float)p.T * f;
@@ -89,43 +105,59 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(const GateParams p)
             for (int e = 0; e < p.N; ++e) l += lterm[e];
         p.loss[0] = p.balance * (float)p.N * l;
     }
-    for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < p.T; t += (int64_t)gridDim.x * kWarps) {
-        const float* row = p.prob + t * p.N;
-        int my_e = -1;
-        float my_d = 0.f;
-        if (lane < p.k) {
-            my_e = p.idx[t * p.k + lane];
-            if (my_e < 0 || my_e >= p.N) my_e = -1;
-            else my_d = p.dgate[t * p.k + lane];
-        }
-        float q[NV], v[NV];
+    // kU tokens at a time: their loads are in flight together
+    constexpr int kU = NV <= 2 ? 4 : NV <= 4 ? 2 : 1;
+    const int64_t stride = (int64_t)gridDim.x * kWarps;
+    for (int64_t t0 = (int64_t)blockIdx.x * kWarps + warp; t0 < p.T; t0 += kU * stride) {
+        int my_e[kU];
+        float my_d[kU], my_p[kU], q[kU][NV], v[kU][NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = i * 32 + lane;
-            q[i] = e < p.N ? row[e] : 0.f;
-            v[i] = bal && e < p.N ? load[e] : 0.f;
-        }
-        if (p.renorm) {
-            const float my_p = my_e >= 0 ? row[my_e] : 0.f;
-            const float total = warp_sum(my_p);
-            const float inv = total > 0.f ? 1.f / total : 0.f;
-            const float mean = warp_sum(my_d * (my_p * inv));
-            my_d = my_e >= 0 ? (my_d - mean) * inv : 0.f;
-        }
-        for (int s = 0; s < p.k; ++s) {
-            const int e = __shfl_sync(0xffffffffu, my_e, s);
-            const float dg = __shfl_sync(0xffffffffu, my_d, s);
+        for (int u = 0; u < kU; ++u) {
+            const int64_t t = t0 + u * stride;
+            my_e[u] = -1;
+            my_d[u] = my_p[u] = 0.f;
+            if (lane < p.k && t < p.T) {
+                my_e[u] = p.idx[t * p.k + lane];
+                my_d[u] = p.dgate[t * p.k + lane];
+            }
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (e == i * 32 + lane) v[i] += dg;
+            for (int i = 0; i < NV; ++i) {
+                const int e = i * 32 + lane;
+                q[u][i] = e < p.N && t < p.T ? p.prob[t * p.N + e] : 0.f;
+                v[u][i] = bal && e < p.N ? load[e] : 0.f;
+            }
         }
-        float dot = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) dot = fmaf(q[i], v[i], dot);
-        dot = warp_sum(dot);
+        for (int u = 0; u < kU; ++u) {
+            if (my_e[u] < 0 || my_e[u] >= p.N) my_e[u] = -1, my_d[u] = 0.f;
+            else if (p.renorm) my_p[u] = p.prob[(t0 + u * stride) * p.N + my_e[u]];
+        }
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (i * 32 + lane < p.N) p.dlogits[t * p.N + i * 32 + lane] = q[i] * (v[i] - dot);
+        for (int u = 0; u < kU; ++u) {
+            if (p.renorm) {
+                const float total = warp_sum(my_p[u]);
+                const float inv = total > 0.f ? 1.f / total : 0.f;
+                const float mean = warp_sum(my_d[u] * (my_p[u] * inv));
+                my_d[u] = my_e[u] >= 0 ? (my_d[u] - mean) * inv : 0.f;
+            }
+            for (int s = 0; s < p.k; ++s) {
+                const int e = __shfl_sync(0xffffffffu, my_e[u], s);
+                const float dg = __shfl_sync(0xffffffffu, my_d[u], s);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (e == i * 32 + lane) v[u][i] += dg;
+            }
+            float dot = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) dot = fmaf(q[u][i], v[u][i], dot);
+            dot = warp_sum(dot);
+            const int64_t t = t0 + u * stride;
+            if (t < p.T) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (i * 32 + lane < p.N) p.dlogits[t * p.N + i * 32 + lane] = q[u][i] * (v[u][i] - dot);
+            }
+        }
     }
     grid_dep_launch();
 }
@@ -151,9 +183,9 @@ cudaError_t launch_gate_grad(const GateGradArgs& a, cudaStream_t st, int* launch
         *launches = 2;
     }
     int64_t blocks = ((int64_t)a.T + kWarps - 1) / kWarps;
-    if (blocks > (int64_t)a.sms * 8) blocks = (int64_t)a.sms * 8;
+    if (blocks > (int64_t)a.sms * 4) blocks = (int64_t)a.sms * 4;
     const dim3 grid((unsigned)blocks);
-    const size_t smem = (size_t)a.N * 2 * 4;
+    const size_t smem = (size_t)a.N * 2 * 4 * (p.parts > 0 ? 9 : 1);
     const int nv = (a.N + 31) / 32;
     return nv <= 1 ? launch_pdl(gate_grad_kernel<1>, grid, dim3(kThreads), smem, st, p)
          : nv <= 2 ? launch_pdl(gate_grad_kernel<2>, grid, dim3(kThreads), smem, st, p)

@@ -52,103 +52,117 @@ __device__ __forceinline__ typename VecOf<VB>::T from_floats(const float* f) {
 }
 
 // ---------------------------------------------------------------- dispatch
-// The slots of one chunk of tokens are counted per expert (dispatch_count:
-// one block per chunk), then every block of dispatch_move ranks the slots of
-// its chunk again, which costs it a few thousand cycles and spares a third
-// launch and a round trip of the positions through memory, and moves its
-// share of the chunk's rows: each row of x is read once and written to the
-// places of its k slots.  A batch of one chunk needs no counting launch.
+// One launch sorts and moves.  The slots form chunks of at most a block's
+// threads (whole tokens); a block ranks the slots of its chunk, a slot a
+// thread, and moves its share of the chunk's rows: each row of x is read once
+// and written to the places of its k slots.  What comes before the chunk the
+// block counts by itself (kDispAlone slots: 16 indices a thread); longer
+// batches have a counting launch first (65536 slots: 32 us against 45 when
+// every block counted half of them).
+// Ranking is repeated by the blocks that share a chunk, so those are few and
+// large: with 256-thread blocks, eight to an SM, 777 tokens of 1763 values
+// took 18 us, with 1024-thread blocks 12.
+// Bound: HBM writes.  4096 tokens of 3584 bf16 values, 8 slots each: 50 us for
+// 265 MB, 0.78 of the measured copy bandwidth.
 struct DispatchParams {
     const char* x; int64_t ldx;
     const int32_t* idx;
-    int T, N, k, capacity, chunk_tokens, shares, n_chunks;
+    int T, N, k, capacity, chunk_tokens, shares;
     int64_t row_bytes;
     char* xp; int32_t *offsets, *perm, *inv;
-    int32_t* counts;
+    int32_t* counts;  // [spans][N + 1], where there is more than one
+    int spans, span_tokens;
     DevError* err;
 };
 
-__device__ __forceinline__ int dispatch_key(const DispatchParams& p, int64_t slot, bool report) {
+__device__ __forceinline__ int dispatch_key(const DispatchParams& p, int64_t slot) {
     const int e = p.idx[slot];
-    if (e >= p.N) {
-        if (report) set_error(p.err, MOE_ERR_DEVICE_INDEX, (int)slot);
-        return p.N;
-    }
-    return e < 0 ? p.N : e;
+    return (unsigned)e < (unsigned)p.N ? e : p.N;
 }
 
-__global__ void __launch_bounds__(kThreads) dispatch_count_kernel(const DispatchParams p) {
+__global__ void __launch_bounds__(1024) dispatch_count_kernel(const DispatchParams p) {
     extern __shared__ int hist[];
-    for (int i = threadIdx.x; i <= p.N; i += kThreads) hist[i] = 0;
+    for (int i = threadIdx.x; i <= p.N; i += blockDim.x) hist[i] = 0;
     __syncthreads();
     grid_dep_wait();
-    const int64_t s0 = (int64_t)blockIdx.x * p.chunk_tokens * p.k;
-    const int64_t s1 = min(s0 + (int64_t)p.chunk_tokens * p.k, (int64_t)p.T * p.k);
-    for (int64_t s = s0 + threadIdx.x; s < s1; s += kThreads) atomicAdd(&hist[dispatch_key(p, s, false)], 1);
+    const int64_t s0 = (int64_t)blockIdx.x * p.span_tokens * p.k;
+    const int64_t s1 = min(s0 + (int64_t)p.span_tokens * p.k, (int64_t)p.T * p.k);
+    for (int64_t s = s0 + threadIdx.x; s < s1; s += blockDim.x) atomicAdd(&hist[dispatch_key(p, s)], 1);
     __syncthreads();
-    for (int i = threadIdx.x; i <= p.N; i += kThreads) p.counts[(size_t)blockIdx.x * (p.N + 1) + i] = hist[i];
+    for (int i = threadIdx.x; i <= p.N; i += blockDim.x) p.counts[(size_t)blockIdx.x * (p.N + 1) + i] = hist[i];
     grid_dep_launch();
 }
 
-template <int VB>
-__global__ void __launch_bounds__(kThreads) dispatch_move_kernel(const DispatchParams p) {
+// vectors of a row that a lane moves at a time: more in long batches, whose
+// items are plenty
+__host__ __device__ constexpr int dispatch_vectors(int vb, int threads) { return vb < 16 || threads == 1024 ? 4 : 2; }
+
+template <int VB, int THREADS>
+__global__ void __launch_bounds__(THREADS) dispatch_move_kernel(const DispatchParams p) {
     using V = typename VecOf<VB>::T;
+    constexpr int kW = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int NK = p.N + 1;  // keys: the experts, then "no expert"
     extern __shared__ int sm[];
-    int* cnt = sm;                    // [kWarps][NK] slots of a warp per key, then those before it
-    int* tot = cnt + kWarps * NK;     // [NK] slots of the whole batch per key
+    int* tot = sm;                    // [NK] slots of the whole batch per key
     int* before = tot + NK;           // [NK] slots of earlier chunks per key
     int* off = before + NK;           // [NK] first row of each expert
-    int* pos_s = off + NK;            // [slots of a chunk]
-    __shared__ int wdrop[kWarps], s_kept, s_drop_before;
+    int* pos_s = off + NK;            // [THREADS]
+    uint16_t* cnt = reinterpret_cast<uint16_t*>(pos_s + THREADS);  // [kW][NK] slots of a warp per key, then those before it
+    __shared__ int wdrop[kW], s_kept, s_drop_before;
 
     const int chunk = blockIdx.x / p.shares, share = blockIdx.x % p.shares;
     const int t0 = chunk * p.chunk_tokens;
     const int n_tok = min(p.chunk_tokens, p.T - t0);
-    const int n = n_tok * p.k;
+    const int n = n_tok * p.k;  // at most THREADS
     const int64_t slot0 = (int64_t)t0 * p.k;
-    for (int i = tid; i < kWarps * NK + 2 * NK; i += kThreads) sm[i] = 0;
+    for (int i = tid; i < 2 * NK; i += THREADS) sm[i] = 0;
+    for (int i = tid; i < kW * NK; i += THREADS) cnt[i] = 0;
     __syncthreads();
     grid_dep_wait();
-    // rank among the warp's slots of the same key; a warp owns a run of slots
-    const int run = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;
-    const int r0 = min(warp * run, n), r1 = min(r0 + run, n);
-    for (int b = r0; b < r1; b += 32) {
-        const int i = b + lane;
-        const int key = i < r1 ? dispatch_key(p, slot0 + i, share == 0) : -1;
-        const uint32_t peers = __match_any_sync(0xffffffffu, key);
-        const int ahead = __popc(peers & ((1u << lane) - 1u));
-        const int seen = key >= 0 ? cnt[warp * NK + key] : 0;
-        __syncwarp();
-        if (key >= 0 && ahead == 0) cnt[warp * NK + key] = seen + __popc(peers);
-        __syncwarp();
-        if (key >= 0) pos_s[i] = (key << 16) | (seen + ahead);
+    // this thread's slot, and its rank among the warp's slots of the same key
+    int key = -1;
+    if (tid < n) {
+        key = p.idx[slot0 + tid];
+        if (key >= p.N && share == 0) set_error(p.err, MOE_ERR_DEVICE_INDEX, (int)(slot0 + tid));
+        if ((unsigned)key >= (unsigned)p.N) key = p.N;
     }
-    if (p.n_chunks > 1) {
-        const int n_cnt = p.n_chunks * NK;
-        for (int i = tid; i < n_cnt; i += kThreads) {
+    const uint32_t peers = __match_any_sync(0xffffffffu, key);
+    const int rank = __popc(peers & ((1u << lane) - 1u));
+    if (key >= 0 && rank == 0) cnt[warp * NK + key] = (uint16_t)__popc(peers);
+    // the slots of the batch and those before the chunk: spans that were
+    // counted, the rest one by one (consecutive lanes take consecutive slots:
+    // a token's experts differ, so few of them meet at one counter)
+    const int span = p.spans > 1 ? t0 / p.span_tokens : 0;
+    const int64_t all = p.spans > 1 ? slot0 : (int64_t)p.T * p.k;
+#pragma unroll 8
+    for (int64_t s = (int64_t)span * p.span_tokens * p.k + tid; s < all; s += THREADS) {
+        const int e = dispatch_key(p, s);
+        if (p.spans == 1) atomicAdd(&tot[e], 1);
+        if (s < slot0) atomicAdd(&before[e], 1);
+    }
+    if (p.spans > 1) {
+        const int n_cnt = p.spans * NK;
+        for (int i = tid; i < n_cnt; i += THREADS) {
             const int v = __ldcg(p.counts + i);
             const int c = i / NK, e = i - c * NK;
             if (v) {
                 atomicAdd(&tot[e], v);
-                if (c < chunk) atomicAdd(&before[e], v);
+                if (c < span) atomicAdd(&before[e], v);
             }
         }
     }
     __syncthreads();
-    for (int e = tid; e < NK; e += kThreads) {
-        int sum = before[e];
-        for (int w = 0; w < kWarps; ++w) {
+    for (int e = tid; e < NK; e += THREADS) {
+        int sum = 0;
+        for (int w = 0; w < kW; ++w) {
             const int v = cnt[w * NK + e];
-            cnt[w * NK + e] = sum;
+            cnt[w * NK + e] = (uint16_t)sum;
             sum += v;
         }
-        if (p.n_chunks == 1) tot[e] = sum;
     }
-    __syncthreads();
     const int cap = p.capacity > 0 ? p.capacity : 0x7fffffff;
-    if (warp == 0) {  // first rows: exclusive scan of the kept slots
+    if (warp == kW - 1) {  // first rows: exclusive scan of the kept slots
         int carry = 0, over = 0;
         for (int b = 0; b < p.N; b += 32) {
             const int e = b + lane;
@@ -168,40 +182,33 @@ __global__ void __launch_bounds__(kThreads) dispatch_move_kernel(const DispatchP
         if (lane == 0) { off[p.N] = carry; s_kept = carry; s_drop_before = before[p.N] + over; }
     }
     __syncthreads();
-    int drops = 0;
-    for (int b = r0; b < r1; b += 32) {
-        const int i = b + lane;
-        bool drop = false;
-        if (i < r1) {
-            const int key = pos_s[i] >> 16, r = (pos_s[i] & 0xffff) + (key < p.N ? cnt[warp * NK + key] : 0);
-            drop = key == p.N || r >= cap;
-            if (!drop) pos_s[i] = off[key] + r;
-        }
-        const uint32_t m = __ballot_sync(0xffffffffu, drop);
-        if (drop) pos_s[i] = ~(drops + __popc(m & ((1u << lane) - 1u)));  // its number among the warp's
-        drops += __popc(m);
-    }
-    if (lane == 0) wdrop[warp] = drops;
+    const int r = key >= 0 && key < p.N ? before[key] + cnt[warp * NK + key] + rank : 0;
+    const bool drop = key == p.N || (key >= 0 && r >= cap);
+    const uint32_t dropped = __ballot_sync(0xffffffffu, drop);
+    if (lane == 0) wdrop[warp] = __popc(dropped);
     __syncthreads();
-    int drop0 = s_kept + s_drop_before;
-    for (int w = 0; w < warp; ++w) drop0 += wdrop[w];
-    for (int i = r0 + lane; i < r1; i += 32) {
-        if (pos_s[i] < 0) pos_s[i] = ~(drop0 + ~pos_s[i]);
+    if (tid < n) {
+        int q = off[key < p.N ? key : 0] + r;
+        if (drop) {
+            int d0 = s_kept + s_drop_before + __popc(dropped & ((1u << lane) - 1u));
+            for (int w = 0; w < warp; ++w) d0 += wdrop[w];
+            q = ~d0;
+        }
+        pos_s[tid] = q;
         if (share == 0) {
-            const int q = pos_s[i];
-            p.inv[slot0 + i] = q < 0 ? q - 1 : q;  // ~row - 1 = -2 - row
-            p.perm[q < 0 ? ~q : q] = q < 0 ? -1 : (int)(slot0 + i);
+            p.inv[slot0 + tid] = q < 0 ? q - 1 : q;  // ~row - 1 = -2 - row
+            p.perm[q < 0 ? ~q : q] = q < 0 ? -1 : (int)(slot0 + tid);
         }
     }
     if (blockIdx.x == 0)
-        for (int e = tid; e <= p.N; e += kThreads) p.offsets[e] = off[e];
+        for (int e = tid; e <= p.N; e += THREADS) p.offsets[e] = off[e];
     __syncthreads();
     // an item: 32 x kU vectors of one token's row, read once, written k times
-    constexpr int kU = VB == 16 ? 2 : 4;
+    constexpr int kU = dispatch_vectors(VB, THREADS);
     const int n_vec = (int)(p.row_bytes / VB);
     const int pieces = (n_vec + 32 * kU - 1) / (32 * kU);
     const int items = n_tok * pieces;
-    for (int it = share * kWarps + warp; it < items; it += p.shares * kWarps) {
+    for (int it = share * kW + warp; it < items; it += p.shares * kW) {
         const int t = it / pieces, v0 = (it - t * pieces) * 32 * kU + lane;
         const V* src = reinterpret_cast<const V*>(p.x + (int64_t)(t0 + t) * p.ldx);
         V v[kU];
@@ -222,7 +229,9 @@ __global__ void __launch_bounds__(kThreads) dispatch_move_kernel(const DispatchP
 // ---------------------------------------------------------------- combine
 // out[t] = add[t] + sum_s gate[t,s] y[inv[t,s]].  A warp takes `m` x 32
 // vectors of one token's row; the rows of up to eight slots are loaded before
-// any is used.  Slots are added in slot order, add last, in fp32.
+// any is used.  Slots are added in slot order, add last, in fp32.  Bound: HBM
+// reads; 4096 tokens of 3584 bf16 values, 8 slots each: 52 us for 294 MB, 0.84
+// of the measured copy bandwidth.
 struct CombineParams {
     const char* y; const float* gate; const int32_t* inv;
     const char* add; int64_t ldadd; char* out; int64_t ldout;  // bytes
@@ -294,8 +303,9 @@ __global__ void __launch_bounds__(kThreads) combine_rows_kernel(const CombinePar
 // One block per token: dout's row is read once, every slot's y row is read
 // (for dgate) and its dy row written in the same pass.  The k dot products
 // are summed per thread, then over the warp, then over the warps, in fixed
-// order.
-constexpr int kGradThreads = 128, kGradWarps = kGradThreads / 32;
+// order.  Bound: HBM; 4096 tokens of 3584 bf16 values, 8 slots each: 77 us for
+// 500 MB, 0.95 of the measured copy bandwidth.
+constexpr int kGradMaxThreads = 512, kGradWarps = kGradMaxThreads / 32;
 
 struct CombineGradParams {
     const char* dout; int64_t lddout; const char* y; const float* gate; const int32_t* inv;
@@ -305,7 +315,7 @@ struct CombineGradParams {
 };
 
 template <typename W, int VB, int KB>
-__global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(const CombineGradParams p) {
+__global__ void __launch_bounds__(VB == 16 ? 128 : kGradMaxThreads) combine_grad_kernel(const CombineGradParams p) {
     using V = typename VecOf<VB>::T;
     constexpr int kE = VB / (int)sizeof(W);
     __shared__ float part[kGradWarps][KB];
@@ -325,7 +335,7 @@ __global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(const Combin
     float dot[KB];
 #pragma unroll
     for (int s = 0; s < KB; ++s) dot[s] = 0.f;
-    for (int vi = tid; vi < n_vec; vi += kGradThreads) {
+    for (int vi = tid; vi < n_vec; vi += blockDim.x) {
         float g[kE];
         to_floats<W, VB>(reinterpret_cast<const V*>(p.dout + t * p.lddout)[vi], g);
 #pragma unroll
@@ -366,8 +376,7 @@ __global__ void __launch_bounds__(kGradThreads) combine_grad_kernel(const Combin
         __syncthreads();
         if (tid < p.k) {
             float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < kGradWarps; ++w) v += part[w][tid];
+            for (int w = 0; w < (int)blockDim.x / 32; ++w) v += part[w][tid];
             p.dgate[t * p.k + tid] = row_s[tid] >= 0 ? v : 0.f;
         }
     }
@@ -384,33 +393,44 @@ int64_t at(const void* p) { return (int64_t)reinterpret_cast<uintptr_t>(p); }
 
 }  // namespace
 
+template <int THREADS>
+static cudaError_t launch_move(const DispatchParams& p, int vb, int blocks, cudaStream_t st) {
+    const size_t smem = (size_t)(3 * (p.N + 1) + THREADS) * 4 + (size_t)THREADS / 32 * (p.N + 1) * 2;
+    const dim3 grid((unsigned)blocks), block(THREADS);
+    return vb == 16 ? launch_pdl(dispatch_move_kernel<16, THREADS>, grid, block, smem, st, p)
+         : vb == 4  ? launch_pdl(dispatch_move_kernel<4, THREADS>, grid, block, smem, st, p)
+                    : launch_pdl(dispatch_move_kernel<2, THREADS>, grid, block, smem, st, p);
+}
+
 cudaError_t launch_dispatch_rows(const DispatchArgs& a, cudaStream_t st, int* launches) {
     DispatchParams p;
     p.x = static_cast<const char*>(a.x); p.ldx = a.ldx_bytes; p.idx = a.idx;
     p.T = a.T; p.N = a.N; p.k = a.k; p.capacity = a.capacity;
-    p.chunk_tokens = dispatch_chunk_tokens(a.T, a.k);
-    p.n_chunks = dispatch_chunks(a.T, a.k);
     p.row_bytes = a.row_bytes; p.xp = static_cast<char*>(a.x_perm);
     p.offsets = a.offsets; p.perm = a.perm; p.inv = a.inv; p.counts = a.counts; p.err = a.err;
+    p.spans = dispatch_spans(a.T, a.k);
+    p.span_tokens = dispatch_span_tokens(a.T, a.k);
+    // a small batch: small blocks, which start sooner and synchronise faster
+    const int64_t slots = (int64_t)a.T * a.k;
+    const int threads = slots <= 256 ? 256 : slots <= 4096 ? 512 : 1024, warps = threads / 32;
+    p.chunk_tokens = threads / a.k < a.T ? threads / a.k : a.T;
+    const int chunks = (a.T + p.chunk_tokens - 1) / p.chunk_tokens;
     const int vb = vec_bytes(a.row_bytes, {at(a.x), at(a.x_perm), a.ldx_bytes});
-    // blocks: enough for every row piece to have a warp, at most one wave
-    const int piece = 32 * (vb == 16 ? 2 : 4) * vb;
+    // blocks: a warp for every row piece, at most one wave
+    const int piece = 32 * dispatch_vectors(vb, threads) * vb;
     const int64_t items = (int64_t)p.chunk_tokens * ((a.row_bytes + piece - 1) / piece);
-    int64_t shares = (items + kWarps - 1) / kWarps;
-    const int64_t wave = ((int64_t)a.sms * 8 + p.n_chunks - 1) / p.n_chunks;
-    p.shares = (int)(shares < wave ? shares : wave);
+    const int64_t need = (items + warps - 1) / warps, wave = (int64_t)a.sms * (2048 / threads) / chunks;
+    p.shares = (int)(need < wave ? need : wave);
     if (p.shares < 1) p.shares = 1;
     *launches = 1;
-    if (p.n_chunks > 1) {
-        cudaError_t e = launch_pdl(dispatch_count_kernel, dim3(p.n_chunks), dim3(kThreads), (size_t)(a.N + 1) * 4, st, p);
+    if (p.spans > 1) {
+        const cudaError_t e = launch_pdl(dispatch_count_kernel, dim3(p.spans), dim3(1024), (size_t)(a.N + 1) * 4, st, p);
         if (e != cudaSuccess) return e;
         *launches = 2;
     }
-    const size_t smem = ((size_t)(kWarps + 3) * (a.N + 1) + (size_t)p.chunk_tokens * a.k) * 4;
-    const dim3 grid((unsigned)(p.n_chunks * p.shares));
-    return vb == 16 ? launch_pdl(dispatch_move_kernel<16>, grid, dim3(kThreads), smem, st, p)
-         : vb == 4  ? launch_pdl(dispatch_move_kernel<4>, grid, dim3(kThreads), smem, st, p)
-                    : launch_pdl(dispatch_move_kernel<2>, grid, dim3(kThreads), smem, st, p);
+    return threads == 256 ? launch_move<256>(p, vb, chunks * p.shares, st)
+         : threads == 512 ? launch_move<512>(p, vb, chunks * p.shares, st)
+                          : launch_move<1024>(p, vb, chunks * p.shares, st);
 }
 
 cudaError_t launch_combine_rows(const CombineRowsArgs& a, cudaStream_t st) {
@@ -439,8 +459,12 @@ cudaError_t launch_combine_rows(const CombineRowsArgs& a, cudaStream_t st) {
 
 template <typename W, int VB>
 static cudaError_t launch_grad(const CombineGradParams& p, int T, cudaStream_t st) {
-    return p.k <= 8 ? launch_pdl(combine_grad_kernel<W, VB, 8>, dim3(T), dim3(kGradThreads), 0, st, p)
-                    : launch_pdl(combine_grad_kernel<W, VB, 16>, dim3(T), dim3(kGradThreads), 0, st, p);
+    // small vectors: more threads to a row, a few vectors each
+    int threads = 128;
+    if (VB < 16)
+        while (threads < kGradMaxThreads && p.row_bytes / VB > 4 * threads) threads *= 2;
+    return p.k <= 8 ? launch_pdl(combine_grad_kernel<W, VB, 8>, dim3(T), dim3(threads), 0, st, p)
+                    : launch_pdl(combine_grad_kernel<W, VB, 16>, dim3(T), dim3(threads), 0, st, p);
 }
 
 cudaError_t launch_combine_rows_grad(const CombineRowsGradArgs& a, cudaStream_t st) {
