@@ -79,7 +79,8 @@ enum TrainForm {
     kFormDown = 1,  // y = h Wd
     kFormDh = 2,    // dg, du from dy (through SwiGLU)
     kFormDx = 3,    // dx = dg Wg + du Wu
-    kFormDw = 4     // dW = a^T b per expert, one or two a
+    kFormDw = 4,    // dW = a^T b per expert, one or two a
+    kFormNone = 5
 };
 struct GroupedArgs {
     TrainForm form;
@@ -97,9 +98,11 @@ struct GroupedArgs {
 bool grouped_tc_shapes(bool bf16, int d, int I);
 bool grouped_tc_usable(const GroupedArgs& a);
 cudaError_t launch_grouped_simt(const GroupedArgs& a, cudaStream_t st);
-// tensor cores: the forms that give rows (one launch), and Dw (two)
-cudaError_t launch_grouped_rows_tc(const GroupedArgs& a, cudaStream_t st);
-cudaError_t launch_grouped_dw_tc(const GroupedArgs& a, cudaStream_t st);
+// tensor cores: the forms that give rows (dw, or NULL: the weight-gradient
+// product that follows, whose tensor maps this launch makes on the side), and
+// Dw (one launch, or two without such maps)
+cudaError_t launch_grouped_rows_tc(const GroupedArgs& a, const GroupedArgs* dw, cudaStream_t st);
+cudaError_t launch_grouped_dw_tc(const GroupedArgs& a, bool have_maps, cudaStream_t st);
 // clusters of `size` CTAs of a kernel that can be resident at once
 cudaError_t resident_clusters(const void* kernel, int size, int threads, uint32_t smem, int sms, int* clusters);
 

@@ -85,13 +85,21 @@ GroupedArgs grouped(const moe_dims* D, TrainForm form, const int32_t* offsets, v
     return a;
 }
 
-moe_status run_grouped(const GroupedArgs& a, void* stream, const char* what) {
-    const bool tc = grouped_tc_usable(a), dw = a.form == kFormDw;
-    const cudaError_t e = !tc  ? launch_grouped_simt(a, S(stream))
-                          : dw ? launch_grouped_dw_tc(a, S(stream))
-                               : launch_grouped_rows_tc(a, S(stream));
+moe_status run_grouped(const GroupedArgs& a, const GroupedArgs* dw, void* stream, const char* what) {
+    // the row product of a gradient call, then its weight product, either of them optional (form = kFormNone)
+    const bool rows = a.form != kFormNone, rows_tc = rows && grouped_tc_usable(a), dw_tc = dw && grouped_tc_usable(*dw);
+    cudaError_t e = cudaSuccess;
+    int launches = 0;
+    if (rows) {
+        e = rows_tc ? launch_grouped_rows_tc(a, dw_tc ? dw : nullptr, S(stream)) : launch_grouped_simt(a, S(stream));
+        ++launches;
+    }
+    if (e == cudaSuccess && dw) {
+        e = dw_tc ? launch_grouped_dw_tc(*dw, rows_tc, S(stream)) : launch_grouped_simt(*dw, S(stream));
+        launches += dw_tc && !rows_tc ? 2 : 1;
+    }
     if (e != cudaSuccess) return cuda_failed(e, what);
-    note_launches(tc && dw ? 2 : 1);
+    note_launches(launches);
     return MOE_OK;
 }
 
@@ -217,7 +225,7 @@ moe_status moe_experts_up(const moe_dims* dims, const void* x_perm, const int32_
     if (g) for (const void* p : {(const void*)g, (const void*)u}) TRAIN_TRY(check_rows(dims, p));
     GroupedArgs a = grouped(dims, kFormUp, expert_offsets, ws);
     a.a0 = x_perm; a.b0 = w_gate; a.b1 = w_up; a.o0 = g; a.o1 = u; a.o2 = h;
-    return run_grouped(a, stream, "moe_experts_up");
+    return run_grouped(a, nullptr, stream, "moe_experts_up");
 }
 
 moe_status moe_experts_down(const moe_dims* dims, const void* h, const int32_t* expert_offsets,
@@ -229,7 +237,7 @@ moe_status moe_experts_down(const moe_dims* dims, const void* h, const int32_t* 
     for (const void* p : {h, w_down, (const void*)y_perm}) TRAIN_TRY(check_rows(dims, p));
     GroupedArgs a = grouped(dims, kFormDown, expert_offsets, ws);
     a.a0 = h; a.b0 = w_down; a.o0 = y_perm;
-    return run_grouped(a, stream, "moe_experts_down");
+    return run_grouped(a, nullptr, stream, "moe_experts_down");
 }
 
 moe_status moe_experts_up_grad(const moe_dims* dims, const void* dg, const void* du, const void* x_perm,
@@ -247,18 +255,15 @@ moe_status moe_experts_up_grad(const moe_dims* dims, const void* dg, const void*
     }
     if (dx_perm && dims->T > 0)
         for (const void* p : {w_gate, w_up, (const void*)dx_perm}) TRAIN_TRY(check_rows(dims, p));
+    GroupedArgs a = grouped(dims, kFormNone, expert_offsets, ws), w = grouped(dims, kFormDw, expert_offsets, ws);
     if (dx_perm && dims->T > 0) {
-        GroupedArgs a = grouped(dims, kFormDx, expert_offsets, ws);
+        a.form = kFormDx;
         a.a0 = dg; a.a1 = du; a.b0 = w_gate; a.b1 = w_up; a.o0 = dx_perm;
-        TRAIN_TRY(run_grouped(a, stream, "moe_experts_up_grad (dx)"));
     }
-    if (dw_gate && !(accumulate && dims->T == 0)) {
-        GroupedArgs a = grouped(dims, kFormDw, expert_offsets, ws);
-        a.a0 = dg; a.a1 = du; a.b0 = x_perm; a.o0 = dw_gate; a.o1 = dw_up;
-        a.out_f32 = gtype == MOE_DTYPE_F32; a.accumulate = accumulate != 0;
-        TRAIN_TRY(run_grouped(a, stream, "moe_experts_up_grad (dw)"));
-    }
-    return MOE_OK;
+    w.a0 = dg; w.a1 = du; w.b0 = x_perm; w.o0 = dw_gate; w.o1 = dw_up;
+    w.out_f32 = gtype == MOE_DTYPE_F32; w.accumulate = accumulate != 0;
+    const bool want = dw_gate && !(accumulate && dims->T == 0);
+    return run_grouped(a, want ? &w : nullptr, stream, "moe_experts_up_grad");
 }
 
 moe_status moe_experts_down_grad(const moe_dims* dims, const void* dy_perm, const void* h, const void* g,
@@ -276,18 +281,15 @@ moe_status moe_experts_down_grad(const moe_dims* dims, const void* dy_perm, cons
     }
     if (dg && dims->T > 0)
         for (const void* p : {g, u, w_down, (const void*)dg, (const void*)du}) TRAIN_TRY(check_rows(dims, p));
+    GroupedArgs a = grouped(dims, kFormNone, expert_offsets, ws), w = grouped(dims, kFormDw, expert_offsets, ws);
     if (dg && dims->T > 0) {
-        GroupedArgs a = grouped(dims, kFormDh, expert_offsets, ws);
+        a.form = kFormDh;
         a.a0 = dy_perm; a.b0 = w_down; a.g = g; a.u = u; a.o0 = dg; a.o1 = du;
-        TRAIN_TRY(run_grouped(a, stream, "moe_experts_down_grad (dh)"));
     }
-    if (dw_down && !(accumulate && dims->T == 0)) {
-        GroupedArgs a = grouped(dims, kFormDw, expert_offsets, ws);
-        a.a0 = h; a.b0 = dy_perm; a.o0 = dw_down;
-        a.out_f32 = gtype == MOE_DTYPE_F32; a.accumulate = accumulate != 0;
-        TRAIN_TRY(run_grouped(a, stream, "moe_experts_down_grad (dw)"));
-    }
-    return MOE_OK;
+    w.a0 = h; w.b0 = dy_perm; w.o0 = dw_down;
+    w.out_f32 = gtype == MOE_DTYPE_F32; w.accumulate = accumulate != 0;
+    const bool want = dw_down && !(accumulate && dims->T == 0);
+    return run_grouped(a, want ? &w : nullptr, stream, "moe_experts_down_grad");
 }
 
 const char* moe_experts_path(const moe_dims* dims) {

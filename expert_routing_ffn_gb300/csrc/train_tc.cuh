@@ -265,5 +265,35 @@ __device__ __forceinline__ void map_acquire(const void* map) {
     asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
 }
 
+
+// The weight gradients' maps: an expert's rows of a0, a1 and b, made from the
+// maps of the whole tensors by one warp (expert_maps), in the workspace.
+constexpr int kMapsPerExpert = 3;
+struct MapParams {
+    CUtensorMap t[kMapsPerExpert];
+    const unsigned char* rows[kMapsPerExpert];  // the tensors
+    int64_t row_bytes[kMapsPerExpert];
+    unsigned char* maps;                        // [N][kMapsPerExpert] of 128 bytes; NULL: none to make
+    const int32_t* offsets;
+    int M, N;
+};
+__device__ __forceinline__ void expert_maps(const MapParams& p, int e) {
+    const int lane = threadIdx.x & 31;
+    const int r0 = min(max(p.offsets[e], 0), p.M), rows = min(max(p.offsets[e + 1], 0), p.M) - r0;
+    if (rows <= 0) return;
+    for (int m = 0; m < kMapsPerExpert; ++m) {
+        unsigned char* out = p.maps + ((size_t)e * kMapsPerExpert + m) * 128;
+        reinterpret_cast<uint32_t*>(out)[lane] = reinterpret_cast<const uint32_t*>(&p.t[m])[lane];
+        __syncwarp();
+        if (lane == 0)
+            map_replace(out, reinterpret_cast<uint64_t>(p.rows[m]) + (uint64_t)r0 * (uint64_t)p.row_bytes[m],
+                        (uint32_t)rows);
+    }
+    if (lane == 0) map_release();
+}
+
 }  // namespace train
+
+// train_tc_dw.cu: the maps' templates for a weight-gradient product
+bool dw_map_params(const struct GroupedArgs& a, train::MapParams& mp);
 }  // namespace moe

@@ -45,7 +45,6 @@ constexpr int kBoxesPerWarp = 2;
 constexpr uint32_t kBK = kTcBK;
 constexpr uint32_t kStageA = kStrip * kBK * 2, kStageB = kBN / 2 * kBK * 2, kStage = kStageA + kStageB;
 constexpr uint32_t kBox = 32 * 128;          // 32 channels x 128 bytes
-constexpr int kMapsPerExpert = 3;            // a0, a1, b
 constexpr int kS = 5;                        // stages
 constexpr uint32_t kBoxes = kS * kStage, kTable = kBoxes + kEpiWarps * kBoxesPerWarp * kBox;  // table: rank -> expert
 constexpr uint32_t kBars = kTable + kTrainMaxExperts * 4 + 16;
@@ -345,34 +344,11 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
 }
 
 // ---------------------------------------------------------------- per-expert maps
-// Expert e's rows of a0, a1 and b as tensor maps of their own, made from the
-// maps of the whole tensors.  A warp per expert.
-struct MapParams {
-    CUtensorMap t[kMapsPerExpert];
-    const unsigned char* rows[kMapsPerExpert];  // the tensors
-    int64_t row_bytes[kMapsPerExpert];
-    unsigned char* maps;
-    const int32_t* offsets;
-    int M, N;
-};
-
+// By a launch of its own where no other kernel of the call has made them.
 __global__ void __launch_bounds__(128) expert_maps_kernel(const __grid_constant__ MapParams p) {
     grid_dep_wait();
-    const int e = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (e < p.N) {
-        const int r0 = min(max(p.offsets[e], 0), p.M), rows = min(max(p.offsets[e + 1], 0), p.M) - r0;
-        if (rows > 0) {
-            for (int m = 0; m < kMapsPerExpert; ++m) {
-                unsigned char* out = p.maps + ((size_t)e * kMapsPerExpert + m) * 128;
-                reinterpret_cast<uint32_t*>(out)[lane] = reinterpret_cast<const uint32_t*>(&p.t[m])[lane];
-                __syncwarp();
-                if (lane == 0)
-                    map_replace(out, reinterpret_cast<uint64_t>(p.rows[m]) + (uint64_t)r0 * (uint64_t)p.row_bytes[m],
-                                (uint32_t)rows);
-            }
-            if (lane == 0) map_release();
-        }
-    }
+    const int e = blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (e < p.N) expert_maps(p, e);
     grid_dep_launch();
 }
 
@@ -394,31 +370,37 @@ cudaError_t launch_dw(const DwParams& p, int sms, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_grouped_dw_tc(const GroupedArgs& a, cudaStream_t st) {
+bool dw_map_params(const GroupedArgs& a, MapParams& mp) {
+    const void* rows[kMapsPerExpert] = {a.a0, a.a1 ? a.a1 : a.a0, a.b0};
+    std::memset(&mp, 0, sizeof(mp));
+    for (int i = 0; i < kMapsPerExpert; ++i) {
+        const uint64_t cols = (uint64_t)(i < 2 ? a.I : a.d);
+        if (encode_bf16_2d(&mp.t[i], rows[i], cols, (uint64_t)a.M, cols * 2, 64, kBK) != MOE_OK) return false;
+        mp.rows[i] = static_cast<const unsigned char*>(rows[i]);
+        mp.row_bytes[i] = (int64_t)cols * 2;
+    }
+    mp.maps = a.maps; mp.offsets = a.offsets; mp.M = a.M; mp.N = a.N;
+    return true;
+}
+
+cudaError_t launch_grouped_dw_tc(const GroupedArgs& a, bool have_maps, cudaStream_t st) {
     DwParams p;
     std::memset(&p, 0, sizeof(p));
     p.maps = a.maps; p.offsets = a.offsets; p.err = a.err;
     p.M = a.M; p.N = a.N; p.d = a.d; p.I = a.I;
     p.n_mat = a.o1 ? 2 : 1;
     p.accumulate = a.accumulate;
-    const uint64_t d = (uint64_t)a.d, I = (uint64_t)a.I, M = (uint64_t)a.M;
-    MapParams mp;
-    std::memset(&mp, 0, sizeof(mp));
-    const void* rows[kMapsPerExpert] = {a.a0, a.a1 ? a.a1 : a.a0, a.b0};
-    for (int i = 0; i < kMapsPerExpert; ++i) {
-        const uint64_t cols = i < 2 ? I : d;
-        if (encode_bf16_2d(&mp.t[i], rows[i], cols, M, cols * 2, 64, kBK) != MOE_OK) return cudaErrorInvalidValue;
-        mp.rows[i] = static_cast<const unsigned char*>(rows[i]);
-        mp.row_bytes[i] = (int64_t)cols * 2;
-    }
-    mp.maps = a.maps; mp.offsets = a.offsets; mp.M = a.M; mp.N = a.N;
     p.out[0] = static_cast<unsigned char*>(a.o0);
     p.out[1] = static_cast<unsigned char*>(a.o1);
     for (int i = 0; i < p.n_mat; ++i)
-        if (encode_3d(&p.o[i], !a.out_f32, i ? a.o1 : a.o0, d, I, (uint64_t)a.N, a.out_f32 ? 32 : 64, 32) != MOE_OK)
+        if (encode_3d(&p.o[i], !a.out_f32, p.out[i], (uint64_t)a.d, (uint64_t)a.I, (uint64_t)a.N, a.out_f32 ? 32 : 64, 32) != MOE_OK)
             return cudaErrorInvalidValue;
-    cudaError_t e = launch_pdl(expert_maps_kernel, dim3((a.N + 3) / 4), dim3(128), 0, st, mp);
-    if (e != cudaSuccess) return e;
+    if (!have_maps) {
+        MapParams mp;
+        if (!dw_map_params(a, mp)) return cudaErrorInvalidValue;
+        const cudaError_t e = launch_pdl(expert_maps_kernel, dim3((a.N + 3) / 4), dim3(128), 0, st, mp);
+        if (e != cudaSuccess) return e;
+    }
     return a.out_f32 ? launch_dw<true>(p, a.sms, st) : launch_dw<false>(p, a.sms, st);
 }
 

@@ -85,6 +85,7 @@ struct RowsParams {
     const int32_t* offsets;
     int M, N, d, I;
     DevError* err;
+    MapParams dw;             // the maps of the weight gradients that follow this kernel
 };
 
 // 1 / (1 + e^-g) with the fast exponential and division (a few ulp in fp32;
@@ -208,6 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
         if (lane == 0) first[p.N] = carry;
     }
     if (warp == 1) tmem_alloc<true>(tmem_s);
+    if (p.dw.maps && warp >= 2)
+        for (int e = (int)blockIdx.x * 8 + warp - 2; e < p.N; e += (int)gridDim.x * 8) expert_maps(p.dw, e);
     {  // rows of no expert
         const int64_t v0 = (int64_t)row_at(p.N) * n_cols / 8, v1 = (int64_t)p.M * n_cols / 8;
         for (int64_t v = v0 + (int64_t)blockIdx.x * kThreads + tid; v < v1; v += (int64_t)gridDim.x * kThreads)
@@ -561,7 +564,7 @@ cudaError_t resident_clusters(const void* kernel, int size, int threads, uint32_
     return cudaSuccess;
 }
 
-cudaError_t launch_grouped_rows_tc(const GroupedArgs& a, cudaStream_t st) {
+cudaError_t launch_grouped_rows_tc(const GroupedArgs& a, const GroupedArgs* dw, cudaStream_t st) {
     RowsParams p;
     std::memset(&p, 0, sizeof(p));
     p.offsets = a.offsets; p.err = a.err;
@@ -597,6 +600,7 @@ cudaError_t launch_grouped_rows_tc(const GroupedArgs& a, cudaStream_t st) {
         p.out[i] = static_cast<__nv_bfloat16*>(outs[i]);
         if (outs[i]) rows_map(&p.o[i], outs[i], cols, kPanel);
     }
+    if (dw) ok = ok && dw_map_params(*dw, p.dw);
     if (!ok) return cudaErrorInvalidValue;
     const int64_t col_tiles = ((int64_t)cols + span - 1) / span;
     // an upper bound of the tiles, each cut into up to eight parts where there are few
