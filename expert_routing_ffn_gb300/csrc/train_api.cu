@@ -1,6 +1,7 @@
 // C ABI of the training step (include/moe_train.h): argument checks,
 // workspace layout and the launches of each call.
 #include <cmath>
+#include <initializer_list>
 
 #include "common.cuh"
 #include "train.h"
@@ -69,6 +70,14 @@ size_t elem(const moe_dims* D) { return D->wtype == MOE_DTYPE_BF16 ? 2 : 4; }
 moe_status check_rows(const moe_dims* D, const void* p) {
     return p && aligned(p, elem(D)) ? MOE_OK : MOE_ERR_INVALID_ARG;
 }
+// indices and float32 values: present, or NULL where that is allowed, and aligned
+bool words(std::initializer_list<const void*> needed, std::initializer_list<const void*> optional = {}) {
+    for (const void* p : needed)
+        if (!p || !aligned(p, 4)) return false;
+    for (const void* p : optional)
+        if (!aligned(p, 4)) return false;
+    return true;
+}
 moe_status check_stride(const moe_dims* D, int64_t* ld) {
     if (*ld == 0) *ld = D->d;
     return *ld < D->d || *ld > ((int64_t)1 << 40) ? MOE_ERR_INVALID_ARG : MOE_OK;
@@ -130,14 +139,14 @@ moe_status moe_dispatch_rows(const moe_dims* dims, const void* x, int64_t ldx, c
     TRAIN_TRY(check_dims(dims));
     TRAIN_TRY(check_ws(dims, ws, ws_bytes));
     TRAIN_TRY(check_stride(dims, &ldx));
-    if (capacity < 0 || !expert_offsets) return MOE_ERR_INVALID_ARG;
+    if (capacity < 0 || !words({expert_offsets})) return MOE_ERR_INVALID_ARG;
     if (dims->T == 0) {
         TRAIN_CUDA(cudaMemsetAsync(expert_offsets, 0, (size_t)(dims->N + 1) * 4, S(stream)));
         return MOE_OK;
     }
     TRAIN_TRY(check_rows(dims, x));
     TRAIN_TRY(check_rows(dims, x_perm));
-    if (!expert_idx || !perm || !inv_perm) return MOE_ERR_INVALID_ARG;
+    if (!words({expert_idx, perm, inv_perm})) return MOE_ERR_INVALID_ARG;
     DispatchArgs a;
     const int64_t es = (int64_t)elem(dims);
     a.x = x; a.ldx_bytes = ldx * es; a.idx = expert_idx;
@@ -161,7 +170,7 @@ moe_status moe_combine_rows(const moe_dims* dims, const void* y_perm, const floa
     if (dims->T == 0) return MOE_OK;
     TRAIN_TRY(check_rows(dims, y_perm));
     TRAIN_TRY(check_rows(dims, out));
-    if (!inv_perm || (add && !aligned(add, elem(dims)))) return MOE_ERR_INVALID_ARG;
+    if (!words({inv_perm}, {gate}) || !aligned(add, elem(dims))) return MOE_ERR_INVALID_ARG;
     CombineRowsArgs a;
     a.y = y_perm; a.gate = gate; a.inv = inv_perm; a.add = add; a.ldadd = ldadd; a.out = out; a.ldout = ldout;
     a.T = dims->T; a.k = dims->k; a.d = dims->d; a.bf16 = dims->wtype == MOE_DTYPE_BF16; a.sms = device_sms();
@@ -183,7 +192,7 @@ moe_status moe_combine_rows_grad(const moe_dims* dims, const void* dout, int64_t
     if (dims->T == 0 || (!dy_perm && !dgate)) return MOE_OK;
     TRAIN_TRY(check_rows(dims, dout));
     if (dgate) TRAIN_TRY(check_rows(dims, y_perm));
-    if (!inv_perm || (dy_perm && !aligned(dy_perm, elem(dims)))) return MOE_ERR_INVALID_ARG;
+    if (!words({inv_perm}, {gate, dgate}) || !aligned(dy_perm, elem(dims))) return MOE_ERR_INVALID_ARG;
     CombineRowsGradArgs a;
     a.dout = dout; a.lddout = lddout; a.y = y_perm; a.gate = gate; a.inv = inv_perm; a.dy = dy_perm;
     a.dgate = dgate; a.T = dims->T; a.k = dims->k; a.d = dims->d; a.bf16 = dims->wtype == MOE_DTYPE_BF16;
@@ -198,11 +207,12 @@ moe_status moe_gate_grad(const moe_dims* dims, const float* router_prob, const i
     TRAIN_TRY(check_dims(dims));
     TRAIN_TRY(check_ws(dims, ws, ws_bytes));
     if (!(balance >= 0.f) || std::isinf(balance)) return MOE_ERR_INVALID_ARG;
+    if (!words({}, {balance_loss})) return MOE_ERR_INVALID_ARG;
     if (dims->T == 0) {
         if (balance_loss) TRAIN_CUDA(cudaMemsetAsync(balance_loss, 0, 4, S(stream)));
         return MOE_OK;
     }
-    if (!router_prob || !topk_idx || !dgate || !dlogits) return MOE_ERR_INVALID_ARG;
+    if (!words({router_prob, topk_idx, dgate, dlogits})) return MOE_ERR_INVALID_ARG;
     GateGradArgs a;
     a.prob = router_prob; a.idx = topk_idx; a.dgate = dgate;
     a.T = dims->T; a.N = dims->N; a.k = dims->k; a.renorm = dims->renorm_topk != 0; a.balance = balance;
@@ -220,7 +230,7 @@ moe_status moe_experts_up(const moe_dims* dims, const void* x_perm, const int32_
     TRAIN_TRY(check_dims(dims));
     TRAIN_TRY(check_ws(dims, ws, ws_bytes));
     if (dims->T == 0) return MOE_OK;
-    if (!expert_offsets || (g == nullptr) != (u == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!words({expert_offsets}) || (g == nullptr) != (u == nullptr)) return MOE_ERR_INVALID_ARG;
     for (const void* p : {x_perm, w_gate, w_up, (const void*)h}) TRAIN_TRY(check_rows(dims, p));
     if (g) for (const void* p : {(const void*)g, (const void*)u}) TRAIN_TRY(check_rows(dims, p));
     GroupedArgs a = grouped(dims, kFormUp, expert_offsets, ws);
@@ -233,7 +243,7 @@ moe_status moe_experts_down(const moe_dims* dims, const void* h, const int32_t* 
     TRAIN_TRY(check_dims(dims));
     TRAIN_TRY(check_ws(dims, ws, ws_bytes));
     if (dims->T == 0) return MOE_OK;
-    if (!expert_offsets) return MOE_ERR_INVALID_ARG;
+    if (!words({expert_offsets})) return MOE_ERR_INVALID_ARG;
     for (const void* p : {h, w_down, (const void*)y_perm}) TRAIN_TRY(check_rows(dims, p));
     GroupedArgs a = grouped(dims, kFormDown, expert_offsets, ws);
     a.a0 = h; a.b0 = w_down; a.o0 = y_perm;
@@ -247,7 +257,7 @@ moe_status moe_experts_up_grad(const moe_dims* dims, const void* dg, const void*
     TRAIN_TRY(check_dims(dims));
     TRAIN_TRY(check_ws(dims, ws, ws_bytes));
     TRAIN_TRY(check_grads(dims, gtype, accumulate));
-    if (!expert_offsets || (dw_gate == nullptr) != (dw_up == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!words({expert_offsets}) || (dw_gate == nullptr) != (dw_up == nullptr)) return MOE_ERR_INVALID_ARG;
     if (dims->T > 0) for (const void* p : {dg, du}) TRAIN_TRY(check_rows(dims, p));
     if (dw_gate) {
         for (const void* p : {(const void*)dw_gate, (const void*)dw_up}) TRAIN_TRY(check_grad_buffer(gtype, p));
@@ -273,7 +283,7 @@ moe_status moe_experts_down_grad(const moe_dims* dims, const void* dy_perm, cons
     TRAIN_TRY(check_dims(dims));
     TRAIN_TRY(check_ws(dims, ws, ws_bytes));
     TRAIN_TRY(check_grads(dims, gtype, accumulate));
-    if (!expert_offsets || (dg == nullptr) != (du == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!words({expert_offsets}) || (dg == nullptr) != (du == nullptr)) return MOE_ERR_INVALID_ARG;
     if (dims->T > 0) TRAIN_TRY(check_rows(dims, dy_perm));
     if (dw_down) {
         TRAIN_TRY(check_grad_buffer(gtype, dw_down));

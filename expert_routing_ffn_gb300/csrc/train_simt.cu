@@ -12,7 +12,10 @@
 // puts the 16-byte reads of eight lanes on different banks.
 //
 // Bound: FMA rate.  The 16-row tiles serve segments that average so few rows
-// that most of a 64-row tile would be padding.  Tiles are numbered expert by
+// that most of a 64-row tile would be padding.  Measured, fp32: 128 rows an
+// expert at d = I = 1024, 16 experts, Up: 304 us, 28 TFLOP/s (ragged rows fill
+// 0.8 of the tiles, the tiles 0.7 of three rounds); 16 tokens of the tiny
+// layer: 11 us.  Tiles are numbered expert by
 // expert; every block forms the prefix sums of the tile counts itself.
 #include <cuda_bf16.h>
 

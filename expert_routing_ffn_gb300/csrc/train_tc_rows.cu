@@ -9,9 +9,9 @@
 // The weights are the MMA's M side and the rows its N side: a tile is 256
 // weight rows (or columns) on a CTA pair (2-CTA MMA, 128 accumulator lanes in
 // each CTA) x up to 256 grouped rows.  N goes in steps of 32, so a segment's
-// rows are split into equal tiles and a ragged end costs at most 31 rows,
-// where rows on the M side cost up to 255: 384 rows an expert took 2 tiles of
-// 256 (DeepSeek-V2-Lite shape, 4096 tokens), a third of the MMA work wasted.
+// rows are split into nearly equal tiles and a ragged end costs at most 31
+// rows, where rows on the M side cost up to 255: 384 rows an expert took 2
+// tiles of 256 (DeepSeek-V2-Lite shape, 4096 tokens), a third of the MMA work.
 // It also serves a decode-size batch, N = 32, as a pure stream of weights.
 //
 // The accumulator comes out transposed (a lane is a channel, a column a row of
@@ -25,11 +25,32 @@
 //
 // The tiles of all experts form one list (expert by expert, row tiles
 // innermost: a weight tile read by several of them comes from L2 after the
-// first), taken round robin by the resident pairs.
+// first), taken round robin by the resident pairs; the tiles of the last,
+// partial round are cut into parts.
 //
-// Block: warp 0 issues the TMA loads, warp 1 the MMAs (one thread of the
-// pair's leader), warps 2-5 the epilogue, in panels of 32 rows through a ring
-// of buffers.  Accumulators are double-buffered.  Every wait is bounded.
+// Block: warp 0 issues the TMA loads, warp 1 the MMAs (of the pair's leader),
+// both converged with one lane picked for the issue; warps 2-9 the epilogue,
+// in panels of 32 rows through a ring of buffers.  Accumulators are
+// double-buffered.  Every wait is bounded.
+//
+// Bound and measurements (GB300; 76 pairs):
+//   few rows an expert: HBM reads of the weights.  8 tokens, Mixtral-8x7B
+//     shape, Down: 121 us for 846 MB, 1.03 of the measured copy bandwidth.
+//   many rows: the tensor pipe at the clock that the power limit leaves.
+//     1024 rows an expert, Up at d 4096, I 3584: 313 us, 1.54 PFLOP/s, 0.91 of
+//     the measured sustained bf16 rate; 4096 tokens of the Qwen2-57B shape,
+//     skewed, Up: 0.89 ms, 1.35 PFLOP/s.
+//   between: both.  384 rows an expert (DeepSeek-V2-Lite shape, 4096 tokens),
+//     Dx: 976 MB and 283 GFLOP take 144 and 146 us at the burst rates; 190 us
+//     measured (218 in long runs).  With every load served by L2 it takes 155,
+//     without loads 145: what is left is HBM latency that 5 or 6 stages do not
+//     cover.
+// Tried and left out: copies into L2 ahead of the loads (slower at every
+// distance: 190 -> 200 us and worse, the weights came from HBM twice); two pairs
+// sharing the rows by multicast (36 clusters of four instead of 76 pairs: no
+// faster, though measured while the issue of the MMAs was still the bound);
+// boxes of 16 rows for a ragged B (a copy costs its issuing warp some
+// 100 cycles whatever its size: 247 -> 295 us before the issue was converged).
 #include <cuda.h>
 
 #include <array>
@@ -141,7 +162,8 @@ __device__ __forceinline__ Tile decode(const RowsParams& p, const int* first, co
     const int r0 = min(max(p.offsets[lo], 0), p.M), rows = min(max(p.offsets[lo + 1], 0), p.M) - r0;
     const int mts = row_tiles<MAXN>(rows), units = (rows + kStepN - 1) / kStepN;
     const int local = t - first[lo], c = local / mts, m = local - c * mts;
-    const int u0 = m * units / mts, nu = (m + 1) * units / mts - u0;  // this tile's units
+    const int base = units / mts, more = units - base * mts;          // the first `more` tiles have a unit more
+    const int u0 = m * base + min(m, more), nu = base + (m < more);   // this tile's units
     const int a = u0 + part * nu / cut, b = u0 + (part + 1) * nu / cut;
     Tile x;
     x.e = lo;
@@ -572,11 +594,10 @@ cudaError_t launch_grouped_rows_tc(const GroupedArgs& a, const GroupedArgs* dw, 
     const bool nt = a.form == kFormUp || a.form == kFormDh;
     const uint64_t d = (uint64_t)a.d, I = (uint64_t)a.I, M = (uint64_t)a.M;
     const uint64_t K = nt ? d : I, cols = nt ? I : d;
-#ifdef MOE_FEW
-    const bool few = MOE_FEW;
-#else
-    const bool few = (long long)a.M <= 24LL * a.N;
-#endif
+    // Tiles of up to 64 rows leave room for 8 or 9 stages instead of 5 or 6, which is what a stream of
+    // weights wants: 48 rows an expert (DeepSeek-V2-Lite shape) took Up 121 us against 129 and Dh 73 against
+    // 77, 96 rows 149 against 132 and 92 against 84.
+    const bool few = (long long)a.M <= 48LL * a.N;
     const int max_n = few ? 64 : 256;
     const int span = a.form == kFormUp ? 128 : 256;
     bool ok = true;

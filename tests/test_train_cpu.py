@@ -160,6 +160,24 @@ def test_rows_off_an_element_boundary_are_refused(call, arg):
     assert _calls(moe.make_dims(**BASE), odd=arg)[call]() == moe.MOE_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("call,arg", [("dispatch", "idx"), ("dispatch", "off"), ("dispatch", "perm"), ("dispatch", "inv"),
+                                      ("combine", "gate"), ("combine", "inv"), ("combine_grad", "gate"),
+                                      ("combine_grad", "dgate"), ("gate_grad", "prob"), ("gate_grad", "dlogits"),
+                                      ("gate_grad", "loss"), ("up", "off"), ("up_grad", "off"), ("down", "off"),
+                                      ("down_grad", "off")])
+def test_indices_and_floats_off_a_word_boundary_are_refused(call, arg):
+    assert _calls(moe.make_dims(**BASE), odd=arg)[call]() == moe.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw,path", [
+    (dict(), "simt"), (dict(d=64, I=64), "tc"), (dict(d=2048, I=1408), "tc"), (dict(d=72, I=200), "tc"),
+    (dict(d=100, I=64), "simt"), (dict(d=64, I=60), "simt"), (dict(d=56, I=64), "simt"), (dict(d=64, I=56), "simt"),
+    (dict(d=2048, I=1408, wtype="f32"), "simt"), (dict(N=512, d=64, I=64), "tc"),
+])
+def test_products_path_choice(kw, path):
+    assert moe.moe_experts_path(moe.make_dims(**dict(BASE, **kw))) == path
+
+
 def test_workspace_stride_capacity_and_type_refusals():
     D = moe.make_dims(**BASE)
     for call in ("dispatch", "gate_grad", "up", "up_grad", "down", "down_grad"):
