@@ -266,8 +266,8 @@ __device__ __forceinline__ void map_acquire(const void* map) {
 }
 
 
-// The weight gradients' maps: an expert's rows of a0, a1 and b, made from the
-// maps of the whole tensors by one warp (expert_maps), in the workspace.
+// The weight gradients' maps: an expert's rows of a0, a1 and b, made from a
+// one-row map of each tensor by one warp (expert_maps), in the workspace.
 constexpr int kMapsPerExpert = 3;
 struct MapParams {
     CUtensorMap t[kMapsPerExpert];

@@ -98,3 +98,35 @@ def test_products_beyond_2_to_31_elements():
     e = (h[last].double().T @ y[last][:, -64:].double()).cpu().numpy()
     m = (h[last].double().abs().T @ y[last][:, -64:].double().abs()).cpu().numpy()
     ref.check(host(dw[-1])[:, -64:], e, ref.bound(e, T, m, "f32"), "dw")
+
+
+def _at_the_end(t):
+    """The same tensor as the last rows of a buffer that fills its allocation."""
+    n = t.numel() * t.element_size()
+    buf = torch.empty((n + (12 << 20)) // (2 << 20) * (2 << 20), dtype=torch.uint8, device="cuda")
+    view = buf[buf.numel() - n:].view(t.dtype).view(t.shape)
+    return view.copy_(t)
+
+
+@pytest.mark.parametrize("T,d,N,k,I", [(48, 1536, 40, 8, 512), (600, 512, 8, 2, 1024)])
+def test_rows_that_end_with_their_allocation(T, d, N, k, I):
+    """Small segments of large row tensors: nothing past the last row is read, and the results are
+    those of rows with others behind them."""
+    torch.cuda.empty_cache()
+    f = Ffn(T, d, N, k, I, "all", "bf16")
+    (dg, _), (du, _), (dy, _), (h, _), (g, _), (u, _) = (f.rows(n) for n in (I, I, d, I, I, I))
+    rows = [torch.nan_to_num(t) for t in (f.x, dg, du, dy, h, g, u)]
+
+    def step(x, dg, du, dy, h, g, u, end):
+        place = _at_the_end if end else (lambda t: t)
+        outs = [place(empty((f.M, n), "bf16")) for n in (I, I, I, d, d, I, I)]
+        dws = [empty((N, I, d), "f32") for _ in range(3)]
+        moe.moe_experts_up(f.D, x, f.doff, f.wg, f.wu, *outs[:3], f.ws)
+        moe.moe_experts_down(f.D, h, f.doff, f.wd, outs[3], f.ws)
+        moe.moe_experts_up_grad(f.D, dg, du, x, f.doff, f.wg, f.wu, outs[4], dws[0], dws[1], False, f.ws)
+        moe.moe_experts_down_grad(f.D, dy, h, g, u, f.doff, f.wd, outs[5], outs[6], dws[2], False, f.ws)
+        f.done()
+        return outs + dws
+
+    for a, b in zip(step(*rows, False), step(*[_at_the_end(t) for t in rows], True)):
+        assert torch.equal(torch.nan_to_num(a), torch.nan_to_num(b))
