@@ -254,7 +254,7 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool pred) {
 // ---------------------------------------------------------------- tensor maps changed on the device
 // Rows [first, first + rows) of a 2-D map, as a map of its own: its address
 // and its row count are replaced in global memory.  A kernel that uses the map
-// acquires it first (map_acquire, by the thread that issues the copies).
+// acquires it first (map_acquire, by the warp that issues the copies).
 __device__ __forceinline__ void map_replace(void* map, uint64_t address, uint32_t rows) {
     asm volatile("tensormap.replace.tile.global_address.global.b1024.b64 [%0], %1;" ::"l"(map), "l"(address) : "memory");
     asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;" ::"l"(map), "r"(rows) : "memory");

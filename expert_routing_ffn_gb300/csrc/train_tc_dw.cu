@@ -186,7 +186,16 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
         const uint32_t full0 = leader_address(&full[0]);
         int st = 0, it = 0;
         uint32_t phase = 1;
-        for (int i = lane; i < p.N * kMapsPerExpert; i += 32) map_acquire(p.maps + (size_t)i * 128);
+        // The maps of the experts that this pair takes tiles of, an expert a lane: all experts' made
+        // the Granite-shaped down gradient 57.3 us instead of 55.0, and each expert's at its first tile, in the loads' way,
+        // 11 us of 193 (8 tokens, DeepSeek-V2-Lite shape, up gradient).
+        const int per = (strips * p.n_mat + 1) / 2 * ((p.d + kBN - 1) / kBN);  // tiles of an expert
+        for (int j = lane; j < live; j += 32) {
+            // the pair's first tile from that expert's first tile on
+            const int t = unit + (max(j * per - unit, 0) + n_units - 1) / n_units * n_units;
+            if (t < (j + 1) * per)
+                for (int m = 0; m < kMapsPerExpert; ++m) map_acquire(p.maps + ((size_t)order[j] * kMapsPerExpert + m) * 128);
+        }
         __syncwarp();
         for (Walk x(p, order, live, unit, n_units); x.more(); x.next(p, order)) {
             if (__any_sync(0xffffffffu, *abort_flag)) break;
