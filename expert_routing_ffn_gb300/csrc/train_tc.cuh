@@ -75,8 +75,8 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
 }
 
 // ---------------------------------------------------------------- loads, stores
-// 2-D and 3-D tile loads; bar: the mbarrier's shared::cluster address (the
-// leader's for a pair).
+// Tile loads; bar: the mbarrier's shared::cluster address (the leader's for a
+// pair; 3-D loads are a pair's).
 template <bool PAIR>
 __device__ __forceinline__ void load_2d(uint32_t dst, const void* map, int c0, int c1, uint32_t bar) {
     if constexpr (PAIR)
@@ -88,27 +88,11 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const void* map, int c0, i
             "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
             " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar) : "memory");
 }
-template <bool PAIR>
 __device__ __forceinline__ void load_3d(uint32_t dst, const void* map, int c0, int c1, int c2, uint32_t bar) {
-    if constexpr (PAIR)
-        asm volatile(
-            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3, %4}], [%5];"
-            ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3, %4}], [%5];"
-            ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
-}
-// A pair's CTA loads a tile into the same place of every CTA in `mask`; each
-// of them signals its own pair's leader.
-__device__ __forceinline__ void load_2d_multicast(uint32_t dst, const void* map, int c0, int c1, uint32_t bar,
-                                                  uint16_t mask) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;"
-        ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar), "h"(mask) : "memory");
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
 }
 // The pair's loads with an L2 policy.
 __device__ __forceinline__ void load_2d_hint(uint32_t dst, const void* map, int c0, int c1, uint32_t bar, uint64_t policy) {
@@ -172,52 +156,30 @@ __device__ __forceinline__ bool elect_one() {
 // the address field is its low 14 bits, and no operand crosses 256 KB.
 __device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
 
-template <bool PAIR>
 __device__ __forceinline__ void mma(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
-    if constexpr (PAIR)
-        asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-            " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n"
-            ::"r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc) : "memory");
-    else tc_mma(tmem_d, adesc, bdesc, idesc, acc);
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+        ::"r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc) : "memory");
 }
-// arrive on `bar` (of both CTAs of a pair) when the MMAs issued so far are done
-template <bool PAIR>
+// arrive on `bar` of both CTAs when the MMAs issued so far are done
 __device__ __forceinline__ void commit(uint64_t* bar) {
-    if constexpr (PAIR)
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-            ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
-    else tc_commit(bar);
-}
-// arrive on `bar` of the cluster's CTAs in `mask`
-__device__ __forceinline__ void commit_mask(uint64_t* bar, uint16_t mask) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-        ::"r"(smem_u32(bar)), "h"(mask) : "memory");
+        ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
 }
 // the same, on this CTA's barrier alone
-template <bool PAIR>
 __device__ __forceinline__ void commit_local(uint64_t* bar) {
-    if constexpr (PAIR)
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                     ::"r"(smem_u32(bar)) : "memory");
-    else tc_commit(bar);
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 ::"r"(smem_u32(bar)) : "memory");
 }
-template <bool PAIR>
+// all 512 columns, of both CTAs: by a warp of each
 __device__ __forceinline__ void tmem_alloc(uint32_t* where) {
-    if constexpr (PAIR) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(where)));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-    } else {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(where)));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(where)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
 }
-template <bool PAIR>
 __device__ __forceinline__ void tmem_free(uint32_t base) {
-    if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(base));
-    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(base));
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(base));
 }
 
 // 32 consecutive accumulator columns of this thread's tensor-memory lane; the
@@ -282,7 +244,6 @@ __device__ __forceinline__ void map_prefetch(const void* map) { asm volatile("pr
 __device__ __forceinline__ void map_acquire(const void* map) {
     asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
 }
-
 
 // The weight gradients' maps: an expert's rows of a0, a1 and b, made from a
 // one-row map of each tensor by one warp (expert_maps), in the workspace.

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
             *abort_flag = 1;
         }
     }
-    if (warp == 1) tmem_alloc<true>(tmem_s);
+    if (warp == 1) tmem_alloc(tmem_s);
     fence_proxy_async();  // the row counts' shared memory becomes a stage that TMA writes
     tc_fence_before();
     __syncthreads();
@@ -254,17 +254,17 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
 #pragma unroll
                         for (int kk = 0; kk < (int)kBK / 16; ++kk)
                             if (kk == 0 || k0 + kk * 16 < rows)
-                                mma<true>(acc, desc_at(da, kk * 2048), desc_at(db, kk * 2048), idesc, (k0 | kk) ? 1u : 0u);
-                        commit<true>(&empty[st]);
+                                mma(acc, desc_at(da, kk * 2048), desc_at(db, kk * 2048), idesc, (k0 | kk) ? 1u : 0u);
+                        commit(&empty[st]);
                     }
                     __syncwarp();
                     if (++st == kS) { st = 0; phase ^= 1; }
                 }
-                if (elect_one()) commit<true>(&tfull[ab]);
+                if (elect_one()) commit(&tfull[ab]);
                 __syncwarp();
             }
             // every MMA issued here is done before tensor memory is released
-            if (elect_one()) commit_local<true>(drain);
+            if (elect_one()) commit_local(drain);
             __syncwarp();
             (void)wait<true>(drain, 0, abort_flag, p.err, 6, false);
         }
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
     // tensor memory, are done before either CTA frees or leaves
     cluster_sync();
     tc_fence_after();
-    if (warp == 1) tmem_free<true>(tmem);
+    if (warp == 1) tmem_free(tmem);
     grid_dep_launch();
 }
 

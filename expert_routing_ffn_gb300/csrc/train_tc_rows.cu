@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
         }
         if (lane == 0) first[p.N] = carry;
     }
-    if (warp == 1) tmem_alloc<true>(tmem_s);
+    if (warp == 1) tmem_alloc(tmem_s);
     if (p.dw.maps && warp >= 2)
         for (int e = (int)blockIdx.x * 8 + warp - 2; e < p.N; e += (int)gridDim.x * 8) expert_maps(p.dw, e);
     {  // rows of no expert
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
                     const uint32_t ad = base + st * C::kStage, bd = ad + kStageA, bar = full0 + st * 8;
                     auto weights = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t b) {
                         if constexpr (MAXN <= 64) load_3d_hint(dst, map, c0, c1, e, b, once);
-                        else load_3d<true>(dst, map, c0, c1, e, b);
+                        else load_3d(dst, map, c0, c1, e, b);
                     };
                     if (leader) mbar_arrive_expect_tx(&full[st], bytes);
                     const int part = FORM == kFormDx && kb >= nk1;
@@ -325,9 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
                         const uint64_t da = desc_at(da0, st * C::kStage), db = desc_at(db0, st * C::kStage);
 #pragma unroll
                         for (int kk = 0; kk < (int)kBK / 16; ++kk)
-                            mma<true>(acc, desc_at(da, kk * kStepA), desc_at(db, kk * kStepB), idesc, (kb | kk) ? 1u : 0u);
-                        commit<true>(&empty[st]);
-                        if (kb + 1 == nk) commit<true>(&tfull[ab]);
+                            mma(acc, desc_at(da, kk * kStepA), desc_at(db, kk * kStepB), idesc, (kb | kk) ? 1u : 0u);
+                        commit(&empty[st]);
+                        if (kb + 1 == nk) commit(&tfull[ab]);
                     }
                     __syncwarp();
                     if (++st == kS) { st = 0; phase ^= 1; }
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
                 ++local;
             }
             // every MMA issued here is done before tensor memory is released
-            if (elect_one()) commit_local<true>(drain);
+            if (elect_one()) commit_local(drain);
             __syncwarp();
             (void)wait<true>(drain, 0, abort_flag, p.err, 6, false);
         }
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
     // tensor memory, are done before either CTA frees or leaves
     cluster_sync();
     tc_fence_after();
-    if (warp == 1) tmem_free<true>(tmem);
+    if (warp == 1) tmem_free(tmem);
     grid_dep_launch();
 }
 
