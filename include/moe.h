@@ -19,6 +19,7 @@
  * the heterogeneous CPU-GPU path: moe_hetero_fetch_min_rows,
  * moe_select_hetero, moe_cpu_experts and moe_layer_forward_hetero (exact
  * host execution of high-confidence misses chosen by a cost model).
+ * The layer's training step has a header of its own, moe_train.h.
  *
  * Conventions (all entry points):
  *   - Every function returns moe_status (the two size helpers and
