@@ -73,7 +73,6 @@ constexpr int kGroups = 2, kGroupThreads = 128;  // epilogue: two groups of four
 constexpr int kThreads = 64 + kGroups * kGroupThreads;
 constexpr int kStepN = 32;     // granularity of N on a CTA pair
 constexpr int kPanel = 32;     // rows per epilogue panel
-constexpr int kBuffers = 2;    // panel buffers of each group
 constexpr uint32_t kBK = kTcBK;
 constexpr uint32_t kStageA = 128 * kBK * 2;
 constexpr uint32_t kBox = kPanel * 128;  // 32 rows x 64 channels
@@ -87,7 +86,11 @@ struct Cfg {
     static constexpr int kBoxes = FORM == kFormUp ? 3 : FORM == kFormDh ? 4 : 2;  // boxes of a panel
     static constexpr uint32_t kStage = kStageA + MAXN / 2 * kBK * 2;
     static constexpr uint32_t kBuffer = kBoxes * kBox;
-    static constexpr uint32_t kSwap = FORM == kFormUp ? kGroupThreads * 64 : 0;  // a group's room to swap values
+    // Panel buffers of a group.  Large tiles of Up have one, which costs a barrier a panel and leaves room for a
+    // sixth stage: 384 rows an expert (DeepSeek-V2-Lite shape) 239 -> 231 us, 4096 tokens of the Qwen2-57B shape
+    // 900 -> 880; 200 rows (Granite shape) 37.4 -> 38.6; 64-row tiles, which have eight stages, 110 -> 112.
+    static constexpr int kBuffers = FORM == kFormUp && MAXN == 256 ? 1 : 2;
+    static constexpr uint32_t kSwap = FORM == kFormUp ? kGroupThreads * 32 : 0;  // a group's room to swap values
     static constexpr uint32_t kEpi = kGroups * (kBuffers * kBuffer + kSwap);
     static constexpr int kStages = (int)((224 * 1024 - kEpi) / kStage);
     static constexpr uint32_t kPanels = (kStages * kStage + 1023) / 1024 * 1024;  // epilogue buffers
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
     int* first = reinterpret_cast<int*>(smem + C::kTable);  // tiles before each expert
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBars);
     uint64_t *empty = full + kS, *tfull = empty + kS, *tempty = tfull + 2, *drain = tempty + 2, *pfull = drain + 1;
-    uint32_t* tmem_s = reinterpret_cast<uint32_t*>(pfull + kGroups * kBuffers);
+    uint32_t* tmem_s = reinterpret_cast<uint32_t*>(pfull + kGroups * C::kBuffers);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_s + 1);
 
     grid_dep_wait();  // the previous kernels' outputs; no tensor memory is taken before it
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
             mbar_init(&tempty[b], 2 * kGroups * 4);  // an arrival per epilogue warp of both CTAs
         }
         mbar_init(drain, 1);
-        for (int b = 0; b < kGroups * kBuffers; ++b) mbar_init(&pfull[b], 1);
+        for (int b = 0; b < kGroups * C::kBuffers; ++b) mbar_init(&pfull[b], 1);
         fence_mbar_init();
         *abort_flag = 0;
         if (base & 1023u) {  // the swizzled tiles need it
@@ -345,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
         const int quarter = warp & 3, group = (warp - 2) >> 2, etid = (tid - 64) & (kGroupThreads - 1);
         const int bar_id = 1 + group;
         const bool boss = etid == 0;  // issues the group's output stores (and Dh's input loads)
-        const uint32_t panels = base + C::kPanels + group * kBuffers * C::kBuffer;
-        uint64_t* const in_bar = pfull + group * kBuffers;
+        const uint32_t panels = base + C::kPanels + group * C::kBuffers * C::kBuffer;
+        uint64_t* const in_bar = pfull + group * C::kBuffers;
         const uint32_t free0 = leader_address(&tempty[0]), free1 = leader_address(&tempty[1]);
         // stmatrix / ldmatrix: lanes 8j .. 8j + 7 address matrix j, a row of 16 bytes each
         const int mj = lane >> 3, mr = lane & 7;
@@ -370,8 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
             const int ch = x.c0 + (int)rank * C::kChannels;
             const bool any = ch < n_cols && group * kPanel < x.rows;  // this group has a panel of this CTA's channels
             if (FORM == kFormDh && any && boss) {  // the first panel's inputs, beside the tile's MMAs
-                stores_read<kBuffers - 1>();
-                load_inputs(x, ch, group * kPanel, pn % kBuffers);
+                stores_read<C::kBuffers - 1>();
+                load_inputs(x, ch, group * kPanel, pn % C::kBuffers);
             }
             const int ab = local & 1;
             bool ok = true;
@@ -384,48 +387,50 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
             if (any) {
 #pragma unroll 1
                 for (int q0 = group * kPanel; q0 < x.rows; q0 += kGroups * kPanel, ++pn) {
-                    const uint32_t buf = panels + (pn % kBuffers) * C::kBuffer;
+                    const uint32_t buf = panels + (pn % C::kBuffers) * C::kBuffer;
                     if (FORM == kFormDh && boss && q0 + kGroups * kPanel < x.rows) {
                         stores_read<0>();  // the last panel's store has left the other buffer
-                        load_inputs(x, ch, q0 + kGroups * kPanel, (pn + 1) % kBuffers);
+                        load_inputs(x, ch, q0 + kGroups * kPanel, (pn + 1) % C::kBuffers);
                     }
                     uint32_t lo[16], hi[16];  // lanes 0-15 and 16-31 of the warp's quarter
                     tmem_ld_16x32(taddr + q0, lo);
                     tmem_ld_16x32(taddr + (16u << 16) + q0, hi);
+                    if constexpr (C::kBuffers == 1) {  // the last panel's store has read the buffer
+                        if (boss) stores_read<0>();
+                        bar_sync(bar_id, kGroupThreads);
+                    }
                     tmem_ld_wait();
                     if constexpr (FORM == kFormUp) {
                         // warps of quarters 0, 1 hold g and those of 2, 3 hold u of the same channels, at the
                         // same registers.  Each pair of warps swaps 16 rows' values for the other 16's, in
                         // fp32, and forms h of the rows it then has both of.
                         const bool is_u = quarter >= 2;
-                        float4* mine = reinterpret_cast<float4*>(smem + C::kPanels + kGroups * kBuffers * C::kBuffer +
+                        float4* mine = reinterpret_cast<float4*>(smem + C::kPanels + kGroups * C::kBuffers * C::kBuffer +
                                                                  group * C::kSwap) + etid;
                         const float4* theirs = mine + (((etid >> 5) ^ 2) - (etid >> 5)) * 32;
-                        // g gives away rows 16-31 (blocks 2, 3), u rows 0-15
+                        // g gives away rows 16-31 (blocks 2, 3), u rows 0-15, a block at a time
+                        const uint32_t at = buf + mr * 128 + (((my_chunk + mj) ^ mr) << 4);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const uint32_t* l = is_u ? lo + 4 * i : lo + 8 + 4 * i;
                             const uint32_t* h = is_u ? hi + 4 * i : hi + 8 + 4 * i;
-                            mine[(2 * i) * kGroupThreads] = make_float4(__uint_as_float(l[0]), __uint_as_float(l[1]),
-                                                                      __uint_as_float(l[2]), __uint_as_float(l[3]));
-                            mine[(2 * i + 1) * kGroupThreads] = make_float4(__uint_as_float(h[0]), __uint_as_float(h[1]),
-                                                                          __uint_as_float(h[2]), __uint_as_float(h[3]));
-                        }
-                        const uint32_t at = buf + mr * 128 + (((my_chunk + mj) ^ mr) << 4);
-                        if (p.out[0]) {
+                            if (i > 0) bar_sync(3 + group * 2 + (quarter & 1), 64);
+                            mine[0] = make_float4(__uint_as_float(l[0]), __uint_as_float(l[1]), __uint_as_float(l[2]),
+                                                  __uint_as_float(l[3]));
+                            mine[kGroupThreads] = make_float4(__uint_as_float(h[0]), __uint_as_float(h[1]),
+                                                              __uint_as_float(h[2]), __uint_as_float(h[3]));
+                            if (p.out[0]) {  // g or u of 16 rows, beside the swap
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                stmatrix_x4_trans(at + (is_u ? kBox : 0) + i * 1024, pack_f(lo[4 * i], lo[4 * i + 1]),
-                                                  pack_f(lo[4 * i + 2], lo[4 * i + 3]), pack_f(hi[4 * i], hi[4 * i + 1]),
-                                                  pack_f(hi[4 * i + 2], hi[4 * i + 3]));
-                        }
-                        bar_sync(3 + group * 2 + (quarter & 1), 64);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
+                                for (int b = 2 * i; b < 2 * i + 2; ++b)
+                                    stmatrix_x4_trans(at + (is_u ? kBox : 0) + b * 1024, pack_f(lo[4 * b], lo[4 * b + 1]),
+                                                      pack_f(lo[4 * b + 2], lo[4 * b + 3]), pack_f(hi[4 * b], hi[4 * b + 1]),
+                                                      pack_f(hi[4 * b + 2], hi[4 * b + 3]));
+                            }
+                            bar_sync(3 + group * 2 + (quarter & 1), 64);
                             uint32_t w[4];
 #pragma unroll
                             for (int z = 0; z < 2; ++z) {
-                                const float4 o = theirs[(2 * i + z) * kGroupThreads];
+                                const float4 o = theirs[z * kGroupThreads];
                                 const uint32_t* m = z ? (is_u ? hi + 8 + 4 * i : hi + 4 * i) : (is_u ? lo + 8 + 4 * i : lo + 4 * i);
                                 const float of[4] = {o.x, o.y, o.z, o.w};
                                 float v[4];
@@ -444,9 +449,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
                         const uint32_t at = buf + my_box * kBox + mr * 128 + (((my_chunk + mj) ^ mr) << 4);
                         if constexpr (FORM == kFormDh) {
                             if (lane == 0)
-                                (void)wait<false>(&in_bar[pn % kBuffers], (in_phase >> (pn % kBuffers)) & 1, abort_flag, p.err, 7, false);
+                                (void)wait<false>(&in_bar[pn % C::kBuffers], (in_phase >> (pn % C::kBuffers)) & 1, abort_flag, p.err, 7, false);
                             __syncwarp();
-                            in_phase ^= 1u << (pn % kBuffers);
+                            in_phase ^= 1u << (pn % C::kBuffers);
                         }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {  // 8 rows, 32 channels
@@ -482,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
                     }
                     fence_proxy_async();
                     // the next panel's buffer is free once the store that last used it has read it
-                    if (FORM != kFormDh && boss) stores_read<kBuffers - 2>();
+                    if (FORM != kFormDh && C::kBuffers == 2 && boss) stores_read<0>();
                     bar_sync(bar_id, kGroupThreads);
                     // box b of the buffer: which output, and its first channel
                     auto out_of = [&](int b) { return FORM == kFormUp ? b : FORM == kFormDh ? b >> 1 : 0; };
