@@ -28,7 +28,7 @@
 // Bound and measurements (GB300): few rows, HBM writes: dWg and dWu of 8 tokens
 // in the Mixtral-8x7B shape 298 us for 1.88 GB, 0.93 of the measured copy
 // bandwidth.  384 rows an expert (DeepSeek-V2-Lite shape, 4096 tokens), both:
-// 976 MB and 283 GFLOP take 144 and 146 us at the burst rates; 245 us measured,
+// 976 MB and 283 GFLOP take 144 and 146 us at the burst rates; 235 us measured,
 // of which the loads' latency beside the stream of stores is most (without the
 // stores 169 us).  Zeroing the foreign rows in shared memory by a warp of its
 // own instead of per-expert maps needs a release across the CTAs of a pair that
@@ -50,15 +50,22 @@ namespace {
 using namespace train;
 
 constexpr int kStrip = 128, kBN = 256, kEpiWarps = 8, kThreads = 64 + 32 * kEpiWarps;
-constexpr int kBoxesPerWarp = 2;
 constexpr uint32_t kBK = kTcBK;
 constexpr uint32_t kStageA = kStrip * kBK * 2, kStageB = kBN / 2 * kBK * 2, kStage = kStageA + kStageB;
 constexpr uint32_t kBox = 32 * 128;          // 32 channels x 128 bytes
-constexpr int kS = 5;                        // stages
-constexpr uint32_t kBoxes = kS * kStage, kTable = kBoxes + kEpiWarps * kBoxesPerWarp * kBox;  // table: rank -> expert
-constexpr uint32_t kBars = kTable + kTrainMaxExperts * 4 + 16;
-constexpr uint32_t kSmem = kBars + (2 * kS + 5) * 8 + 16;
-static_assert(kSmem <= 232448, "227 KB of shared memory per block");
+
+// BOXES: store boxes of an epilogue warp.  One keeps fewer stores under way and leaves room for a sixth stage:
+// 384 rows an expert (DeepSeek-V2-Lite shape), dWg and dWu 249 -> 235 us, one matrix 139 -> 131.  With few rows,
+// where the stores are the work, two: 8 tokens 118 us against 125, 96 rows an expert 140 against 153, 160 rows
+// 158 against 150.
+template <int BOXES>
+struct DwCfg {
+    static constexpr int kS = BOXES == 1 ? 6 : 5;  // stages
+    static constexpr uint32_t kBoxes = kS * kStage, kTable = kBoxes + kEpiWarps * BOXES * kBox;  // table: rank -> expert
+    static constexpr uint32_t kBars = kTable + kTrainMaxExperts * 4 + 16;
+    static constexpr uint32_t kSmem = kBars + (2 * kS + 5) * 8 + 16;
+    static_assert(kSmem <= 232448, "227 KB of shared memory per block");
+};
 
 struct DwParams {
     CUtensorMap o[2];
@@ -111,12 +118,14 @@ struct Walk {
     }
 };
 
-template <bool F32>
+template <bool F32, int BOXES>
 __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_constant__ DwParams p) {
+    using C = DwCfg<BOXES>;
+    constexpr int kS = C::kS;
     extern __shared__ __align__(1024) unsigned char smem[];
-    int* order = reinterpret_cast<int*>(smem + kTable);  // rank -> expert
+    int* order = reinterpret_cast<int*>(smem + C::kTable);  // rank -> expert
     int* live_s = order + kTrainMaxExperts;               // experts with rows
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBars);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBars);
     uint64_t *empty = full + kS, *tfull = empty + kS, *tempty = tfull + 2, *drain = tempty + 2;
     uint32_t* tmem_s = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_s + 1);
@@ -272,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
         // ---------------- epilogue: a thread owns a channel of dW, two warps share a quarter of
         // the lanes, 128 columns each
         const int quarter = warp & 3, half = (warp - 2) >> 2;
-        const uint32_t boxes = base + kBoxes + (warp - 2) * kBoxesPerWarp * kBox;
+        const uint32_t boxes = base + C::kBoxes + (warp - 2) * BOXES * kBox;
         const uint32_t sw = lane & 7;  // 128-byte swizzle: chunk j of row i at chunk j ^ (i & 7)
         const uint32_t free0 = leader_address(&tempty[0]), free1 = leader_address(&tempty[1]);
         int local = 0;
@@ -299,11 +308,11 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
                 else mbar_arrive(&tempty[ab]);
             }
             if (m >= p.I) continue;
-            // a box at a time: one is filled while the store of the other drains
+            // a box at a time; of two, one is filled while the store of the other drains
 #pragma unroll
             for (int r = 0; r < 128 / kW; ++r) {
-                const uint32_t box = boxes + (r & 1) * kBox;
-                if (lane == 0) stores_read<1>();
+                const uint32_t box = boxes + r % BOXES * kBox;
+                if (lane == 0) stores_read<BOXES - 1>();
                 __syncwarp();
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {  // 16 bytes
@@ -328,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
         }
         // zeros for the experts without rows, in contiguous pieces of this warp's boxes
         if (!p.accumulate && live < p.N) {
-            constexpr uint32_t kPiece = kBoxesPerWarp * kBox;
+            constexpr uint32_t kPiece = BOXES * kBox;
             if (lane == 0) stores_read<0>();
             __syncwarp();
             for (uint32_t i = lane * 16; i < kPiece; i += 512) st_shared16(boxes + i, 0, 0, 0, 0);
@@ -370,9 +379,10 @@ __global__ void __launch_bounds__(128) expert_maps_kernel(const __grid_constant_
     grid_dep_launch();
 }
 
-template <bool F32>
+template <bool F32, int BOXES>
 cudaError_t launch_dw(const DwParams& p, int sms, cudaStream_t st) {
-    auto kern = grouped_dw_kernel<F32>;
+    auto kern = grouped_dw_kernel<F32, BOXES>;
+    constexpr uint32_t kSmem = DwCfg<BOXES>::kSmem;
     cudaError_t e = allow_max_smem(kern);
     if (e != cudaSuccess) return e;
     int most = 0;
@@ -423,7 +433,9 @@ cudaError_t launch_grouped_dw_tc(const GroupedArgs& a, bool have_maps, cudaStrea
         const cudaError_t e = launch_pdl(expert_maps_kernel, dim3((a.N + 3) / 4), dim3(128), 0, st, mp);
         if (e != cudaSuccess) return e;
     }
-    return a.out_f32 ? launch_dw<true>(p, a.sms, st) : launch_dw<false>(p, a.sms, st);
+    const bool few = (long long)a.M <= 128LL * a.N;
+    return few ? (a.out_f32 ? launch_dw<true, 2>(p, a.sms, st) : launch_dw<false, 2>(p, a.sms, st))
+               : (a.out_f32 ? launch_dw<true, 1>(p, a.sms, st) : launch_dw<false, 1>(p, a.sms, st));
 }
 
 }  // namespace moe

@@ -39,17 +39,18 @@
 //   many rows: the tensor pipe at the clock that the power limit leaves.
 //     1024 rows an expert, Up at d 4096, I 3584: 313 us, 1.54 PFLOP/s, 0.91 of
 //     the measured sustained bf16 rate; 4096 tokens of the Qwen2-57B shape,
-//     skewed, Up: 0.89 ms, 1.35 PFLOP/s.
+//     skewed, Up: 0.88 ms, 1.37 PFLOP/s.
 //   between: both.  384 rows an expert (DeepSeek-V2-Lite shape, 4096 tokens),
 //     Dx: 976 MB and 283 GFLOP take 144 and 146 us at the burst rates; 190 us
 //     measured (218 in long runs).  With every load served by L2 it takes 155,
-//     without loads 145: what is left is HBM latency that 5 or 6 stages do not
-//     cover.
+//     without loads 145, without stores 181: what is left is HBM latency beside
+//     the stores that six stages do not cover (five: 202 us).
 // Tried and left out: copies into L2 ahead of the loads (slower at every
 // distance: 190 -> 200 us and worse, the weights came from HBM twice); two pairs
 // sharing the rows by multicast (36 clusters of four instead of 76 pairs: no
 // faster, though measured while the issue of the MMAs was still the bound);
-// boxes of 16 rows for a ragged B (a copy costs its issuing warp some
+// tiles of 512 rows over both accumulators, which load a third less but leave the
+// epilogue beside no MMA (384 rows an expert, Up: 229 -> 249 us, Dx even); boxes of 16 rows for a ragged B (a copy costs its issuing warp some
 // 100 cycles whatever its size: 247 -> 295 us before the issue was converged).
 #include <cuda.h>
 
