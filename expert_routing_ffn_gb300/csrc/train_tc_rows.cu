@@ -50,8 +50,10 @@
 // sharing the rows by multicast (36 clusters of four instead of 76 pairs: no
 // faster, though measured while the issue of the MMAs was still the bound);
 // tiles of 512 rows over both accumulators, which load a third less but leave the
-// epilogue beside no MMA (384 rows an expert, Up: 229 -> 249 us, Dx even); boxes of 16 rows for a ragged B (a copy costs its issuing warp some
-// 100 cycles whatever its size: 247 -> 295 us before the issue was converged).
+// epilogue beside no MMA (384 rows an expert, Up: 229 -> 249 us, Dx even); one
+// epilogue buffer in Down and Dx (even); L2 policies on the stores (even); boxes
+// of 16 rows for a ragged B (a copy costs its issuing warp some 100 cycles
+// whatever its size: 247 -> 295 us before the issue was converged).
 #include <cuda.h>
 
 #include <array>
