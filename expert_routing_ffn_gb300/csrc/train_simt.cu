@@ -12,11 +12,12 @@
 // puts the 16-byte reads of eight lanes on different banks.
 //
 // Bound: FMA rate.  The 16-row tiles serve segments that average so few rows
-// that most of a 64-row tile would be padding.  Measured, fp32: 128 rows an
-// expert at d = I = 1024, 16 experts, Up: 304 us, 28 TFLOP/s (ragged rows fill
-// 0.8 of the tiles, the tiles 0.7 of three rounds); 16 tokens of the tiny
-// layer: 11 us.  Tiles are numbered expert by
-// expert; every block forms the prefix sums of the tile counts itself.
+// that most of a 64-row tile would be padding; with fewer still, or without
+// 16-byte loads, grouped_few_kernel streams the weights past eight rows.
+// Measured, fp32: 128 rows an expert at d = I = 1024, 16 experts, Up: 297 us, 29
+// TFLOP/s (ragged rows fill 0.8 of the tiles, the tiles 0.7 of three rounds).
+// Tiles are numbered expert by expert; every block forms the prefix sums of the
+// tile counts itself.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -74,29 +75,17 @@ struct Cfg {
     static constexpr int kSmem = kStages * kStage * 4;
 };
 
-template <typename W, int FORM, int BM>
-__global__ void __launch_bounds__(kThreads) grouped_simt_kernel(const SimtParams p) {
-    using C = Cfg<W, FORM, BM>;
-    constexpr int kR = BM / 8;  // rows of a lane
-    constexpr bool kF32 = sizeof(W) == 4;
-    extern __shared__ __align__(16) float stages[];
-    __shared__ int row_s[kTrainMaxExperts + 1], tile_s[kTrainMaxExperts + 1];
-    const W* tag = nullptr;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    grid_dep_wait();
+// row_s: the experts' first rows, tile_s: the tiles before each expert, of(its rows) each
+template <typename F>
+__device__ __forceinline__ void count_tiles(const SimtParams& p, int* row_s, int* tile_s, F of) {
+    const int tid = threadIdx.x;
     for (int e = tid; e <= p.N; e += kThreads) row_s[e] = min(max(p.offsets[e], 0), p.M);
     __syncthreads();
-    const int n_cols = C::kNT ? p.I : p.d;
-    constexpr int kCols = FORM == kFormUp ? kBN / 2 : kBN;  // output columns of a tile
-    const int nt = (n_cols + kCols - 1) / kCols;
-    const int n_mat = FORM == kFormDw && p.o1 ? 2 : 1;
-    const int mt_w = (p.I + BM - 1) / BM;
-    if (tid < 32) {  // tiles before each expert
+    if (tid < 32) {
         int carry = 0;
         for (int b = 0; b < p.N; b += 32) {
             const int e = b + tid;
-            int v = 0;
-            if (e < p.N) v = FORM == kFormDw ? n_mat * mt_w * nt : (max(row_s[e + 1] - row_s[e], 0) + BM - 1) / BM * nt;
+            const int v = e < p.N ? of(max(row_s[e + 1] - row_s[e], 0)) : 0;
             int inc = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -109,14 +98,63 @@ __global__ void __launch_bounds__(kThreads) grouped_simt_kernel(const SimtParams
         if (tid == 0) tile_s[p.N] = carry;
     }
     __syncthreads();
+}
+// the last expert whose tiles start at or before this one
+__device__ __forceinline__ int expert_of(const int* tile_s, int N, int tile) {
+    int lo = 0, hi = N;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (tile_s[mid] <= tile) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+// the products that give rows: value c (Up: g, and u) of a grouped row and a column
+template <typename W, int FORM>
+__device__ __forceinline__ void emit(const SimtParams& p, int64_t row, int n, float c, float u) {
+    const W* tag = nullptr;
+    if constexpr (FORM == kFormUp) {
+        const int64_t at = row * p.I + n;
+        if (p.o0) { st(p.o0, at, c, tag); st(p.o1, at, u, tag); }
+        st(p.o2, at, c * sigmoid(c) * u, tag);
+    } else if constexpr (FORM == kFormDh) {
+        const int64_t at = row * p.I + n;
+        const float g = ld(p.g, at, tag), v = ld(p.u, at, tag), sg = sigmoid(g);
+        st(p.o0, at, c * v * sg * (1.f + g * (1.f - sg)), tag);
+        st(p.o1, at, c * g * sg, tag);
+    } else st(p.o0, row * p.d + n, c, tag);
+}
+// zeros for the rows of no expert
+template <typename W>
+__device__ __forceinline__ void zero_rest(const SimtParams& p, int first_row, int n_cols) {
+    const W* tag = nullptr;
+    const int64_t first = (int64_t)first_row * n_cols, last = (int64_t)p.M * n_cols;
+    for (int64_t i = first + (int64_t)blockIdx.x * kThreads + threadIdx.x; i < last; i += (int64_t)gridDim.x * kThreads) {
+        if (p.o0) st(p.o0, i, 0.f, tag);
+        if (p.o1) st(p.o1, i, 0.f, tag);
+        if (p.o2) st(p.o2, i, 0.f, tag);
+    }
+}
+
+template <typename W, int FORM, int BM>
+__global__ void __launch_bounds__(kThreads) grouped_simt_kernel(const SimtParams p) {
+    using C = Cfg<W, FORM, BM>;
+    constexpr int kR = BM / 8;  // rows of a lane
+    constexpr bool kF32 = sizeof(W) == 4;
+    extern __shared__ __align__(16) float stages[];
+    __shared__ int row_s[kTrainMaxExperts + 1], tile_s[kTrainMaxExperts + 1];
+    const W* tag = nullptr;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    grid_dep_wait();
+    const int n_cols = C::kNT ? p.I : p.d;
+    constexpr int kCols = FORM == kFormUp ? kBN / 2 : kBN;  // output columns of a tile
+    const int nt = (n_cols + kCols - 1) / kCols;
+    const int n_mat = FORM == kFormDw && p.o1 ? 2 : 1;
+    const int mt_w = (p.I + BM - 1) / BM;
+    count_tiles(p, row_s, tile_s,
+                [&](int rows) { return FORM == kFormDw ? n_mat * mt_w * nt : (rows + BM - 1) / BM * nt; });
     for (int tile = blockIdx.x; tile < tile_s[p.N]; tile += gridDim.x) {
-        int lo = 0, hi = p.N;  // the last expert whose tiles start at or before this one
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (tile_s[mid] <= tile) lo = mid;
-            else hi = mid;
-        }
-        const int e = lo, row0 = row_s[e], rows = max(row_s[e + 1] - row0, 0);
+        const int e = expert_of(tile_s, p.N, tile), row0 = row_s[e], rows = max(row_s[e + 1] - row0, 0);
         int local = tile - tile_s[e];
         const int mts = FORM == kFormDw ? mt_w : (rows + BM - 1) / BM;
         const int mat = local / (mts * nt);
@@ -258,36 +296,160 @@ __global__ void __launch_bounds__(kThreads) grouped_simt_kernel(const SimtParams
                 const int n = n0 + (C::kNT ? lane + 32 * j : lane * 4 + j);
                 if (n >= n_cols) continue;
                 const float c = acc[i][j];
-                if constexpr (FORM == kFormUp) {
-                    const int64_t at = (int64_t)(row0 + m) * p.I + n;
-                    const float u = acc[i][j + 2];
-                    if (p.o0) { st(p.o0, at, c, tag); st(p.o1, at, u, tag); }
-                    st(p.o2, at, c * sigmoid(c) * u, tag);
-                } else if constexpr (FORM == kFormDh) {
-                    const int64_t at = (int64_t)(row0 + m) * p.I + n;
-                    const float g = ld(p.g, at, tag), u = ld(p.u, at, tag), sg = sigmoid(g);
-                    st(p.o0, at, c * u * sg * (1.f + g * (1.f - sg)), tag);
-                    st(p.o1, at, c * g * sg, tag);
-                } else if constexpr (FORM == kFormDw) {
+                if constexpr (FORM == kFormDw) {
                     const int64_t at = w0 + (int64_t)m * p.d + n;
                     void* o = mat ? p.o1 : p.o0;
                     if (p.out_f32) {
                         float* f = static_cast<float*>(o) + at;
                         *f = p.accumulate ? *f + c : c;
                     } else st(o, at, c, tag);
-                } else st(p.o0, (int64_t)(row0 + m) * p.d + n, c, tag);
+                } else emit<W, FORM>(p, row0 + m, n, c, FORM == kFormUp ? acc[i][j + (FORM == kFormUp ? 2 : 0)] : 0.f);
             }
         }
     }
-    if constexpr (FORM != kFormDw) {  // rows of no expert
-        const int64_t first = (int64_t)row_s[p.N] * n_cols, last = (int64_t)p.M * n_cols;
-        for (int64_t i = first + (int64_t)blockIdx.x * kThreads + tid; i < last; i += (int64_t)gridDim.x * kThreads) {
-            if (p.o0) st(p.o0, i, 0.f, tag);
-            if (p.o1) st(p.o1, i, 0.f, tag);
-            if (p.o2) st(p.o2, i, 0.f, tag);
+    if constexpr (FORM != kFormDw) zero_rest<W>(p, row_s[p.N], n_cols);
+    grid_dep_launch();
+}
+
+// ---------------------------------------------------------------- few rows an expert
+// Eight rows against weights that are read once, straight into registers, each
+// value for eight FMAs: a stream of the weights, where the tiles above spend
+// their time on shared memory.  16 tokens of the tiny layer: Up 10.9 -> 7.9 us
+// (the call's host time is 6.5), Dx 34 -> 10.5; 32 tokens of d 511, I 301 in
+// bf16, Up 36 -> 7.6.  Bound: the loads' latency, a block an SM (4 rows an
+// expert at d = I = 1024, Dh: 25 us for 67 MB, 0.39 of the copy bandwidth).
+// The rows wait in shared memory, kFewK values of K at a time.
+//   K contiguous (Up, Dh): a warp owns eight rows of the weights (Up: four of
+//   either matrix), a lane every 32nd group of four values of K; the 64 sums
+//   of a warp are added over its lanes by a halving exchange that leaves two to
+//   a lane, in Up the g and u of one channel.
+//   columns contiguous (Down, Dx): a half-warp owns every 16th value of K, a
+//   lane four columns; the sixteen sums of an output are added in order.
+constexpr int kFewRows = 8, kFewK = 512;
+
+// four values of a weight row from i on; `left` of the row are there (VEC: none or four at least)
+template <typename W, bool VEC>
+__device__ __forceinline__ void load4(const void* p, int64_t i, int left, float (&v)[4]) {
+    const W* tag = nullptr;
+    if constexpr (VEC) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (left > 0) x = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = j < left ? ld(p, i + j, tag) : 0.f;
+    }
+}
+
+template <typename W, int FORM, bool VEC>
+__global__ void __launch_bounds__(kThreads) grouped_few_kernel(const SimtParams p) {
+    constexpr bool kNT = FORM == kFormUp || FORM == kFormDh;
+    constexpr int kCols = FORM == kFormUp ? 32 : 64, kParts = FORM == kFormDx ? 2 : 1;
+    constexpr int kSums = kThreads / 16;  // of an output (columns contiguous)
+    __shared__ __align__(16) float sm[kNT ? kFewK * kFewRows : kSums * kFewRows * kCols];  // the rows, then the sums
+    static_assert(kSums * kFewRows * 64 >= kFewK * kFewRows, "room for the rows");
+    __shared__ int row_s[kTrainMaxExperts + 1], tile_s[kTrainMaxExperts + 1];
+    const W* tag = nullptr;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int n_cols = kNT ? p.I : p.d, K = kNT ? p.d : p.I, nt = (n_cols + kCols - 1) / kCols;
+    grid_dep_wait();
+    count_tiles(p, row_s, tile_s, [&](int rows) { return (rows + kFewRows - 1) / kFewRows * nt; });
+    for (int tile = blockIdx.x; tile < tile_s[p.N]; tile += gridDim.x) {
+        const int e = expert_of(tile_s, p.N, tile), rows = max(row_s[e + 1] - row_s[e], 0);
+        const int local = tile - tile_s[e], mts = (rows + kFewRows - 1) / kFewRows;
+        const int m0 = local % mts * kFewRows, n0 = local / mts * kCols, n_rows = min(rows - m0, kFewRows);
+        const int64_t first = row_s[e] + m0, w0 = (int64_t)e * p.I * p.d;
+        float acc[kNT ? 64 : 32];  // [row][weight row] or [row][column]
+#pragma unroll
+        for (int i = 0; i < (kNT ? 64 : 32); ++i) acc[i] = 0.f;
+        for (int part = 0; part < kParts; ++part) {
+            const void *A = part ? p.a1 : p.a0, *B = part ? p.b1 : p.b0;
+            for (int k0 = 0; k0 < K; k0 += kFewK) {
+                const int kc = min(kFewK, K - k0);
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < kFewK * kFewRows / kThreads; ++j) {
+                    const int i = j * kThreads + tid, r = i / kFewK, k = i % kFewK;
+                    sm[kNT ? i : k * kFewRows + r] = r < n_rows && k < kc ? ld(A, (first + r) * K + k0 + k, tag) : 0.f;
+                }
+                __syncthreads();
+                if constexpr (kNT) {
+#pragma unroll 1
+                    for (int k = lane * 4; k < kc; k += 128) {
+                        float w[8][4];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const int n = n0 + (FORM == kFormUp ? warp * 4 + c / 2 : warp * 8 + c);
+                            load4<W, VEC>(FORM == kFormUp && c % 2 ? p.b1 : B, w0 + (int64_t)n * K + k0 + k,
+                                          n < n_cols ? kc - k : 0, w[c]);
+                        }
+#pragma unroll
+                        for (int r = 0; r < kFewRows; ++r) {
+                            const float4 x = *reinterpret_cast<const float4*>(sm + r * kFewK + k);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                acc[r * 8 + c] = fmaf(x.w, w[c][3], fmaf(x.z, w[c][2], fmaf(x.y, w[c][1], fmaf(x.x, w[c][0], acc[r * 8 + c]))));
+                        }
+                    }
+                } else {
+                    const int n = n0 + lane % 16 * 4;
+#pragma unroll 8
+                    for (int k = tid / 16; k < kc; k += kSums) {
+                        float w[4];
+                        load4<W, VEC>(B, w0 + (int64_t)(k0 + k) * p.d + n, n_cols - n, w);
+                        float x[kFewRows];
+                        *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(sm + k * kFewRows);
+                        *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(sm + k * kFewRows + 4);
+#pragma unroll
+                        for (int r = 0; r < kFewRows; ++r)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) acc[r * 4 + j] = fmaf(x[r], w[j], acc[r * 4 + j]);
+                    }
+                }
+            }
+        }
+        if constexpr (kNT) {
+            // lane L ends with sums 2 L and 2 L + 1: row L / 4
+#pragma unroll
+            for (int o = 16, n = 32; o > 0; o >>= 1, n >>= 1)
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    const float keep = lane & o ? acc[i + n] : acc[i], give = lane & o ? acc[i] : acc[i + n];
+                    acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+            const int r = lane / 4, n = n0 + warp * (FORM == kFormUp ? 4 : 8) + lane % 4 * (FORM == kFormUp ? 1 : 2);
+            if (r < n_rows && n < n_cols) emit<W, FORM>(p, first + r, n, acc[0], acc[1]);
+            if (FORM == kFormDh && r < n_rows && n + 1 < n_cols) emit<W, FORM>(p, first + r, n + 1, acc[1], 0.f);
+        } else {
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r)
+                *reinterpret_cast<float4*>(sm + (tid / 16 * kFewRows + r) * kCols + lane % 16 * 4) =
+                    make_float4(acc[r * 4], acc[r * 4 + 1], acc[r * 4 + 2], acc[r * 4 + 3]);
+            __syncthreads();
+            for (int i = tid; i < kFewRows * kCols; i += kThreads) {
+                const int r = i / kCols, n = n0 + i % kCols;
+                float c = 0.f;
+#pragma unroll
+                for (int q = 0; q < kSums; ++q) c += sm[q * kFewRows * kCols + i];
+                if (r < n_rows && n < n_cols) emit<W, FORM>(p, first + r, n, c, 0.f);
+            }
         }
     }
+    zero_rest<W>(p, row_s[p.N], n_cols);
     grid_dep_launch();
+}
+
+template <typename W, int FORM>
+cudaError_t launch_few(const GroupedArgs& a, const SimtParams& p, cudaStream_t stream) {
+    constexpr int kCols = FORM == kFormUp ? 32 : 64;
+    const int64_t nt = ((FORM == kFormUp || FORM == kFormDh ? a.I : a.d) + kCols - 1) / kCols;
+    int64_t tiles = ((int64_t)a.M / kFewRows + (a.N < a.M ? a.N : a.M)) * nt;
+    if (tiles > (int64_t)a.sms * 8) tiles = (int64_t)a.sms * 8;
+    const dim3 grid((unsigned)(tiles < 1 ? 1 : tiles));
+    if constexpr (sizeof(W) == 4)
+        if (p.vec) return launch_pdl(grouped_few_kernel<W, FORM, true>, grid, dim3(kThreads), 0, stream, p);
+    return launch_pdl(grouped_few_kernel<W, FORM, false>, grid, dim3(kThreads), 0, stream, p);
 }
 
 template <typename W, int FORM, int BM>
@@ -307,8 +469,17 @@ cudaError_t launch_tiles(const GroupedArgs& a, const SimtParams& p, cudaStream_t
 
 template <typename W, int FORM>
 cudaError_t launch_form(const GroupedArgs& a, const SimtParams& p, cudaStream_t stream) {
-    // Dw's tile rows are channels, of which there are many
-    if (FORM != kFormDw && (int64_t)a.M <= 24LL * a.N) return launch_tiles<W, FORM, 16>(a, p, stream);
+    // Dw's tile rows are channels, of which there are many.  Of the others, few rows an expert: fp32 at
+    // d = I = 1024, 16 experts, few against 16-row tiles, us, at 4, 8 and 16 rows: Up 47 60, 59 60, 96 76; Dx 49 73,
+    // 90 73, 125 118; Dh 25 53, 36 43, 56 66; 64-row tiles pass the 16-row ones at 40 rows (Up 119 both, at 16 rows
+    // 119 against 79).  Without 16-byte loads, against 64-row tiles, at 25, 64 and 128 rows of d 511, I 301: Up 14 60,
+    // 34 61, 60 62; Dx 20 63, 39 64, 69 64.
+    if constexpr (FORM != kFormDw) {
+        const int few = !p.vec ? 96 : FORM == kFormDh ? 16 : 6;
+        if ((int64_t)a.M <= (int64_t)few * a.N) return launch_few<W, FORM>(a, p, stream);
+        if constexpr (sizeof(W) == 4)
+            if (p.vec && (int64_t)a.M <= 24LL * a.N) return launch_tiles<W, FORM, 16>(a, p, stream);
+    }
     return launch_tiles<W, FORM, 64>(a, p, stream);
 }
 
