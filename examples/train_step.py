@@ -102,9 +102,10 @@ class TrainLayer:
 
 def train(layer="tiny", tokens=64, steps=20, lr=None, seed=0):
     """SGD on a fixed random linear target; the losses, step by step.  The
-    gradients grow with the width, so the default rate falls with it."""
+    gradients grow with the width, and the curvature with the width over the
+    tokens where these are few, so the default rate falls with both."""
     cfg = CONFIGS[layer]
-    lr = 300.0 / cfg.d if lr is None else lr
+    lr = 300.0 / cfg.d * min(1.0, 8.0 * tokens / cfg.d) if lr is None else lr
     L = TrainLayer(cfg, tokens, seed=seed)
     gen = torch.Generator("cuda").manual_seed(seed + 1)
     kind = L.out.dtype
