@@ -1,9 +1,13 @@
 // The router's gradient: from the gates of a token's slots back through the
 // (optional) renormalisation and the softmax to the logits, with the
 // load-balance loss.
-//   v_e  = sum of d gate over the token's slots on e  (renormalised gates:
-//          (dgate_s - sum_j dgate_j gate_j) / sum_j p_j)  +  c N f_e / T
+//   v_e  = sum of d gate over the token's slots on e  +  c N f_e / T
 //   dl_e = p_e (v_e - sum_j p_j v_j)
+// Renormalised gates w_s = p_s / sum_j p_j have a gradient of their own form:
+// through them dl_e gains sum over the slots on e of w_s (dgate_s - sum_j
+// dgate_j w_j), whose sum over e is zero, and v_e keeps the load's term alone.
+// The slots' sum may be as small as float32 goes, and 1 / 2^-128 is no float32
+// number, while the w_s are ordinary: only they are formed.
 //   loss = c N sum_e f_e P_e,  f_e = slots on e / (T k),  P_e = mean_t p_te
 // T x N floats in and out: latency decides at every size (16384 tokens of 40
 // experts, 6 MB: 14 us in two launches).  A warp owns a token, up to four at a
@@ -18,11 +22,11 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kBlocksPerSm = 4;
 
 struct GateParams {
     const float* prob; const int32_t* idx; const float* dgate;
-    int T, N, k, renorm, parts, rows_per_part;
+    int T, N, k, parts, rows_per_part;
     float balance;
     float *dlogits, *loss, *part;
 };
@@ -62,8 +66,10 @@ __global__ void __launch_bounds__(kThreads) gate_load_kernel(const GateParams p)
     grid_dep_launch();
 }
 
-template <int NV>  // experts per lane
-__global__ void __launch_bounds__(kThreads) gate_grad_kernel(const GateParams p) {
+// NV: experts per lane.  Four blocks an SM, which is the grid's size: where the compiler took 78 registers (NV 16)
+// a fourth of the blocks had to wait, and 16384 tokens of 500 experts took 71 us instead of 59.
+template <int NV, bool RENORM>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) gate_grad_kernel(const GateParams p) {
     extern __shared__ float gsm[];
     float* load = gsm;            // [N] c N f_e / T
     float* lterm = gsm + p.N;     // [N] f_e P_e
@@ -130,36 +136,52 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(const GateParams p)
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             if (my_e[u] < 0 || my_e[u] >= p.N) my_e[u] = -1, my_d[u] = 0.f;
-            else if (p.renorm) my_p[u] = p.prob[(t0 + u * stride) * p.N + my_e[u]];
+            else if (RENORM) my_p[u] = p.prob[(t0 + u * stride) * p.N + my_e[u]];
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            if (p.renorm) {
+            if (RENORM) {
                 const float total = warp_sum(my_p[u]);
-                const float inv = total > 0.f ? 1.f / total : 0.f;
-                const float mean = warp_sum(my_d[u] * (my_p[u] * inv));
-                my_d[u] = my_e[u] >= 0 ? (my_d[u] - mean) * inv : 0.f;
+                const float w = total > 0.f ? my_p[u] / total : 0.f;
+                const float mean = warp_sum(my_d[u] * w);
+                my_d[u] = w * (my_d[u] - mean);
             }
-            for (int s = 0; s < p.k; ++s) {
-                const int e = __shfl_sync(0xffffffffu, my_e[u], s);
-                const float dg = __shfl_sync(0xffffffffu, my_d[u], s);
+            // the slots' terms: into v (gates that are probabilities), or into dl itself (renormalised)
+            auto add_slots = [&] {
+                for (int s = 0; s < p.k; ++s) {
+                    const int e = __shfl_sync(0xffffffffu, my_e[u], s);
+                    const float dg = __shfl_sync(0xffffffffu, my_d[u], s);
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if (e == i * 32 + lane) v[u][i] += dg;
-            }
+                    for (int i = 0; i < NV; ++i)
+                        if (e == i * 32 + lane) v[u][i] += dg;
+                }
+            };
+            if (!RENORM) add_slots();
             float dot = 0.f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) dot = fmaf(q[u][i], v[u][i], dot);
             dot = warp_sum(dot);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) v[u][i] = q[u][i] * (v[u][i] - dot);
+            if (RENORM) add_slots();
             const int64_t t = t0 + u * stride;
             if (t < p.T) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
-                    if (i * 32 + lane < p.N) p.dlogits[t * p.N + i * 32 + lane] = q[u][i] * (v[u][i] - dot);
+                    if (i * 32 + lane < p.N) p.dlogits[t * p.N + i * 32 + lane] = v[u][i];
             }
         }
     }
     grid_dep_launch();
+}
+
+template <bool RENORM>
+cudaError_t launch_grad(const GateParams& p, int nv, dim3 grid, size_t smem, cudaStream_t st) {
+    return nv <= 1 ? launch_pdl(gate_grad_kernel<1, RENORM>, grid, dim3(kThreads), smem, st, p)
+         : nv <= 2 ? launch_pdl(gate_grad_kernel<2, RENORM>, grid, dim3(kThreads), smem, st, p)
+         : nv <= 4 ? launch_pdl(gate_grad_kernel<4, RENORM>, grid, dim3(kThreads), smem, st, p)
+         : nv <= 8 ? launch_pdl(gate_grad_kernel<8, RENORM>, grid, dim3(kThreads), smem, st, p)
+                   : launch_pdl(gate_grad_kernel<16, RENORM>, grid, dim3(kThreads), smem, st, p);
 }
 
 }  // namespace
@@ -167,7 +189,7 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(const GateParams p)
 cudaError_t launch_gate_grad(const GateGradArgs& a, cudaStream_t st, int* launches) {
     GateParams p;
     p.prob = a.prob; p.idx = a.idx; p.dgate = a.dgate;
-    p.T = a.T; p.N = a.N; p.k = a.k; p.renorm = a.renorm; p.balance = a.balance;
+    p.T = a.T; p.N = a.N; p.k = a.k; p.balance = a.balance;
     p.dlogits = a.dlogits; p.loss = a.loss; p.part = a.part;
     p.parts = 0; p.rows_per_part = 0;
     *launches = 1;
@@ -183,15 +205,11 @@ cudaError_t launch_gate_grad(const GateGradArgs& a, cudaStream_t st, int* launch
         *launches = 2;
     }
     int64_t blocks = ((int64_t)a.T + kWarps - 1) / kWarps;
-    if (blocks > (int64_t)a.sms * 4) blocks = (int64_t)a.sms * 4;
+    if (blocks > (int64_t)a.sms * kBlocksPerSm) blocks = (int64_t)a.sms * kBlocksPerSm;
     const dim3 grid((unsigned)blocks);
     const size_t smem = (size_t)a.N * 2 * 4 * (p.parts > 0 ? 9 : 1);
     const int nv = (a.N + 31) / 32;
-    return nv <= 1 ? launch_pdl(gate_grad_kernel<1>, grid, dim3(kThreads), smem, st, p)
-         : nv <= 2 ? launch_pdl(gate_grad_kernel<2>, grid, dim3(kThreads), smem, st, p)
-         : nv <= 4 ? launch_pdl(gate_grad_kernel<4>, grid, dim3(kThreads), smem, st, p)
-         : nv <= 8 ? launch_pdl(gate_grad_kernel<8>, grid, dim3(kThreads), smem, st, p)
-                   : launch_pdl(gate_grad_kernel<16>, grid, dim3(kThreads), smem, st, p);
+    return a.renorm ? launch_grad<true>(p, nv, grid, smem, st) : launch_grad<false>(p, nv, grid, smem, st);
 }
 
 }  // namespace moe
