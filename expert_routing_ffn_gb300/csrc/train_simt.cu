@@ -47,7 +47,12 @@ __device__ __forceinline__ void st(void* p, int64_t i, float v, const __nv_bfloa
     static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
-__device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + expf(-g)); }
+// 1 / (1 + e^-g) = e^g / (1 + e^g), of the two the one whose exponential is at most 1: e^-g is infinite from
+// g = -88.73 on, where h, dg and du are still numbers of the type
+__device__ __forceinline__ float sigmoid(float g) {
+    const float e = expf(-fabsf(g));
+    return (g < 0.f ? e : 1.f) / (1.f + e);
+}
 
 // 16 or 4 bytes global -> shared, zeros where `in` is false (nothing is read then)
 __device__ __forceinline__ void copy16(float* dst, const float* src, bool in) {

@@ -115,10 +115,16 @@ struct RowsParams {
     MapParams dw;             // the maps of the weight gradients that follow this kernel
 };
 
-// 1 / (1 + e^-g) with the fast exponential and division (a few ulp in fp32;
-// the results are rounded to bf16).  e^-g overflows to infinity for very
-// negative g and 1 / (1 + inf) = 0, the limit.
-__device__ __forceinline__ float fast_sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+// 1 / (1 + e^-g) = e^g / (1 + e^g), of the two the one whose exponential is
+// at most 1: from g = -87.34 on (e^-g past 2^126) the first form is flushed
+// to zero, where h, dg and du are still bf16 numbers.  The fast exponential is
+// within 2 + 1.173 |g| ulp of float32 (documented), 105 at |g| = 88, and the
+// fast division within 2; bf16 rounds at 2^15 ulp.  Below 2^-126 a sigmoid has
+// float32's absolute spacing of 2^-149, and below g = -104 it is zero.
+__device__ __forceinline__ float fast_sigmoid(float g) {
+    const float e = __expf(-fabsf(g));
+    return __fdividef(g < 0.f ? e : 1.f, 1.f + e);
+}
 
 __device__ __forceinline__ uint32_t pack_f(uint32_t lo, uint32_t hi) {
     return pack_bf16x2(__uint_as_float(lo), __uint_as_float(hi));
