@@ -6,8 +6,10 @@ Argument marshalling only, like the package's other calls: every function
 checks dtype, device, layout and size, then calls the C function of the same
 name.  Outputs are the caller's buffers.  Tensors of token rows ([T, d]: x,
 dx, out, dout, add) may have any row stride with contiguous columns; all
-others are contiguous.  The tensors belong to the stream the call is queued
-on: order other streams' work on them with events, as for any kernel.
+others are contiguous.  A call runs on the current CUDA device, where all its
+tensors (and the stream, where one is given) have to be; others are refused.
+The tensors belong to the stream the call is queued on: order other streams'
+work on them with events, as for any kernel.
 """
 from __future__ import annotations
 
@@ -40,11 +42,21 @@ _F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
 _WTYPE = {MOE_DTYPE_F32: torch.float32, MOE_DTYPE_BF16: torch.bfloat16}
 
 
-def _refuse(t, dtype, numel, name):
+def _here():
+    """The current CUDA device's index (-2: there is none)."""
+    try:
+        return torch._C._cuda_getDevice()
+    except RuntimeError:
+        return -2
+
+
+def _refuse(dev, t, dtype, numel, name):
     if t is None:
         raise ValueError(f"{name} is required")
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, but the call runs on the current device, cuda:{dev}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
@@ -52,23 +64,23 @@ def _refuse(t, dtype, numel, name):
     raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
 
 
-def _buf(t, dtype, numel, name, optional=False):
-    """Address of a contiguous CUDA tensor of at least numel elements (None -> None if optional)."""
+def _buf(dev, t, dtype, numel, name, optional=False):
+    """Address of a contiguous tensor of at least numel elements on device dev (None -> None if optional)."""
     try:
-        if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= numel:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= numel:
             return t.data_ptr()
     except AttributeError:
         if t is None and optional:
             return None
-    _refuse(t, dtype, numel, name)
+    _refuse(dev, t, dtype, numel, name)
 
 
-def _rows(t, dtype, T, d, name, optional=False):
+def _rows(dev, t, dtype, T, d, name, optional=False):
     """Address and row stride of token rows [T, d] (contiguous columns)."""
     if t is None and optional:
         return None, 0
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype:
-        _refuse(t, dtype, T * d, name)
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype:
+        _refuse(dev, t, dtype, T * d, name)
     shape = t.shape
     if len(shape) != 2 or shape[0] < T or shape[1] != d:
         raise ValueError(f"{name} has shape {tuple(shape)}, needs [{T}, {d}]")
@@ -82,14 +94,16 @@ def _rows(t, dtype, T, d, name, optional=False):
     return t.data_ptr(), ld
 
 
-def _queue(t, stream):
-    """The stream of a call: the given one, or the current one of the device of tensor t."""
+def _queue(dev, stream):
+    """The stream of a call: the given one, or the device's current one."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+        raise ValueError(f"the stream is of cuda:{stream.device_index}, but the current device is cuda:{dev}")
     return _stream(stream)
 
 
-def _grad_type(dims, a, b, names, numel):
+def _grad_type(dev, dims, a, b, names, numel):
     """Addresses of the weight gradients and their type code (both of wtype or both float32)."""
     given = [t for t in (a, b) if t is not None]
     if not given:
@@ -97,7 +111,7 @@ def _grad_type(dims, a, b, names, numel):
     dtype = given[0].dtype
     if dtype not in (_F32, _WTYPE[dims.wtype]):
         raise TypeError(f"{names[0]} has dtype {dtype}, expected {_WTYPE[dims.wtype]} or {_F32}")
-    pa, pb = (_buf(t, dtype, numel, n, True) for t, n in zip((a, b), names))
+    pa, pb = (_buf(dev, t, dtype, numel, n, True) for t, n in zip((a, b), names))
     return pa, pb, MOE_DTYPE_F32 if dtype is _F32 else MOE_DTYPE_BF16
 
 
@@ -115,65 +129,76 @@ def moe_experts_path(dims: moe_dims) -> str:
 
 def moe_dispatch_rows(dims, x, expert_idx, capacity, x_perm, expert_offsets, perm, inv_perm, ws, stream=None):
     """Sort the slots by expert and copy the token rows: x [T, d] -> x_perm [T*k, d]."""
-    T, d, wt, slots = dims.T, dims.d, _WTYPE[dims.wtype], dims.T * dims.k
-    px, ldx = _rows(x, wt, T, d, "x")
+    dev = _here()
+    T, d, wt = dims.T, dims.d, _WTYPE[dims.wtype]
+    slots = T * dims.k
+    px, ldx = _rows(dev, x, wt, T, d, "x")
     _check(lib().moe_dispatch_rows(
-        C.byref(dims), px, ldx, _buf(expert_idx, _I32, slots, "expert_idx"), int(capacity),
-        _buf(x_perm, wt, slots * d, "x_perm"), _buf(expert_offsets, _I32, dims.N + 1, "expert_offsets"),
-        _buf(perm, _I32, slots, "perm"), _buf(inv_perm, _I32, slots, "inv_perm"),
-        _buf(ws, _U8, 0, "ws"), ws.numel(), _queue(x, stream)), "moe_dispatch_rows")
+        dims, px, ldx, _buf(dev, expert_idx, _I32, slots, "expert_idx"), int(capacity),
+        _buf(dev, x_perm, wt, slots * d, "x_perm"), _buf(dev, expert_offsets, _I32, dims.N + 1, "expert_offsets"),
+        _buf(dev, perm, _I32, slots, "perm"), _buf(dev, inv_perm, _I32, slots, "inv_perm"),
+        _buf(dev, ws, _U8, 0, "ws"), ws.numel(), _queue(dev, stream)), "moe_dispatch_rows")
 
 
 def moe_dispatch_rows_grad(dims, dx_perm, inv_perm, add, dx, stream=None):
     """dx [T, d] = add + the sum of every token's rows of dx_perm [T*k, d]."""
-    T, d, wt, slots = dims.T, dims.d, _WTYPE[dims.wtype], dims.T * dims.k
-    padd, ldadd = _rows(add, wt, T, d, "add", True)
-    pdx, lddx = _rows(dx, wt, T, d, "dx")
+    dev = _here()
+    T, d, wt = dims.T, dims.d, _WTYPE[dims.wtype]
+    slots = T * dims.k
+    padd, ldadd = _rows(dev, add, wt, T, d, "add", True)
+    pdx, lddx = _rows(dev, dx, wt, T, d, "dx")
     _check(lib().moe_dispatch_rows_grad(
-        C.byref(dims), _buf(dx_perm, wt, slots * d, "dx_perm"), _buf(inv_perm, _I32, slots, "inv_perm"), padd, ldadd,
-        pdx, lddx, _queue(dx_perm, stream)), "moe_dispatch_rows_grad")
+        dims, _buf(dev, dx_perm, wt, slots * d, "dx_perm"), _buf(dev, inv_perm, _I32, slots, "inv_perm"), padd,
+        ldadd, pdx, lddx, _queue(dev, stream)), "moe_dispatch_rows_grad")
 
 
 def moe_combine_rows(dims, y_perm, gate, inv_perm, add, out, stream=None):
     """out [T, d] = add + the gate-weighted sum of every token's rows of y_perm [T*k, d]."""
-    T, d, wt, slots = dims.T, dims.d, _WTYPE[dims.wtype], dims.T * dims.k
-    padd, ldadd = _rows(add, wt, T, d, "add", True)
-    pout, ldout = _rows(out, wt, T, d, "out")
+    dev = _here()
+    T, d, wt = dims.T, dims.d, _WTYPE[dims.wtype]
+    slots = T * dims.k
+    padd, ldadd = _rows(dev, add, wt, T, d, "add", True)
+    pout, ldout = _rows(dev, out, wt, T, d, "out")
     _check(lib().moe_combine_rows(
-        C.byref(dims), _buf(y_perm, wt, slots * d, "y_perm"), _buf(gate, _F32, slots, "gate", True),
-        _buf(inv_perm, _I32, slots, "inv_perm"), padd, ldadd, pout, ldout, _queue(y_perm, stream)), "moe_combine_rows")
+        dims, _buf(dev, y_perm, wt, slots * d, "y_perm"), _buf(dev, gate, _F32, slots, "gate", True),
+        _buf(dev, inv_perm, _I32, slots, "inv_perm"), padd, ldadd, pout, ldout, _queue(dev, stream)), "moe_combine_rows")
 
 
 def moe_combine_rows_grad(dims, dout, y_perm, gate, inv_perm, dy_perm, dgate, stream=None):
     """dy_perm [T*k, d] and dgate [T, k] (either may be None) from dout [T, d]."""
-    T, d, wt, slots = dims.T, dims.d, _WTYPE[dims.wtype], dims.T * dims.k
-    pd, ldd = _rows(dout, wt, T, d, "dout")
+    dev = _here()
+    T, d, wt = dims.T, dims.d, _WTYPE[dims.wtype]
+    slots = T * dims.k
+    pd, ldd = _rows(dev, dout, wt, T, d, "dout")
     _check(lib().moe_combine_rows_grad(
-        C.byref(dims), pd, ldd, _buf(y_perm, wt, slots * d, "y_perm", dgate is None),
-        _buf(gate, _F32, slots, "gate", True), _buf(inv_perm, _I32, slots, "inv_perm"),
-        _buf(dy_perm, wt, slots * d, "dy_perm", True), _buf(dgate, _F32, slots, "dgate", True),
-        _queue(dout, stream)), "moe_combine_rows_grad")
+        dims, pd, ldd, _buf(dev, y_perm, wt, slots * d, "y_perm", dgate is None),
+        _buf(dev, gate, _F32, slots, "gate", True), _buf(dev, inv_perm, _I32, slots, "inv_perm"),
+        _buf(dev, dy_perm, wt, slots * d, "dy_perm", True), _buf(dev, dgate, _F32, slots, "dgate", True),
+        _queue(dev, stream)), "moe_combine_rows_grad")
 
 
 def moe_gate_grad(dims, router_prob, topk_idx, dgate, balance, dlogits, balance_loss, ws, stream=None):
     """dlogits [T, N] from dgate [T, k]; balance_loss [1] may be None."""
-    T, N, slots = dims.T, dims.N, dims.T * dims.k
+    dev = _here()
+    T, N = dims.T, dims.N
+    slots = T * dims.k
     _check(lib().moe_gate_grad(
-        C.byref(dims), _buf(router_prob, _F32, T * N, "router_prob"), _buf(topk_idx, _I32, slots, "topk_idx"),
-        _buf(dgate, _F32, slots, "dgate"), float(balance), _buf(dlogits, _F32, T * N, "dlogits"),
-        _buf(balance_loss, _F32, 1, "balance_loss", True), _buf(ws, _U8, 0, "ws"), ws.numel(), _queue(router_prob, stream)),
-        "moe_gate_grad")
+        dims, _buf(dev, router_prob, _F32, T * N, "router_prob"), _buf(dev, topk_idx, _I32, slots, "topk_idx"),
+        _buf(dev, dgate, _F32, slots, "dgate"), float(balance), _buf(dev, dlogits, _F32, T * N, "dlogits"),
+        _buf(dev, balance_loss, _F32, 1, "balance_loss", True), _buf(dev, ws, _U8, 0, "ws"), ws.numel(),
+        _queue(dev, stream)), "moe_gate_grad")
 
 
 def moe_experts_up(dims, x_perm, expert_offsets, w_gate, w_up, g, u, h, ws, stream=None):
     """g = x Wg^T, u = x Wu^T (both may be None), h = SiLU(g) u per expert's rows."""
+    dev = _here()
     d, I, wt, slots = dims.d, dims.I, _WTYPE[dims.wtype], dims.T * dims.k
     nw = dims.N * I * d
     _check(lib().moe_experts_up(
-        C.byref(dims), _buf(x_perm, wt, slots * d, "x_perm"), _buf(expert_offsets, _I32, dims.N + 1, "expert_offsets"),
-        _buf(w_gate, wt, nw, "w_gate"), _buf(w_up, wt, nw, "w_up"), _buf(g, wt, slots * I, "g", True),
-        _buf(u, wt, slots * I, "u", True), _buf(h, wt, slots * I, "h"), _buf(ws, _U8, 0, "ws"), ws.numel(),
-        _queue(x_perm, stream)), "moe_experts_up")
+        dims, _buf(dev, x_perm, wt, slots * d, "x_perm"), _buf(dev, expert_offsets, _I32, dims.N + 1, "expert_offsets"),
+        _buf(dev, w_gate, wt, nw, "w_gate"), _buf(dev, w_up, wt, nw, "w_up"), _buf(dev, g, wt, slots * I, "g", True),
+        _buf(dev, u, wt, slots * I, "u", True), _buf(dev, h, wt, slots * I, "h"), _buf(dev, ws, _U8, 0, "ws"), ws.numel(),
+        _queue(dev, stream)), "moe_experts_up")
 
 
 def moe_experts_up_grad(dims, dg, du, x_perm, expert_offsets, w_gate, w_up, dx_perm, dw_gate, dw_up, accumulate, ws,
@@ -181,36 +206,39 @@ def moe_experts_up_grad(dims, dg, du, x_perm, expert_offsets, w_gate, w_up, dx_p
     """dx_perm = dg Wg + du Wu (may be None); dw_gate = dg^T x, dw_up = du^T x
     [N, I, d] in the layer's type or float32 (both may be None).  accumulate
     adds to the float32 buffers."""
+    dev = _here()
     d, I, wt, slots = dims.d, dims.I, _WTYPE[dims.wtype], dims.T * dims.k
     nw = dims.N * I * d
-    pg, pu, gtype = _grad_type(dims, dw_gate, dw_up, ("dw_gate", "dw_up"), nw)
+    pg, pu, gtype = _grad_type(dev, dims, dw_gate, dw_up, ("dw_gate", "dw_up"), nw)
     _check(lib().moe_experts_up_grad(
-        C.byref(dims), _buf(dg, wt, slots * I, "dg"), _buf(du, wt, slots * I, "du"),
-        _buf(x_perm, wt, slots * d, "x_perm", pg is None), _buf(expert_offsets, _I32, dims.N + 1, "expert_offsets"),
-        _buf(w_gate, wt, nw, "w_gate", dx_perm is None), _buf(w_up, wt, nw, "w_up", dx_perm is None),
-        _buf(dx_perm, wt, slots * d, "dx_perm", True), pg, pu, gtype, int(bool(accumulate)),
-        _buf(ws, _U8, 0, "ws"), ws.numel(), _queue(dg, stream)), "moe_experts_up_grad")
+        dims, _buf(dev, dg, wt, slots * I, "dg"), _buf(dev, du, wt, slots * I, "du"),
+        _buf(dev, x_perm, wt, slots * d, "x_perm", pg is None), _buf(dev, expert_offsets, _I32, dims.N + 1, "expert_offsets"),
+        _buf(dev, w_gate, wt, nw, "w_gate", dx_perm is None), _buf(dev, w_up, wt, nw, "w_up", dx_perm is None),
+        _buf(dev, dx_perm, wt, slots * d, "dx_perm", True), pg, pu, gtype, int(bool(accumulate)),
+        _buf(dev, ws, _U8, 0, "ws"), ws.numel(), _queue(dev, stream)), "moe_experts_up_grad")
 
 
 def moe_experts_down(dims, h, expert_offsets, w_down, y_perm, ws, stream=None):
     """y_perm = h Wd per expert's rows."""
+    dev = _here()
     d, I, wt, slots = dims.d, dims.I, _WTYPE[dims.wtype], dims.T * dims.k
     _check(lib().moe_experts_down(
-        C.byref(dims), _buf(h, wt, slots * I, "h"), _buf(expert_offsets, _I32, dims.N + 1, "expert_offsets"),
-        _buf(w_down, wt, dims.N * I * d, "w_down"), _buf(y_perm, wt, slots * d, "y_perm"), _buf(ws, _U8, 0, "ws"),
-        ws.numel(), _queue(h, stream)), "moe_experts_down")
+        dims, _buf(dev, h, wt, slots * I, "h"), _buf(dev, expert_offsets, _I32, dims.N + 1, "expert_offsets"),
+        _buf(dev, w_down, wt, dims.N * I * d, "w_down"), _buf(dev, y_perm, wt, slots * d, "y_perm"),
+        _buf(dev, ws, _U8, 0, "ws"), ws.numel(), _queue(dev, stream)), "moe_experts_down")
 
 
 def moe_experts_down_grad(dims, dy_perm, h, g, u, expert_offsets, w_down, dg, du, dw_down, accumulate, ws, stream=None):
     """dg, du through h = SiLU(g) u (both may be None); dw_down = h^T dy
     [N, I, d] in the layer's type or float32 (may be None).  accumulate adds
     to the float32 buffer."""
+    dev = _here()
     d, I, wt, slots = dims.d, dims.I, _WTYPE[dims.wtype], dims.T * dims.k
     nw, skip = dims.N * I * d, dg is None and du is None
-    pw, _, gtype = _grad_type(dims, dw_down, None, ("dw_down", ""), nw)
+    pw, _, gtype = _grad_type(dev, dims, dw_down, None, ("dw_down", ""), nw)
     _check(lib().moe_experts_down_grad(
-        C.byref(dims), _buf(dy_perm, wt, slots * d, "dy_perm"), _buf(h, wt, slots * I, "h", pw is None),
-        _buf(g, wt, slots * I, "g", skip), _buf(u, wt, slots * I, "u", skip),
-        _buf(expert_offsets, _I32, dims.N + 1, "expert_offsets"), _buf(w_down, wt, nw, "w_down", skip),
-        _buf(dg, wt, slots * I, "dg", True), _buf(du, wt, slots * I, "du", True), pw, gtype, int(bool(accumulate)),
-        _buf(ws, _U8, 0, "ws"), ws.numel(), _queue(dy_perm, stream)), "moe_experts_down_grad")
+        dims, _buf(dev, dy_perm, wt, slots * d, "dy_perm"), _buf(dev, h, wt, slots * I, "h", pw is None),
+        _buf(dev, g, wt, slots * I, "g", skip), _buf(dev, u, wt, slots * I, "u", skip),
+        _buf(dev, expert_offsets, _I32, dims.N + 1, "expert_offsets"), _buf(dev, w_down, wt, nw, "w_down", skip),
+        _buf(dev, dg, wt, slots * I, "dg", True), _buf(dev, du, wt, slots * I, "du", True), pw, gtype, int(bool(accumulate)),
+        _buf(dev, ws, _U8, 0, "ws"), ws.numel(), _queue(dev, stream)), "moe_experts_down_grad")

@@ -2,7 +2,8 @@
  * moe_train.h — the MoE layer's training step: token rows moved by expert and
  * back, the router's gradient, and the experts' grouped products, each with
  * its gradient.  Conventions as in moe.h (status codes, caller-owned device
- * buffers, everything queued on the caller's stream, device-detected errors
+ * buffers, everything queued on the caller's stream, on the current device,
+ * to which stream and buffers have to belong; device-detected errors
  * in the workspace's error word, read by moe_check()).
  *
  * A slot (t, s) is one of token t's k choices; its expert is
