@@ -112,7 +112,8 @@ moe_status run_grouped(const GroupedArgs& a, const GroupedArgs* dw, void* stream
     return MOE_OK;
 }
 
-moe_status check_grads(const moe_dims* D, moe_dtype gtype, int accumulate) {
+// accumulate: into weight gradients that are there
+moe_status check_grads(const moe_dims* D, moe_dtype gtype, bool accumulate) {
     if (gtype != MOE_DTYPE_F32 && gtype != MOE_DTYPE_BF16) return MOE_ERR_UNSUPPORTED;
     if (gtype != MOE_DTYPE_F32 && gtype != D->wtype) return MOE_ERR_UNSUPPORTED;
     return accumulate && gtype != MOE_DTYPE_F32 ? MOE_ERR_UNSUPPORTED : MOE_OK;
@@ -256,7 +257,7 @@ moe_status moe_experts_up_grad(const moe_dims* dims, const void* dg, const void*
                                void* ws, size_t ws_bytes, void* stream) {
     TRAIN_TRY(check_dims(dims));
     TRAIN_TRY(check_ws(dims, ws, ws_bytes));
-    TRAIN_TRY(check_grads(dims, gtype, accumulate));
+    TRAIN_TRY(check_grads(dims, gtype, accumulate && (dw_gate || dw_up)));
     if (!words({expert_offsets}) || (dw_gate == nullptr) != (dw_up == nullptr)) return MOE_ERR_INVALID_ARG;
     if (dims->T > 0) for (const void* p : {dg, du}) TRAIN_TRY(check_rows(dims, p));
     if (dw_gate) {
@@ -282,7 +283,7 @@ moe_status moe_experts_down_grad(const moe_dims* dims, const void* dy_perm, cons
                                  size_t ws_bytes, void* stream) {
     TRAIN_TRY(check_dims(dims));
     TRAIN_TRY(check_ws(dims, ws, ws_bytes));
-    TRAIN_TRY(check_grads(dims, gtype, accumulate));
+    TRAIN_TRY(check_grads(dims, gtype, accumulate && dw_down));
     if (!words({expert_offsets}) || (dg == nullptr) != (du == nullptr)) return MOE_ERR_INVALID_ARG;
     if (dims->T > 0) TRAIN_TRY(check_rows(dims, dy_perm));
     if (dw_down) {

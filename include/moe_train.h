@@ -121,7 +121,7 @@ moe_status moe_experts_up(const moe_dims* dims, const void* x_perm, const int32_
  * dw_gate[e] = dg^T x, dw_up[e] = du^T x over expert e's rows (both or neither
  * NULL; an expert without rows gets zeros).  gtype: the type of dw_gate and
  * dw_up [N, I, d], wtype or float32.  accumulate != 0 adds to what they hold
- * (float32 only, UNSUPPORTED otherwise). */
+ * (float32 only, UNSUPPORTED otherwise; without them it says nothing). */
 moe_status moe_experts_up_grad(const moe_dims* dims, const void* dg, const void* du, const void* x_perm,
                                const int32_t* expert_offsets, const void* w_gate, const void* w_up,
                                void* dx_perm, void* dw_gate, void* dw_up, moe_dtype gtype, int accumulate,
