@@ -20,7 +20,6 @@ int device_sms();
 constexpr int kTrainMaxExperts = 512;
 constexpr int kTrainMaxTopK = 16;
 constexpr int kTrainMaxSlots = 1 << 24;
-constexpr size_t kTrainMaxWs = 16u << 20;
 
 // ---------------------------------------------------------------- token rows
 // Batches of up to kDispAlone slots are sorted in one launch, each block

@@ -36,7 +36,6 @@
 #include <cuda.h>
 
 #include <cstring>
-#include <mutex>
 
 #include "common.cuh"
 #include "tma.h"
