@@ -24,7 +24,8 @@ from workloads import CONFIGS  # noqa: E402
 
 class TrainLayer:
     """The weights of one MoE layer, the buffers of a step of T tokens, and the
-    step's calls.  Everything is allocated once; a step allocates nothing."""
+    step's calls.  The library's calls work in buffers allocated once; the plain
+    products around them (the router's linear map, the update) take their own."""
 
     def __init__(self, cfg, T, capacity=0, balance=0.01, renorm=True, seed=0, device="cuda"):
         self.cfg, self.T, self.capacity, self.balance = cfg, T, capacity, balance

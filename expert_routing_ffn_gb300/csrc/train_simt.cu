@@ -474,11 +474,12 @@ cudaError_t launch_tiles(const GroupedArgs& a, const SimtParams& p, cudaStream_t
 
 template <typename W, int FORM>
 cudaError_t launch_form(const GroupedArgs& a, const SimtParams& p, cudaStream_t stream) {
-    // Dw's tile rows are channels, of which there are many.  Of the others, few rows an expert: fp32 at
-    // d = I = 1024, 16 experts, few against 16-row tiles, us, at 4, 8 and 16 rows: Up 47 60, 59 60, 96 76; Dx 49 73,
-    // 90 73, 125 118; Dh 25 53, 36 43, 56 66; 64-row tiles pass the 16-row ones at 40 rows (Up 119 both, at 16 rows
-    // 119 against 79).  Without 16-byte loads, against 64-row tiles, at 25, 64 and 128 rows of d 511, I 301: Up 14 60,
-    // 34 61, 60 62; Dx 20 63, 39 64, 69 64.
+    // Dw's tile rows are channels, of which there are many.  Of the others, few rows an expert by the batch's
+    // average, dropped slots included; the limits were measured at one size with 16-byte loads and one without, and
+    // other sizes may cross over elsewhere.  fp32 at d = I = 1024, 16 experts, few against 16-row tiles, us, at 4, 8
+    // and 16 rows: Up 47 60, 59 60, 96 76; Dx 49 73, 90 73, 125 118; Dh 25 53, 36 43, 56 66; 64-row tiles pass the
+    // 16-row ones at 40 rows (Up 119 both, at 16 rows 119 against 79).  Without 16-byte loads, against 64-row tiles,
+    // at 25, 64 and 128 rows of d 511, I 301: Up 14 60, 34 61, 60 62; Dx 20 63, 39 64, 69 64.
     if constexpr (FORM != kFormDw) {
         const int few = !p.vec ? 96 : FORM == kFormDh ? 16 : 6;
         if ((int64_t)a.M <= (int64_t)few * a.N) return launch_few<W, FORM>(a, p, stream);

@@ -39,7 +39,7 @@
 //   many rows: the tensor pipe at the clock that the power limit leaves.
 //     1024 rows an expert, Up at d 4096, I 3584: 313 us, 1.54 PFLOP/s, 0.91 of
 //     the measured sustained bf16 rate; 4096 tokens of the Qwen2-57B shape,
-//     skewed, Up: 0.88 ms, 1.37 PFLOP/s.
+//     skewed, Up: 0.88-0.91 ms, 1.32-1.37 PFLOP/s.
 //   between: both.  384 rows an expert (DeepSeek-V2-Lite shape, 4096 tokens),
 //     Dx: 976 MB and 283 GFLOP take 144 and 146 us at the burst rates; 190 us
 //     measured (218 in long runs).  With every load served by L2 it takes 155,
@@ -262,9 +262,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
         // ---------------- loads (each CTA its own stages, on the leader's barrier)
         const uint32_t full0 = leader_address(&full[0]);
         // The rows are read for every tile of channels and by the products that follow: they stay in L2.  The
-        // weights of few rows pass through it once.  DeepSeek-V2-Lite shape, Up: 8 tokens 63.8 -> 61.6 us, 64
-        // tokens 111.5 -> 108.1; the weight gradients after Dx, 4096 tokens, 254 -> 246.  With many rows the
-        // weights are shared by row tiles, and any policy on them cost 2 %.
+        // weights of few rows pass through it once (those of an expert that has more than 64 rows in such a batch
+        // serve its other row tiles too; skewed batches were not measured apart).  DeepSeek-V2-Lite shape, Up: 8
+        // tokens 63.8 -> 61.6 us, 64 tokens 111.5 -> 108.1; the weight gradients after Dx, 4096 tokens, 254 -> 246.
+        // With many rows the weights are shared by row tiles, and any policy on them cost 2 %.
         const uint64_t keep = l2_evict_last_policy(), once = l2_evict_first_policy();
         int st = 0, it = 0;
         uint32_t phase = 1;
@@ -617,9 +618,9 @@ cudaError_t launch_grouped_rows_tc(const GroupedArgs& a, const GroupedArgs* dw, 
     const bool nt = a.form == kFormUp || a.form == kFormDh;
     const uint64_t d = (uint64_t)a.d, I = (uint64_t)a.I, M = (uint64_t)a.M;
     const uint64_t K = nt ? d : I, cols = nt ? I : d;
-    // Tiles of up to 64 rows leave room for 8 or 9 stages instead of 5 or 6, which is what a stream of
-    // weights wants: 48 rows an expert (DeepSeek-V2-Lite shape) took Up 121 us against 129 and Dh 73 against
-    // 77, 96 rows 149 against 132 and 92 against 84.
+    // By the batch's average rows an expert, dropped slots included.  Tiles of up to 64 rows leave room for 8 or 9
+    // stages instead of 5 or 6, which is what a stream of weights wants: 48 rows an expert (DeepSeek-V2-Lite
+    // shape) took Up 121 us against 129 and Dh 73 against 77, 96 rows 149 against 132 and 92 against 84.
     const bool few = (long long)a.M <= 48LL * a.N;
     const int max_n = few ? 64 : 256;
     const int span = a.form == kFormUp ? 128 : 256;

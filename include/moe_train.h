@@ -23,8 +23,8 @@
  *   moe_gate_grad                  -> dlogits, balance loss
  *   moe_dispatch_rows_grad         -> dx
  *
- * dims (moe_dims) as in moe.h, with the limits of these calls: d, I >= 1 of
- * any value, N <= 512, k <= 16, k <= N, T * k <= 2^24; n_shared, I_shared, r and
+ * dims (moe_dims) as in moe.h, with the limits of these calls: d and I of any
+ * value from 1 to 65536, N <= 512, k <= 16, k <= N, T * k <= 2^24; n_shared, I_shared, r and
  * delta_max are not looked at.  Rows (x, y_perm, h, weights, their gradients)
  * have the layer's type wtype (bf16 or float32); gates, router probabilities
  * and logits' gradients are float32; indices int32.  Sums run in float32 in an
@@ -87,7 +87,8 @@ moe_status moe_combine_rows(const moe_dims* dims, const void* y_perm, const floa
 
 /* Gradient of moe_combine_rows:
  *   dy_perm[inv_perm[t, s]] = gate[t, s] * dout[t] (NULL = skip), zero in the
- *   rows past the last expert's; dgate[t, s] = <dout[t], y_perm[inv_perm[t, s]]>,
+ *   rows past the last expert's (with moe_permute's inv_perm, whose -1 names no
+ *   row, those stay unwritten); dgate[t, s] = <dout[t], y_perm[inv_perm[t, s]]>,
  *   zero for a slot without an expert (NULL = skip; needs y_perm).  gate NULL
  *   = 1.  add's gradient is dout. */
 moe_status moe_combine_rows_grad(const moe_dims* dims, const void* dout, int64_t lddout, const void* y_perm,
