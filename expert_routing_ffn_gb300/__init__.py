@@ -642,6 +642,9 @@ def moe_testing_wait_timeout(ws, stream=None):
 from .layer import DeviceLayer, LayerBuffers  # noqa: E402,F401
 
 
-from .train import (moe_combine_rows, moe_combine_rows_grad, moe_dispatch_rows, moe_dispatch_rows_grad,  # noqa: E402
-                    moe_experts_down, moe_experts_down_grad, moe_experts_path, moe_experts_up, moe_experts_up_grad,
-                    moe_gate_grad, moe_train_workspace_size)
+from .train import (MOE_GATE_CHANNEL, MOE_GATE_FULL, MOE_GATE_NONE, MOE_GATE_TOKEN, make_block, moe_block,  # noqa: E402
+                    moe_block_out, moe_block_out_grad, moe_combine_rows, moe_combine_rows_grad,
+                    moe_combine_rows_grad_packed, moe_dispatch_rows, moe_dispatch_rows_grad, moe_experts_down,
+                    moe_experts_down_grad, moe_experts_down_grad_packed, moe_experts_path, moe_experts_up,
+                    moe_experts_up_grad, moe_experts_up_packed, moe_gate_grad, moe_norm_rows, moe_norm_rows_grad,
+                    moe_pack_rows, moe_packed_size, moe_train_workspace_size, moe_unpack_rows, packed_rows)

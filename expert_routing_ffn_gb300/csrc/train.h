@@ -72,6 +72,61 @@ struct GateGradArgs {
 };
 cudaError_t launch_gate_grad(const GateGradArgs& a, cudaStream_t st, int* launches);
 
+// ---------------------------------------------------------------- the block around the layer
+struct NormArgs {
+    const void* y; int64_t ldy; bool y_f32;  // NULL: a norm alone (x in residual, its norm in next)
+    const void* residual; int64_t ldr;
+    const void* gate; int gate_kind;         // moe_block_gate
+    const void *w_post, *w_next;             // NULL: zeros
+    void* out; int64_t ldo; void* next; int64_t ldn;
+    float *rstd_post, *rstd_next;
+    int T, d, post;
+    float eps, offset, scale;
+    bool bf16;
+    int sms;
+};
+cudaError_t launch_block_out(const NormArgs& a, cudaStream_t st);
+
+constexpr int kNormMaxParts = 1024;              // column sums of so many row groups
+constexpr size_t kNormPartBytes = 12u << 20;     // and in so much of the workspace
+// row groups whose column sums (two float32 [d]) the workspace holds
+inline int norm_parts(int T, int d) {
+    long long n = (long long)(kNormPartBytes / (8 * (size_t)d));
+    if (n > kNormMaxParts) n = kNormMaxParts;
+    return (int)(n < T ? n : T > 0 ? T : 1);
+}
+struct NormGradArgs {
+    const void* dout; int64_t lddout; const void* dnext; int64_t lddnext;  // either may be NULL
+    const void* y; int64_t ldy; bool y_f32;  // NULL: nothing of the branch is asked for
+    const void* out; int64_t ldo;            // the next norm's input (with dnext)
+    const void* gate; int gate_kind;
+    const void *w_post, *w_next;
+    const float *rstd_post, *rstd_next;
+    void* dresidual; int64_t lddr; void* dy; int64_t lddy;
+    void* dgate; void *dw_post, *dw_next;    // NULL: not asked for
+    int T, d, post;
+    float offset, scale;
+    bool bf16, grads_f32, accumulate;
+    float* part;                             // workspace: norm_parts x 2 x d
+    int sms;
+};
+cudaError_t launch_block_out_grad(const NormGradArgs& a, cudaStream_t st, int* launches);
+
+// ---------------------------------------------------------------- rows in 8 bits
+constexpr int kPackBlock = 32;
+inline int pack_blocks(int cols) { return (cols + kPackBlock - 1) / kPackBlock; }
+cudaError_t launch_pack_rows(int64_t rows, int cols, const void* x, int64_t ldx, bool bf16, int8_t* q, uint8_t* scale,
+                             int sms, cudaStream_t st);
+cudaError_t launch_unpack_rows(int64_t src_rows, int cols, const int8_t* q, const uint8_t* scale, const int32_t* index,
+                               int divisor, int64_t rows, void* out, int64_t ldo, bool bf16, int sms, cudaStream_t st);
+struct CombineRowsGradPackedArgs {
+    const void* dout; int64_t lddout; const int8_t* q; const uint8_t* scale; const float* gate; const int32_t* inv;
+    void* dy; float* dgate;
+    int T, k, d;
+    bool bf16;
+};
+cudaError_t launch_combine_rows_grad_packed(const CombineRowsGradPackedArgs& a, cudaStream_t st);
+
 // ---------------------------------------------------------------- grouped products
 enum TrainForm {
     kFormUp = 0,    // g, u, h from x
@@ -86,7 +141,10 @@ struct GroupedArgs {
     const void *a0, *a1;      // rows: [M, K] (Up: x; Down: h; Dh: dy; Dx: dg, du; Dw: [M, I], one or two)
     const void *b0, *b1;      // weights [N, I, d] (Up, Dx: gate, up; Down, Dh: down); Dw: b0 = rows [M, d]
     const void *g, *u;        // Dh: pre-activations [M, I]
-    void *o0, *o1, *o2;       // Up: g, u, h; Down: y; Dh: dg, du; Dx: dx; Dw: dW of a0, a1
+    void *o0, *o1, *o2;       // Up: g, u, h; Down: y; Dh: dg, du (packed: and h); Dx: dx; Dw: dW of a0, a1
+    bool packed;              // Up: g, u leave as packed rows, Dh: they come so; their scales
+    const uint8_t *gs, *us;   // Dh
+    uint8_t *s0, *s1;         // Up
     const int32_t* offsets;   // device [N + 1]
     int M, N, d, I;
     bool bf16, out_f32, accumulate;  // out_f32, accumulate: Dw

@@ -1,0 +1,122 @@
+// Building blocks of the block's norms (train_norm.cu, train_norm_grad.cu):
+// rows as vectors of E values a thread, and sums over a row's threads.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "train.h"
+
+namespace moe {
+namespace norm {
+
+constexpr int kMaxGroup = 512, kMaxGroupWarps = kMaxGroup / 32, kBlock = 256;
+
+struct None {};  // the type of a y that is not there
+
+// E consecutive values of type W, as they lie in memory
+template <typename W, int E>
+struct Raw {
+    static constexpr int kBytes = E * (int)sizeof(W), kVec = kBytes < 16 ? kBytes : 16, kN = kBytes / kVec;
+    uint4 v[(kBytes + 15) / 16];
+    __device__ __forceinline__ void load(const void* row, int i) {
+        const char* p = static_cast<const char*>(row) + (int64_t)i * kBytes;
+        if constexpr (kVec == 16) {
+#pragma unroll
+            for (int j = 0; j < kN; ++j) v[j] = reinterpret_cast<const uint4*>(p)[j];
+        } else if constexpr (kVec == 8) {
+            const uint2 t = *reinterpret_cast<const uint2*>(p);
+            v[0].x = t.x; v[0].y = t.y;
+        } else if constexpr (kVec == 4) v[0].x = *reinterpret_cast<const uint32_t*>(p);
+        else v[0].x = *reinterpret_cast<const uint16_t*>(p);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int j = 0; j < (kBytes + 15) / 16; ++j) v[j] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ uint32_t word(int i) const {
+        const uint4& q = v[i / 4];
+        return i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
+    }
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (sizeof(W) == 4) return __uint_as_float(word(i));
+        else return i % 2 ? bf16_hi(word(i / 2)) : bf16_lo(word(i / 2));
+    }
+};
+template <int E>
+struct Raw<None, E> {
+    __device__ __forceinline__ void load(const void*, int) {}
+    __device__ __forceinline__ void zero() {}
+    __device__ __forceinline__ float operator[](int) const { return 0.f; }
+};
+
+// values to vector i of a row, each rounded once
+template <typename W, int E>
+__device__ __forceinline__ void store(void* row, int i, const float (&f)[E]) {
+    if constexpr (!std::is_same_v<W, None>) {
+        char* p = static_cast<char*>(row) + (int64_t)i * E * (int)sizeof(W);
+        if constexpr (sizeof(W) == 4) {
+            if constexpr (E % 4 == 0) {
+#pragma unroll
+                for (int j = 0; j < E / 4; ++j)
+                    reinterpret_cast<float4*>(p)[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+            } else if constexpr (E == 2) *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+            else *reinterpret_cast<float*>(p) = f[0];
+        } else {
+            uint32_t w[(E + 1) / 2];
+#pragma unroll
+            for (int j = 0; j < E; j += 2) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(f[j], j + 1 < E ? f[j + 1 < E ? j + 1 : j] : 0.f);
+                w[j / 2] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            if constexpr (E == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+            else if constexpr (E == 2) *reinterpret_cast<uint32_t*>(p) = w[0];
+            else *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
+        }
+    }
+}
+
+// Sums over the threads of a row: a group of G threads (whole warps), beside
+// other groups of the block.  Every thread gets them, in an order that does not
+// change.  Two buffers: a group's barrier for one sum also frees the buffer of
+// the sum before it.
+struct Sums {
+    float (*buf)[kMaxGroupWarps][4];  // [2][warps][values], the group's own
+    int warps, warp, bar, threads, at;
+    __device__ __forceinline__ void sync() const { asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory"); }
+    template <int N>
+    __device__ __forceinline__ void sum(float (&v)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+        if (warps == 1) return;
+        float(*b)[4] = buf[at];
+        at ^= 1;
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) b[warp][i] = v[i];
+        sync();
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = 0.f;
+        for (int w = 0; w < warps; ++w)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += b[w][i];
+    }
+};
+
+// Threads of a row and rows of a block, for rows of n_vec vectors, `chunks` of
+// them a thread (0: as many as it takes).
+struct Shape {
+    int group, rows;
+    int threads() const { return group * rows; }
+};
+inline Shape shape_of(int n_vec, int chunks) {
+    Shape s;
+    const int per = 32 * (chunks > 0 ? chunks : 4);
+    s.group = 32 * ((n_vec + per - 1) / per);
+    if (s.group > kMaxGroup) s.group = kMaxGroup;  // with chunks > 0 the caller has seen to it
+    s.rows = s.group >= kBlock ? 1 : kBlock / s.group;
+    return s;
+}
+
+}  // namespace norm
+}  // namespace moe

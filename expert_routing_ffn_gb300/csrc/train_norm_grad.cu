@@ -1,0 +1,220 @@
+// The gradient of a block's end (norm, gate, residual scale, residual, next
+// norm) and of a norm alone.
+//
+// With xo = out b, g = dnext w_next', v = yn w_post' gate (post_norm) or y gate:
+//   D = dout + b g - xo c,       c = b mean(g xo)
+//   mean(D v) = mean((dout + b g) v) - c mean(xo v)
+// so the three sums of a row, of g xo, (dout + b g) v and xo v, are taken at
+// once; D and dy follow.  The error is that of D's own cancellation.
+//
+// Sums over the tokens: a group of threads that owns a row's columns takes
+// many rows and keeps two sums a column, of dnext xo and of D v without the
+// weights; dgate of a channel and dw_post are both multiples of the latter.
+// A second launch adds the groups' sums in their order.
+#include "train_norm.cuh"
+
+namespace moe {
+
+namespace {
+
+using namespace norm;
+
+struct BlockGradParams {
+    const char* dout; int64_t lddout; const char* dnext; int64_t lddnext;
+    const char* y; int64_t ldy; const char* out; int64_t ldo;
+    const void* gate; int gate_kind;
+    const void *w_post, *w_next;
+    const float *rstd_post, *rstd_next;
+    char* dr; int64_t lddr; char* dy; int64_t lddy;  // strides in bytes
+    void* dgate;
+    int T, d, n_vec, post, group, rows, columns;     // columns: sums over the tokens are asked for
+    float offset, scale;
+    float* part;                                     // [groups][2][d]
+};
+
+template <typename W, typename Y, int E>
+__global__ void __launch_bounds__(kMaxGroup) block_grad_kernel(const BlockGradParams p) {
+    constexpr bool kY = !std::is_same_v<Y, None>;
+    __shared__ float red[kBlock / 32][2][kMaxGroupWarps][4];
+    const int tid = threadIdx.x % p.group, grp = threadIdx.x / p.group;
+    Sums sums = {red[grp], p.group / 32, tid / 32, 1 + grp, p.group, 0};
+    grid_dep_wait();
+    const int64_t groups = (int64_t)gridDim.x * p.rows, first = (int64_t)blockIdx.x * p.rows + grp;
+    float *col_next = p.part + first * 2 * p.d, *col_post = col_next + p.d;
+    for (int64_t t = first; t < p.T; t += groups) {
+        const float a = kY && p.post ? p.rstd_post[t] : 1.f, b = p.dnext ? p.rstd_next[t] : 0.f;
+        const float gt = kY && p.gate_kind == MOE_GATE_TOKEN ? static_cast<const float*>(p.gate)[t] : 1.f;
+        struct Vector {
+            Raw<W, E> dout, dnext, xo, wn, wp, gate;
+            Raw<Y, E> y;
+        };
+        auto load = [&](int i, Vector& q) {
+            q.dout.zero(); q.dnext.zero(); q.xo.zero(); q.wn.zero(); q.wp.zero();
+            if (p.dout) q.dout.load(p.dout + t * p.lddout, i);
+            if (p.dnext) {
+                q.dnext.load(p.dnext + t * p.lddnext, i);
+                q.xo.load(p.out + t * p.ldo, i);
+                if (p.w_next) q.wn.load(p.w_next, i);
+            }
+            if constexpr (kY) {
+                q.y.load(p.y + t * p.ldy, i);
+                if (p.w_post) q.wp.load(p.w_post, i);
+                if (p.gate_kind == MOE_GATE_CHANNEL) q.gate.load(p.gate, i);
+                if (p.gate_kind == MOE_GATE_FULL) q.gate.load(static_cast<const char*>(p.gate) + t * p.d * (int64_t)sizeof(W), i);
+            }
+        };
+        float s[3] = {0.f, 0.f, 0.f};
+        if (p.dnext || kY) {
+            for (int i = tid; i < p.n_vec; i += p.group) {
+                Vector q;
+                load(i, q);
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const float xo = q.xo[j] * b, g = q.dnext[j] * (p.offset + q.wn[j]);
+                    s[0] = fmaf(g, xo, s[0]);
+                    if constexpr (kY) {
+                        float v = q.y[j] * a;
+                        if (p.post) v *= p.offset + q.wp[j];
+                        if (p.gate_kind >= MOE_GATE_CHANNEL) v *= q.gate[j];
+                        s[1] = fmaf(fmaf(b, g, q.dout[j]), v, s[1]);
+                        s[2] = fmaf(xo, v, s[2]);
+                    }
+                }
+            }
+            sums.sum(s);
+        }
+        const float c = b * (s[0] / (float)p.d);
+        const float dv = s[1] - c * s[2];                        // sum D v
+        const float m = p.scale * gt * (dv / (float)p.d);        // mean(dp w_post' yn)
+        if (kY && p.gate_kind == MOE_GATE_TOKEN && p.dgate && tid == 0) static_cast<float*>(p.dgate)[t] = p.scale * dv;
+        for (int i = tid; i < p.n_vec; i += p.group) {
+            Vector q;
+            load(i, q);
+            float D[E], dyv[E], dg[E], cn[E], cp[E];
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const float xo = q.xo[j] * b, g = q.dnext[j] * (p.offset + q.wn[j]);
+                D[j] = fmaf(b, g, q.dout[j]) - xo * c;
+                cn[j] = q.dnext[j] * xo;
+                if constexpr (kY) {
+                    const float yn = q.y[j] * a, w = p.post ? p.offset + q.wp[j] : 1.f;
+                    const float gate = p.gate_kind >= MOE_GATE_CHANNEL ? q.gate[j] : gt, dq = p.scale * D[j];
+                    dg[j] = dq * yn * w;
+                    dyv[j] = dq * gate * w;
+                    if (p.post) dyv[j] = a * (dyv[j] - yn * m);
+                    cp[j] = D[j] * yn;
+                    if (p.gate_kind == MOE_GATE_TOKEN || p.gate_kind == MOE_GATE_FULL) cp[j] *= gate;
+                }
+            }
+            if (p.dr) store<W, E>(p.dr + t * p.lddr, i, D);
+            if constexpr (kY) {
+                if (p.dy) store<Y, E>(p.dy + t * p.lddy, i, dyv);
+                if (p.gate_kind == MOE_GATE_FULL && p.dgate)
+                    store<W, E>(static_cast<char*>(p.dgate) + t * p.d * (int64_t)sizeof(W), i, dg);
+            }
+            if (p.columns) {
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const int col = i * E + j;
+                    col_next[col] = t == first ? cn[j] : col_next[col] + cn[j];
+                    if constexpr (kY) col_post[col] = t == first ? cp[j] : col_post[col] + cp[j];
+                }
+            }
+        }
+    }
+    grid_dep_launch();
+}
+
+// The groups' sums of 32 columns, added by eight warps, each in the groups'
+// order, then in the warps'.
+struct ColumnParams {
+    const float* part;
+    int groups, d, gate_kind, post, accumulate;
+    float offset, scale;
+    const void *gate, *w_post;
+    void *dw_next, *dw_post, *dgate;  // dgate: of a channel
+};
+
+template <typename W, typename G>
+__global__ void __launch_bounds__(256) column_sums_kernel(const ColumnParams p) {
+    __shared__ float red[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane, which = blockIdx.y;
+    grid_dep_wait();
+    float s = 0.f;
+    if (col < p.d && (which || p.dw_next))
+#pragma unroll 8
+        for (int g = warp; g < p.groups; g += 8) s += __ldcg(p.part + ((int64_t)g * 2 + which) * p.d + col);
+    red[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && col < p.d) {
+        s = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) s += red[w][lane];
+        auto put = [&](void* to, float v) {
+            G* o = static_cast<G*>(to) + col;
+            if constexpr (sizeof(G) == 4) *o = p.accumulate ? *o + v : v;
+            else *o = __float2bfloat16_rn(v);
+        };
+        if (!which) {
+            if (p.dw_next) put(p.dw_next, s);
+        } else {
+            s *= p.scale;
+            if (p.dw_post) put(p.dw_post, p.gate_kind == MOE_GATE_CHANNEL ? s * to_f32(static_cast<const W*>(p.gate)[col]) : s);
+            if (p.dgate) put(p.dgate, p.post ? s * (p.offset + (p.w_post ? to_f32(static_cast<const W*>(p.w_post)[col]) : 0.f)) : s);
+        }
+    }
+    grid_dep_launch();
+}
+
+template <typename W, typename Y, int E>
+cudaError_t launch(BlockGradParams p, int parts, int sms, int* groups, cudaStream_t st) {
+    p.n_vec = p.d / E;
+    const Shape s = shape_of(p.n_vec, 0);
+    p.group = s.group; p.rows = s.rows;
+    int64_t blocks = ((int64_t)p.T + s.rows - 1) / s.rows, most = (int64_t)sms * 2;
+    if (p.columns && most > parts / s.rows) most = parts / s.rows;
+    if (most < 1) { most = 1; p.rows = 1; }
+    if (blocks > most) blocks = most;
+    const int64_t all = blocks * p.rows;
+    *groups = (int)(all < p.T ? all : p.T);
+    return launch_pdl(block_grad_kernel<W, Y, E>, dim3((unsigned)blocks), dim3(p.group * p.rows), 0, st, p);
+}
+
+}  // namespace
+
+cudaError_t launch_block_out_grad(const NormGradArgs& a, cudaStream_t st, int* launches) {
+    const int64_t es = a.bf16 ? 2 : 4, ys = a.y_f32 ? 4 : es;
+    BlockGradParams p;
+    p.dout = static_cast<const char*>(a.dout); p.lddout = a.lddout * es;
+    p.dnext = static_cast<const char*>(a.dnext); p.lddnext = a.lddnext * es;
+    p.y = static_cast<const char*>(a.y); p.ldy = a.ldy * ys;
+    p.out = static_cast<const char*>(a.out); p.ldo = a.ldo * es;
+    p.gate = a.gate; p.gate_kind = a.gate_kind; p.w_post = a.w_post; p.w_next = a.w_next;
+    p.rstd_post = a.rstd_post; p.rstd_next = a.rstd_next;
+    p.dr = static_cast<char*>(a.dresidual); p.lddr = a.lddr * es;
+    p.dy = static_cast<char*>(a.dy); p.lddy = a.lddy * ys;
+    const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
+    p.dgate = channel ? nullptr : a.dgate;
+    p.T = a.T; p.d = a.d; p.post = a.post; p.offset = a.offset; p.scale = a.scale; p.part = a.part;
+    p.columns = a.dw_post || a.dw_next || (channel && a.dgate);
+    const int parts = norm_parts(a.T, a.d);
+    int groups = 0;
+    *launches = 1;
+    cudaError_t e;
+    if (!a.bf16) e = a.y ? launch<float, float, 1>(p, parts, a.sms, &groups, st) : launch<float, None, 1>(p, parts, a.sms, &groups, st);
+    else if (!a.y) e = launch<__nv_bfloat16, None, 1>(p, parts, a.sms, &groups, st);
+    else if (a.y_f32) e = launch<__nv_bfloat16, float, 1>(p, parts, a.sms, &groups, st);
+    else e = launch<__nv_bfloat16, __nv_bfloat16, 1>(p, parts, a.sms, &groups, st);
+    if (e != cudaSuccess || !p.columns) return e;
+    ColumnParams c;
+    c.part = a.part; c.groups = groups; c.d = a.d; c.gate_kind = a.gate_kind; c.post = a.post; c.accumulate = a.accumulate;
+    c.offset = a.offset; c.scale = a.scale; c.gate = a.gate; c.w_post = a.w_post;
+    c.dw_next = a.dw_next; c.dw_post = a.dw_post; c.dgate = channel ? a.dgate : nullptr;
+    const dim3 grid((unsigned)((a.d + 31) / 32), a.y ? 2 : 1);
+    *launches = 2;
+    if (!a.bf16) return launch_pdl(column_sums_kernel<float, float>, grid, dim3(256), 0, st, c);
+    return a.grads_f32 ? launch_pdl(column_sums_kernel<__nv_bfloat16, float>, grid, dim3(256), 0, st, c)
+                       : launch_pdl(column_sums_kernel<__nv_bfloat16, __nv_bfloat16>, grid, dim3(256), 0, st, c);
+}
+
+}  // namespace moe

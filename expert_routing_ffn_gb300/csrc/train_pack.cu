@@ -1,0 +1,227 @@
+// Rows kept in 8 bits: packed, restored (and gathered), and read by the
+// combine's gradient.  The format stands in moe_train.h.
+//
+// The work is bytes.  A thread has eight columns of a row, four threads a
+// block of 32: its largest magnitude takes two shuffles, and the turn from
+// columns to the order of a matrix fragment two more.
+#include "pack8.cuh"
+#include "train.h"
+
+namespace moe {
+
+namespace {
+
+using namespace pack8;
+
+constexpr int kThreads = 256, kWarps = kThreads / 32, kCols = 256;  // columns of a warp
+
+struct PackParams {
+    const void* x; int64_t ldx;  // elements
+    int8_t* q; uint8_t* scale;
+    int64_t rows;
+    int cols, nb, pieces;        // pieces of kCols columns
+    const int32_t* index; int divisor;
+    int64_t src_rows;
+};
+
+template <typename W, bool VEC>
+__global__ void __launch_bounds__(kThreads) pack_rows_kernel(const PackParams p) {
+    const int lane = threadIdx.x & 31;
+    grid_dep_wait();
+    const int64_t items = p.rows * p.pieces;
+    for (int64_t it = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); it < items; it += (int64_t)gridDim.x * kWarps) {
+        const int64_t r = it / p.pieces;
+        const int c = (int)(it - r * p.pieces) * kCols + lane * 8;
+        float f[8];
+        load8<W, VEC>(static_cast<const W*>(p.x) + r * p.ldx, c, p.cols, f);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, magnitude(f[i]));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const uint32_t E = exponent(m);
+        const float inv = to_steps(E);
+        uint32_t b[8];
+        if (E == kTop)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = within(f[i], E);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = E == 255u ? 0u : quantise(f[i], inv);
+        const uint2 w = to_packed(bytes4(b[0], b[1], b[2], b[3]), bytes4(b[4], b[5], b[6], b[7]));
+        const int block = c / 32;
+        if (block < p.nb) {
+            const int64_t at = r * p.nb + block;
+            *reinterpret_cast<uint2*>(p.q + at * 32 + (lane & 3) * 8) = w;
+            if ((lane & 3) == 0) p.scale[at] = (uint8_t)E;
+        }
+    }
+    grid_dep_launch();
+}
+
+template <typename W, bool VEC>
+__global__ void __launch_bounds__(kThreads) unpack_rows_kernel(const PackParams p) {
+    const int lane = threadIdx.x & 31;
+    grid_dep_wait();
+    const int64_t items = p.rows * p.pieces;
+    for (int64_t it = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); it < items; it += (int64_t)gridDim.x * kWarps) {
+        const int64_t r = it / p.pieces;
+        const int c = (int)(it - r * p.pieces) * kCols + lane * 8, block = c / 32;
+        int64_t src = r;
+        if (p.index) {
+            const int i = p.index[r];
+            src = i < 0 ? -1 : i / p.divisor;
+        }
+        uint2 w = make_uint2(0, 0);
+        float s = 0.f;
+        if (src >= 0 && src < p.src_rows && block < p.nb) {
+            const int64_t at = src * p.nb + block;
+            w = *reinterpret_cast<const uint2*>(p.q + at * 32 + (lane & 3) * 8);
+            s = step(p.scale[at]);
+        }
+        w = to_columns(w);
+        const uint32_t lo = biased(w.x), hi = biased(w.y);
+        const float f[8] = {value<0>(lo) * s, value<1>(lo) * s, value<2>(lo) * s, value<3>(lo) * s,
+                            value<0>(hi) * s, value<1>(hi) * s, value<2>(hi) * s, value<3>(hi) * s};
+        store8<W, VEC>(static_cast<W*>(const_cast<void*>(p.x)) + r * p.ldx, c, p.cols, f);
+    }
+    grid_dep_launch();
+}
+
+// ---------------------------------------------------------------- combine, gradient
+// One block per token, as in combine_grad_kernel: dout's row once, every slot's
+// row of y in 8 bits for dgate, and its row of dy written.
+constexpr int kGradThreads = 128, kGradWarps = kGradThreads / 32;
+
+struct GradParams {
+    const void* dout; int64_t lddout; const int8_t* q; const uint8_t* scale; const float* gate; const int32_t* inv;
+    void* dy; float* dgate;
+    int k, n_rows, d, nb;
+};
+
+template <typename W, bool VEC, int KB>
+__global__ void __launch_bounds__(kGradThreads) combine_grad_packed_kernel(const GradParams p) {
+    __shared__ float part[kGradWarps][KB];
+    __shared__ int row_s[KB];
+    __shared__ float gate_s[KB];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t t = blockIdx.x;
+    grid_dep_wait();
+    if (tid < KB) {
+        int r = tid < p.k ? p.inv[t * p.k + tid] : -1;
+        if (r >= p.n_rows || r < -1 - p.n_rows) r = -1;  // out of range: no row
+        row_s[tid] = r;
+        gate_s[tid] = tid < p.k && p.gate ? p.gate[t * p.k + tid] : 1.f;
+    }
+    __syncthreads();
+    const W* dout = static_cast<const W*>(p.dout) + t * p.lddout;
+    float dot[KB];
+#pragma unroll
+    for (int s = 0; s < KB; ++s) dot[s] = 0.f;
+    for (int c0 = warp * kCols; c0 < p.d; c0 += kGradWarps * kCols) {
+        const int c = c0 + lane * 8, block = c / 32;
+        float g[8];
+        load8<W, VEC>(dout, c, p.d, g);
+#pragma unroll
+        for (int s = 0; s < KB; ++s) {
+            const int row = row_s[s];
+            if (row == -1) continue;
+            if (row >= 0 && p.dgate) {
+                uint2 w = make_uint2(0, 0);
+                float e = 0.f;
+                if (block < p.nb) {
+                    const int64_t at = (int64_t)row * p.nb + block;
+                    w = *reinterpret_cast<const uint2*>(p.q + at * 32 + (lane & 3) * 8);
+                    e = step(p.scale[at]);
+                }
+                w = to_columns(w);
+                const uint32_t lo = biased(w.x), hi = biased(w.y);
+                float v = g[0] * value<0>(lo);
+                v = fmaf(g[1], value<1>(lo), v); v = fmaf(g[2], value<2>(lo), v); v = fmaf(g[3], value<3>(lo), v);
+                v = fmaf(g[4], value<0>(hi), v); v = fmaf(g[5], value<1>(hi), v);
+                v = fmaf(g[6], value<2>(hi), v); v = fmaf(g[7], value<3>(hi), v);
+                dot[s] = fmaf(v, e, dot[s]);
+            }
+            if (p.dy) {
+                float f[8];
+                const float a = row >= 0 ? gate_s[s] : 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = row >= 0 ? a * g[i] : 0.f;
+                store8<W, VEC>(static_cast<W*>(p.dy) + (int64_t)(row >= 0 ? row : -2 - row) * p.d, c, p.d, f);
+            }
+        }
+    }
+    if (p.dgate) {
+#pragma unroll
+        for (int s = 0; s < KB; ++s) {
+            const float v = warp_sum(dot[s]);
+            if (lane == 0) part[warp][s] = v;
+        }
+        __syncthreads();
+        if (tid < p.k) {
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < kGradWarps; ++w) v += part[w][tid];
+            p.dgate[t * p.k + tid] = row_s[tid] >= 0 ? v : 0.f;
+        }
+    }
+    grid_dep_launch();
+}
+
+// rows that start on 16 bytes and hold whole vectors of them
+bool vectors(const void* p, int64_t ld, int cols, bool bf16) {
+    const int n = bf16 ? 8 : 4;
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % n == 0 && cols % n == 0;
+}
+
+unsigned pack_grid(int64_t items, int sms) {
+    const int64_t blocks = (items + kWarps - 1) / kWarps, most = (int64_t)sms * 8;
+    return (unsigned)(blocks < most ? blocks : most);
+}
+
+}  // namespace
+
+cudaError_t launch_pack_rows(int64_t rows, int cols, const void* x, int64_t ldx, bool bf16, int8_t* q, uint8_t* scale,
+                             int sms, cudaStream_t st) {
+    PackParams p = {};
+    p.x = x; p.ldx = ldx; p.q = q; p.scale = scale; p.rows = rows; p.cols = cols; p.nb = pack_blocks(cols);
+    p.pieces = (cols + kCols - 1) / kCols;
+    const dim3 grid(pack_grid(rows * p.pieces, sms)), block(kThreads);
+    const bool vec = vectors(x, ldx, cols, bf16);
+    if (bf16)
+        return vec ? launch_pdl(pack_rows_kernel<__nv_bfloat16, true>, grid, block, 0, st, p)
+                   : launch_pdl(pack_rows_kernel<__nv_bfloat16, false>, grid, block, 0, st, p);
+    return vec ? launch_pdl(pack_rows_kernel<float, true>, grid, block, 0, st, p)
+               : launch_pdl(pack_rows_kernel<float, false>, grid, block, 0, st, p);
+}
+
+cudaError_t launch_unpack_rows(int64_t src_rows, int cols, const int8_t* q, const uint8_t* scale, const int32_t* index,
+                               int divisor, int64_t rows, void* out, int64_t ldo, bool bf16, int sms, cudaStream_t st) {
+    PackParams p = {};
+    p.x = out; p.ldx = ldo; p.q = const_cast<int8_t*>(q); p.scale = const_cast<uint8_t*>(scale); p.rows = rows;
+    p.cols = cols; p.nb = pack_blocks(cols); p.pieces = (cols + kCols - 1) / kCols;
+    p.index = index; p.divisor = divisor; p.src_rows = src_rows;
+    const dim3 grid(pack_grid(rows * p.pieces, sms)), block(kThreads);
+    const bool vec = vectors(out, ldo, cols, bf16);
+    if (bf16)
+        return vec ? launch_pdl(unpack_rows_kernel<__nv_bfloat16, true>, grid, block, 0, st, p)
+                   : launch_pdl(unpack_rows_kernel<__nv_bfloat16, false>, grid, block, 0, st, p);
+    return vec ? launch_pdl(unpack_rows_kernel<float, true>, grid, block, 0, st, p)
+               : launch_pdl(unpack_rows_kernel<float, false>, grid, block, 0, st, p);
+}
+
+template <typename W, bool VEC>
+static cudaError_t launch_grad(const GradParams& p, int T, cudaStream_t st) {
+    return p.k <= 8 ? launch_pdl(combine_grad_packed_kernel<W, VEC, 8>, dim3(T), dim3(kGradThreads), 0, st, p)
+                    : launch_pdl(combine_grad_packed_kernel<W, VEC, 16>, dim3(T), dim3(kGradThreads), 0, st, p);
+}
+
+cudaError_t launch_combine_rows_grad_packed(const CombineRowsGradPackedArgs& a, cudaStream_t st) {
+    GradParams p;
+    p.dout = a.dout; p.lddout = a.lddout; p.q = a.q; p.scale = a.scale; p.gate = a.gate; p.inv = a.inv;
+    p.dy = a.dy; p.dgate = a.dgate; p.k = a.k; p.n_rows = a.T * a.k; p.d = a.d; p.nb = pack_blocks(a.d);
+    const bool vec = vectors(a.dout, a.lddout, a.d, a.bf16) && (!a.dy || vectors(a.dy, a.d, a.d, a.bf16));
+    if (a.bf16) return vec ? launch_grad<__nv_bfloat16, true>(p, a.T, st) : launch_grad<__nv_bfloat16, false>(p, a.T, st);
+    return vec ? launch_grad<float, true>(p, a.T, st) : launch_grad<float, false>(p, a.T, st);
+}
+
+}  // namespace moe

@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "pack8.cuh"
 #include "train.h"
 
 namespace moe {
@@ -32,8 +33,10 @@ constexpr int kThreads = 256, kBN = 128, kBK = 16, kPitch = kBK + 4, kStages = 3
 struct SimtParams {
     const void *a0, *a1, *b0, *b1, *g, *u;
     void *o0, *o1, *o2;
+    const uint8_t *gs, *us;  // PACKED: the scales of g, u (Dh) or of o0, o1 (Up)
+    uint8_t *s0, *s1;
     const int32_t* offsets;
-    int M, N, d, I;
+    int M, N, d, I, nb;      // nb: blocks of a packed row
     int out_f32, accumulate;
     int vec;  // fp32: every row of every operand starts on a 16-byte boundary
 };
@@ -115,33 +118,70 @@ __device__ __forceinline__ int expert_of(const int* tile_s, int N, int tile) {
     return lo;
 }
 // the products that give rows: value c (Up: g, and u) of a grouped row and a column
-template <typename W, int FORM>
+template <typename W, int FORM, bool PACKED>
 __device__ __forceinline__ void emit(const SimtParams& p, int64_t row, int n, float c, float u) {
     const W* tag = nullptr;
     if constexpr (FORM == kFormUp) {
+        static_assert(!PACKED, "a block at a time: emit_block");
         const int64_t at = row * p.I + n;
         if (p.o0) { st(p.o0, at, c, tag); st(p.o1, at, u, tag); }
         st(p.o2, at, c * sigmoid(c) * u, tag);
     } else if constexpr (FORM == kFormDh) {
         const int64_t at = row * p.I + n;
-        const float g = ld(p.g, at, tag), v = ld(p.u, at, tag), sg = sigmoid(g);
+        float g, v;
+        if constexpr (PACKED) {
+            g = pack8::value_at(static_cast<const int8_t*>(p.g), p.gs, row, n, p.nb);
+            v = pack8::value_at(static_cast<const int8_t*>(p.u), p.us, row, n, p.nb);
+        } else {
+            g = ld(p.g, at, tag);
+            v = ld(p.u, at, tag);
+        }
+        const float sg = sigmoid(g);
+        if constexpr (PACKED) st(p.o2, at, g * sg * v, tag);
         st(p.o0, at, c * v * sg * (1.f + g * (1.f - sg)), tag);
         st(p.o1, at, c * g * sg, tag);
     } else st(p.o0, row * p.d + n, c, tag);
 }
-// zeros for the rows of no expert
+// Up, PACKED: the g and u of one block of a row, a column a lane (zeros past the last column)
 template <typename W>
+__device__ __forceinline__ void emit_block(const SimtParams& p, int64_t row, int n, float g, float u) {
+    const W* tag = nullptr;
+    const int lane = threadIdx.x & 31;
+    if (n - lane >= p.I) return;  // the same for the warp
+    const int64_t at = row * p.nb + n / 32;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const float v = which ? u : g;
+        const uint32_t E = pack8::exponent(__reduce_max_sync(0xffffffffu, pack8::magnitude(v)));
+        int8_t* q = static_cast<int8_t*>(which ? p.o1 : p.o0) + at * 32;
+        q[4 * (lane & 7) + (lane >> 3)] = E == 255u ? 0 : (int8_t)pack8::quantise(pack8::within(v, E), pack8::to_steps(E));
+        if (lane == 0) (which ? p.s1 : p.s0)[at] = (uint8_t)E;
+    }
+    if (n < p.I) st(p.o2, row * p.I + n, g * sigmoid(g) * u, tag);
+}
+// zeros for the rows of no expert
+template <typename W, bool PACKED_UP>
 __device__ __forceinline__ void zero_rest(const SimtParams& p, int first_row, int n_cols) {
     const W* tag = nullptr;
     const int64_t first = (int64_t)first_row * n_cols, last = (int64_t)p.M * n_cols;
-    for (int64_t i = first + (int64_t)blockIdx.x * kThreads + threadIdx.x; i < last; i += (int64_t)gridDim.x * kThreads) {
-        if (p.o0) st(p.o0, i, 0.f, tag);
-        if (p.o1) st(p.o1, i, 0.f, tag);
+    const int64_t start = (int64_t)blockIdx.x * kThreads + threadIdx.x, step = (int64_t)gridDim.x * kThreads;
+    for (int64_t i = first + start; i < last; i += step) {
+        if (p.o0 && !PACKED_UP) st(p.o0, i, 0.f, tag);
+        if (p.o1 && !PACKED_UP) st(p.o1, i, 0.f, tag);
         if (p.o2) st(p.o2, i, 0.f, tag);
+    }
+    if constexpr (PACKED_UP) {
+        for (int64_t i = (int64_t)first_row * p.nb + start; i < (int64_t)p.M * p.nb; i += step) {
+            for (void* o : {p.o0, p.o1}) {
+                uint4* q = static_cast<uint4*>(o) + 2 * i;
+                q[0] = q[1] = make_uint4(0, 0, 0, 0);
+            }
+            p.s0[i] = p.s1[i] = 0;
+        }
     }
 }
 
-template <typename W, int FORM, int BM>
+template <typename W, int FORM, int BM, bool PACKED>
 __global__ void __launch_bounds__(kThreads) grouped_simt_kernel(const SimtParams p) {
     using C = Cfg<W, FORM, BM>;
     constexpr int kR = BM / 8;  // rows of a lane
@@ -299,6 +339,10 @@ __global__ void __launch_bounds__(kThreads) grouped_simt_kernel(const SimtParams
 #pragma unroll
             for (int j = 0; j < (FORM == kFormUp ? 2 : 4); ++j) {
                 const int n = n0 + (C::kNT ? lane + 32 * j : lane * 4 + j);
+                if constexpr (FORM == kFormUp && PACKED) {
+                    emit_block<W>(p, row0 + m, n, acc[i][j], acc[i][j + 2]);
+                    continue;
+                }
                 if (n >= n_cols) continue;
                 const float c = acc[i][j];
                 if constexpr (FORM == kFormDw) {
@@ -308,11 +352,12 @@ __global__ void __launch_bounds__(kThreads) grouped_simt_kernel(const SimtParams
                         float* f = static_cast<float*>(o) + at;
                         *f = p.accumulate ? *f + c : c;
                     } else st(o, at, c, tag);
-                } else emit<W, FORM>(p, row0 + m, n, c, FORM == kFormUp ? acc[i][j + (FORM == kFormUp ? 2 : 0)] : 0.f);
+                } else if constexpr (!(FORM == kFormUp && PACKED))
+                    emit<W, FORM, PACKED>(p, row0 + m, n, c, FORM == kFormUp ? acc[i][j + (FORM == kFormUp ? 2 : 0)] : 0.f);
             }
         }
     }
-    if constexpr (FORM != kFormDw) zero_rest<W>(p, row_s[p.N], n_cols);
+    if constexpr (FORM != kFormDw) zero_rest<W, FORM == kFormUp && PACKED>(p, row_s[p.N], n_cols);
     grid_dep_launch();
 }
 
@@ -346,7 +391,7 @@ __device__ __forceinline__ void load4(const void* p, int64_t i, int left, float 
     }
 }
 
-template <typename W, int FORM, bool VEC>
+template <typename W, int FORM, bool VEC, bool PACKED>
 __global__ void __launch_bounds__(kThreads) grouped_few_kernel(const SimtParams p) {
     constexpr bool kNT = FORM == kFormUp || FORM == kFormDh;
     constexpr int kCols = FORM == kFormUp ? 32 : 64, kParts = FORM == kFormDx ? 2 : 1;
@@ -423,8 +468,18 @@ __global__ void __launch_bounds__(kThreads) grouped_few_kernel(const SimtParams 
                     acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
                 }
             const int r = lane / 4, n = n0 + warp * (FORM == kFormUp ? 4 : 8) + lane % 4 * (FORM == kFormUp ? 1 : 2);
-            if (r < n_rows && n < n_cols) emit<W, FORM>(p, first + r, n, acc[0], acc[1]);
-            if (FORM == kFormDh && r < n_rows && n + 1 < n_cols) emit<W, FORM>(p, first + r, n + 1, acc[1], 0.f);
+            if constexpr (FORM == kFormUp && PACKED) {
+                // the tile is one block of 32 channels: a row a warp, through shared memory
+                static_assert(kCols == 32, "a block of packed values");
+                __syncthreads();
+                sm[r * 32 + n - n0] = acc[0];
+                sm[kFewRows * 32 + r * 32 + n - n0] = acc[1];
+                __syncthreads();
+                if (warp < n_rows) emit_block<W>(p, first + warp, n0 + lane, sm[warp * 32 + lane], sm[kFewRows * 32 + warp * 32 + lane]);
+            } else {
+                if (r < n_rows && n < n_cols) emit<W, FORM, PACKED>(p, first + r, n, acc[0], acc[1]);
+                if (FORM == kFormDh && r < n_rows && n + 1 < n_cols) emit<W, FORM, PACKED>(p, first + r, n + 1, acc[1], 0.f);
+            }
         } else {
             __syncthreads();
 #pragma unroll
@@ -437,15 +492,15 @@ __global__ void __launch_bounds__(kThreads) grouped_few_kernel(const SimtParams 
                 float c = 0.f;
 #pragma unroll
                 for (int q = 0; q < kSums; ++q) c += sm[q * kFewRows * kCols + i];
-                if (r < n_rows && n < n_cols) emit<W, FORM>(p, first + r, n, c, 0.f);
+                if (r < n_rows && n < n_cols) emit<W, FORM, PACKED>(p, first + r, n, c, 0.f);
             }
         }
     }
-    zero_rest<W>(p, row_s[p.N], n_cols);
+    zero_rest<W, FORM == kFormUp && PACKED>(p, row_s[p.N], n_cols);
     grid_dep_launch();
 }
 
-template <typename W, int FORM>
+template <typename W, int FORM, bool PACKED>
 cudaError_t launch_few(const GroupedArgs& a, const SimtParams& p, cudaStream_t stream) {
     constexpr int kCols = FORM == kFormUp ? 32 : 64;
     const int64_t nt = ((FORM == kFormUp || FORM == kFormDh ? a.I : a.d) + kCols - 1) / kCols;
@@ -453,13 +508,13 @@ cudaError_t launch_few(const GroupedArgs& a, const SimtParams& p, cudaStream_t s
     if (tiles > (int64_t)a.sms * 8) tiles = (int64_t)a.sms * 8;
     const dim3 grid((unsigned)(tiles < 1 ? 1 : tiles));
     if constexpr (sizeof(W) == 4)
-        if (p.vec) return launch_pdl(grouped_few_kernel<W, FORM, true>, grid, dim3(kThreads), 0, stream, p);
-    return launch_pdl(grouped_few_kernel<W, FORM, false>, grid, dim3(kThreads), 0, stream, p);
+        if (p.vec) return launch_pdl(grouped_few_kernel<W, FORM, true, PACKED>, grid, dim3(kThreads), 0, stream, p);
+    return launch_pdl(grouped_few_kernel<W, FORM, false, PACKED>, grid, dim3(kThreads), 0, stream, p);
 }
 
-template <typename W, int FORM, int BM>
+template <typename W, int FORM, int BM, bool PACKED>
 cudaError_t launch_tiles(const GroupedArgs& a, const SimtParams& p, cudaStream_t stream) {
-    auto kern = grouped_simt_kernel<W, FORM, BM>;
+    auto kern = grouped_simt_kernel<W, FORM, BM, PACKED>;
     constexpr int kSmem = Cfg<W, FORM, BM>::kSmem;
     cudaError_t e = allow_max_smem(kern);
     if (e != cudaSuccess) return e;
@@ -472,7 +527,7 @@ cudaError_t launch_tiles(const GroupedArgs& a, const SimtParams& p, cudaStream_t
                        launch_pdl(kern, dim3((unsigned)(tiles < 1 ? 1 : tiles)), dim3(kThreads), kSmem, stream, p));
 }
 
-template <typename W, int FORM>
+template <typename W, int FORM, bool PACKED = false>
 cudaError_t launch_form(const GroupedArgs& a, const SimtParams& p, cudaStream_t stream) {
     // Dw's tile rows are channels, of which there are many.  Of the others, few rows an expert by the batch's
     // average, dropped slots included; the limits were measured at one size with 16-byte loads and one without, and
@@ -482,19 +537,19 @@ cudaError_t launch_form(const GroupedArgs& a, const SimtParams& p, cudaStream_t 
     // at 25, 64 and 128 rows of d 511, I 301: Up 14 60, 34 61, 60 62; Dx 20 63, 39 64, 69 64.
     if constexpr (FORM != kFormDw) {
         const int few = !p.vec ? 96 : FORM == kFormDh ? 16 : 6;
-        if ((int64_t)a.M <= (int64_t)few * a.N) return launch_few<W, FORM>(a, p, stream);
+        if ((int64_t)a.M <= (int64_t)few * a.N) return launch_few<W, FORM, PACKED>(a, p, stream);
         if constexpr (sizeof(W) == 4)
-            if (p.vec && (int64_t)a.M <= 24LL * a.N) return launch_tiles<W, FORM, 16>(a, p, stream);
+            if (p.vec && (int64_t)a.M <= 24LL * a.N) return launch_tiles<W, FORM, 16, PACKED>(a, p, stream);
     }
-    return launch_tiles<W, FORM, 64>(a, p, stream);
+    return launch_tiles<W, FORM, 64, PACKED>(a, p, stream);
 }
 
 template <typename W>
 cudaError_t launch(const GroupedArgs& a, const SimtParams& p, cudaStream_t stream) {
     switch (a.form) {
-        case kFormUp: return launch_form<W, kFormUp>(a, p, stream);
+        case kFormUp: return a.packed ? launch_form<W, kFormUp, true>(a, p, stream) : launch_form<W, kFormUp>(a, p, stream);
         case kFormDown: return launch_form<W, kFormDown>(a, p, stream);
-        case kFormDh: return launch_form<W, kFormDh>(a, p, stream);
+        case kFormDh: return a.packed ? launch_form<W, kFormDh, true>(a, p, stream) : launch_form<W, kFormDh>(a, p, stream);
         case kFormDx: return launch_form<W, kFormDx>(a, p, stream);
         case kFormDw: return launch_form<W, kFormDw>(a, p, stream);
     }
@@ -507,6 +562,7 @@ cudaError_t launch_grouped_simt(const GroupedArgs& a, cudaStream_t stream) {
     SimtParams p;
     p.a0 = a.a0; p.a1 = a.a1; p.b0 = a.b0; p.b1 = a.b1; p.g = a.g; p.u = a.u;
     p.o0 = a.o0; p.o1 = a.o1; p.o2 = a.o2; p.offsets = a.offsets;
+    p.gs = a.gs; p.us = a.us; p.s0 = a.s0; p.s1 = a.s1; p.nb = pack_blocks(a.I);
     p.M = a.M; p.N = a.N; p.d = a.d; p.I = a.I; p.out_f32 = a.out_f32; p.accumulate = a.accumulate;
     p.vec = !a.bf16 && a.d % 4 == 0 && a.I % 4 == 0;
     for (const void* q : {a.a0, a.a1, a.b0, a.b1}) p.vec = p.vec && (reinterpret_cast<uintptr_t>(q) & 15u) == 0;

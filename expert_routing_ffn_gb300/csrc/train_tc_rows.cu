@@ -576,7 +576,7 @@ bool grouped_tc_shapes(bool bf16, int d, int I) {
 }
 
 bool grouped_tc_usable(const GroupedArgs& a) {
-    if (!grouped_tc_shapes(a.bf16, a.d, a.I) || a.M == 0) return false;
+    if (!grouped_tc_shapes(a.bf16, a.d, a.I) || a.M == 0 || a.packed) return false;
     for (const void* q : {a.a0, a.a1, a.b0, a.b1, a.g, a.u, (const void*)a.o0, (const void*)a.o1, (const void*)a.o2})
         if (reinterpret_cast<uintptr_t>(q) & 15u) return false;
     return true;
