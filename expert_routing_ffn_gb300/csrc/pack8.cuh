@@ -37,10 +37,11 @@ __device__ __forceinline__ uint32_t quantise(float x, float inv) { return __floa
 
 // byte i of a word of packed values as a float: 2^23 + 128 + q has q + 128 in its low byte
 __device__ __forceinline__ uint32_t biased(uint32_t word) { return word ^ 0x80808080u; }
-template <int I>
-__device__ __forceinline__ float value(uint32_t biased_word) {
-    return __uint_as_float(__byte_perm(biased_word, 0x4b000000u, 0x7440 | I)) - 8388736.f;
+__device__ __forceinline__ float value(uint32_t biased_word, int i) {
+    return __uint_as_float(__byte_perm(biased_word, 0x4b000000u, 0x7440 | i)) - 8388736.f;
 }
+template <int I>
+__device__ __forceinline__ float value(uint32_t biased_word) { return value(biased_word, I); }
 
 __device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);

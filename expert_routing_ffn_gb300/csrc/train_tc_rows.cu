@@ -23,6 +23,14 @@
 // shared memory, in fp32.  In Dh g and u come in by TMA and ldmatrix in the
 // same layout, and dg, du overwrite them.
 //
+// PACKED: g and u are rows in 8 bits (the format stands in moe_train.h).  The
+// 32 lanes of a warp are one block of 32 channels, so a row's largest magnitude
+// takes three shuffles, and a thread's four channels of a row are one word of
+// the block: eight threads write (Up) or read (Dh) its 32 bytes straight from
+// registers, a whole sector, without shared memory.  Dh fetches a panel's words
+// while it waits for the accumulator or works on the panel before, and gives h
+// beside dg and du.
+//
 // The tiles of all experts form one list (expert by expert, row tiles
 // innermost: a weight tile read by several of them comes from L2 after the
 // first), taken round robin by the resident pairs; the tiles of the last,
@@ -62,6 +70,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "pack8.cuh"
 #include "tma.h"
 #include "train.h"
 #include "train_tc.cuh"
@@ -82,17 +91,17 @@ constexpr uint32_t kBox = kPanel * 128;  // 32 rows x 64 channels
 constexpr int kBoxHeights = 8;
 
 // MAXN: the most rows of a tile.
-template <int FORM, int MAXN>
+template <int FORM, int MAXN, bool PACKED>
 struct Cfg {
     static constexpr bool kNT = FORM == kFormUp || FORM == kFormDh;  // weights K-major
     static constexpr int kChannels = FORM == kFormUp ? 64 : 128;     // output channels of one CTA
-    static constexpr int kBoxes = FORM == kFormUp ? 3 : FORM == kFormDh ? 4 : 2;  // boxes of a panel
+    static constexpr int kBoxes = FORM == kFormUp ? (PACKED ? 1 : 3) : FORM == kFormDh ? (PACKED ? 6 : 4) : 2;  // boxes of a panel
     static constexpr uint32_t kStage = kStageA + MAXN / 2 * kBK * 2;
     static constexpr uint32_t kBuffer = kBoxes * kBox;
     // Panel buffers of a group.  Large tiles of Up have one, which costs a barrier a panel and leaves room for a
     // sixth stage: 384 rows an expert (DeepSeek-V2-Lite shape) 239 -> 231 us, 4096 tokens of the Qwen2-57B shape
     // 900 -> 880; 200 rows (Granite shape) 37.4 -> 38.6; 64-row tiles, which have eight stages, 110 -> 112.
-    static constexpr int kBuffers = FORM == kFormUp && MAXN == 256 ? 1 : 2;
+    static constexpr int kBuffers = PACKED ? (FORM == kFormDh ? 1 : 2) : FORM == kFormUp && MAXN == 256 ? 1 : 2;
     static constexpr uint32_t kSwap = FORM == kFormUp ? kGroupThreads * 32 : 0;  // a group's room to swap values
     static constexpr uint32_t kEpi = kGroups * (kBuffers * kBuffer + kSwap);
     static constexpr int kStages = (int)((224 * 1024 - kEpi) / kStage);
@@ -109,8 +118,10 @@ struct RowsParams {
     CUtensorMap in[2];        // Dh: g, u
     CUtensorMap o[3];         // outputs (boxes of 32 rows x 64 channels)
     __nv_bfloat16* out[3];
+    int8_t* q[2];             // PACKED: g, u (Up writes them, Dh reads them)
+    uint8_t* scale[2];
     const int32_t* offsets;
-    int M, N, d, I;
+    int M, N, d, I, nb;       // nb: blocks of a packed row
     DevError* err;
     MapParams dw;             // the maps of the weight gradients that follow this kernel
 };
@@ -157,7 +168,7 @@ __device__ __forceinline__ Schedule schedule(int n_tiles, int n_units) {
 }
 
 // List entry t; rows = 0 for a part that its tile is too short for.
-template <int FORM, int MAXN>
+template <int FORM, int MAXN, bool PACKED>
 __device__ __forceinline__ Tile decode(const RowsParams& p, const int* first, const Schedule& sc, int t) {
     int part = 0, cut = 1;
     if (t >= sc.whole) {
@@ -181,13 +192,20 @@ __device__ __forceinline__ Tile decode(const RowsParams& p, const int* first, co
     x.e = lo;
     x.row0 = r0 + a * kStepN;
     x.rows = min(b * kStepN, rows) - a * kStepN;
-    x.c0 = c * 2 * Cfg<FORM, MAXN>::kChannels;
+    x.c0 = c * 2 * Cfg<FORM, MAXN, PACKED>::kChannels;
     return x;
 }
 
-template <int FORM, int MAXN>
+// A panel's g and u in 8 bits, as a thread of the epilogue holds them: its four
+// channels of eight rows, and the steps of row `lane`.
+struct PackedPanel {
+    uint32_t g[8], u[8];
+    float sg, su;
+};
+
+template <int FORM, int MAXN, bool PACKED>
 __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_constant__ RowsParams p) {
-    using C = Cfg<FORM, MAXN>;
+    using C = Cfg<FORM, MAXN, PACKED>;
     constexpr int kS = C::kStages;
     extern __shared__ __align__(1024) unsigned char smem[];
     int* first = reinterpret_cast<int*>(smem + C::kTable);  // tiles before each expert
@@ -250,6 +268,15 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
         for (int64_t v = v0 + (int64_t)blockIdx.x * kThreads + tid; v < v1; v += (int64_t)gridDim.x * kThreads)
             for (int o = 0; o < 3; ++o)
                 if (p.out[o]) reinterpret_cast<uint4*>(p.out[o])[v] = make_uint4(0, 0, 0, 0);
+        if constexpr (FORM == kFormUp && PACKED) {
+            const int64_t b1 = (int64_t)p.M * p.nb;
+            for (int64_t b = (int64_t)row_at(p.N) * p.nb + (int64_t)blockIdx.x * kThreads + tid; b < b1; b += (int64_t)gridDim.x * kThreads)
+                for (int o = 0; o < 2; ++o) {
+                    uint4* q = reinterpret_cast<uint4*>(p.q[o]) + 2 * b;
+                    q[0] = q[1] = make_uint4(0, 0, 0, 0);
+                    p.scale[o][b] = 0;
+                }
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -271,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
         uint32_t phase = 1;
         for (int t = unit; t < sc.total; t += n_units) {
             if (__any_sync(0xffffffffu, *abort_flag)) break;
-            const Tile x = decode<FORM, MAXN>(p, first, sc, t);
+            const Tile x = decode<FORM, MAXN, PACKED>(p, first, sc, t);
             const int rows = __shfl_sync(0xffffffffu, x.rows, 0), e = __shfl_sync(0xffffffffu, x.e, 0);
             if (rows <= 0) continue;
             const int half = (rows + kStepN - 1) / kStepN * kStepN / 2;  // rows staged by each CTA
@@ -321,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
             uint32_t phase = 0;
             for (int t = unit; t < sc.total; t += n_units) {
                 if (__any_sync(0xffffffffu, *abort_flag)) break;
-                const Tile x = decode<FORM, MAXN>(p, first, sc, t);
+                const Tile x = decode<FORM, MAXN, PACKED>(p, first, sc, t);
                 const int rows = __shfl_sync(0xffffffffu, x.rows, 0);
                 if (rows <= 0) continue;
                 const uint32_t idesc = tc_idesc(256, (rows + kStepN - 1) / kStepN * kStepN, 0, C::kNT ? 0 : 1);
@@ -377,12 +404,32 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
                 load_2d<false>(dst + (2 + j) * kBox, &p.in[1], ch + j * 64, x.row0 + q0, bar);
             }
         };
+        // Dh, PACKED: g and u of 32 rows from q0 on, 32 channels of this warp; what lies past the rows is not used
+        PackedPanel ahead;
+        auto load_packed = [&](const Tile& x, int ch, int q0) {
+            const int block = (ch + quarter * 32) / 32;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ahead.g[i] = ahead.u[i] = 0;
+            ahead.sg = ahead.su = 0.f;
+            if (block >= p.nb) return;  // the same for the warp
+            const int r0 = x.row0 + q0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int64_t at = ((int64_t)min(r0 + (i >> 1) * 8 + (lane & 3) * 2 + (i & 1), p.M - 1) * p.nb + block) * 32 + (lane >> 2) * 4;
+                ahead.g[i] = *reinterpret_cast<const uint32_t*>(p.q[0] + at);
+                ahead.u[i] = *reinterpret_cast<const uint32_t*>(p.q[1] + at);
+            }
+            const int64_t at = (int64_t)min(r0 + lane, p.M - 1) * p.nb + block;
+            ahead.sg = pack8::step(p.scale[0][at]);
+            ahead.su = pack8::step(p.scale[1][at]);
+        };
         for (int t = unit; t < sc.total; t += n_units) {
-            const Tile x = decode<FORM, MAXN>(p, first, sc, t);
+            const Tile x = decode<FORM, MAXN, PACKED>(p, first, sc, t);
             if (x.rows <= 0) continue;
             const int ch = x.c0 + (int)rank * C::kChannels;
             const bool any = ch < n_cols && group * kPanel < x.rows;  // this group has a panel of this CTA's channels
-            if (FORM == kFormDh && any && boss) {  // the first panel's inputs, beside the tile's MMAs
+            if (FORM == kFormDh && PACKED && any) load_packed(x, ch, group * kPanel);
+            if (FORM == kFormDh && !PACKED && any && boss) {  // the first panel's inputs, beside the tile's MMAs
                 stores_read<C::kBuffers - 1>();
                 load_inputs(x, ch, group * kPanel, pn % C::kBuffers);
             }
@@ -398,7 +445,12 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
 #pragma unroll 1
                 for (int q0 = group * kPanel; q0 < x.rows; q0 += kGroups * kPanel, ++pn) {
                     const uint32_t buf = panels + (pn % C::kBuffers) * C::kBuffer;
-                    if (FORM == kFormDh && boss && q0 + kGroups * kPanel < x.rows) {
+                    PackedPanel in;
+                    if constexpr (FORM == kFormDh && PACKED) {
+                        in = ahead;
+                        if (q0 + kGroups * kPanel < x.rows) load_packed(x, ch, q0 + kGroups * kPanel);
+                    }
+                    if (FORM == kFormDh && !PACKED && boss && q0 + kGroups * kPanel < x.rows) {
                         stores_read<0>();  // the last panel's store has left the other buffer
                         load_inputs(x, ch, q0 + kGroups * kPanel, (pn + 1) % C::kBuffers);
                     }
@@ -415,6 +467,31 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
                         // same registers.  Each pair of warps swaps 16 rows' values for the other 16's, in
                         // fp32, and forms h of the rows it then has both of.
                         const bool is_u = quarter >= 2;
+                        if constexpr (PACKED) {
+                            const int block = (ch + (quarter & 1) * 32) / 32;
+                            int8_t* const q = p.q[is_u] + (lane >> 2) * 4;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {  // a row: channels lane / 4 + 0, 8, 16, 24
+                                const int k = (i >> 1) * 4 + (i & 1), r = q0 + (i >> 1) * 8 + (lane & 3) * 2 + (i & 1);
+                                float v[4] = {__uint_as_float(lo[k]), __uint_as_float(lo[k + 2]), __uint_as_float(hi[k]), __uint_as_float(hi[k + 2])};
+                                uint32_t m = max(max(pack8::magnitude(v[0]), pack8::magnitude(v[1])), max(pack8::magnitude(v[2]), pack8::magnitude(v[3])));
+#pragma unroll
+                                for (int o = 4; o < 32; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                                const uint32_t E = pack8::exponent(m);
+                                const float inv = pack8::to_steps(E);
+                                if (E == pack8::kTop)
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) v[j] = pack8::within(v[j], E);
+                                uint32_t w = pack8::bytes4(pack8::quantise(v[0], inv), pack8::quantise(v[1], inv), pack8::quantise(v[2], inv),
+                                                           pack8::quantise(v[3], inv));
+                                if (E == 255u) w = 0;
+                                if (r < x.rows && block < p.nb) {
+                                    const int64_t at = (int64_t)(x.row0 + r) * p.nb + block;
+                                    *reinterpret_cast<uint32_t*>(q + at * 32) = w;
+                                    if (lane < 4) p.scale[is_u][at] = (uint8_t)E;
+                                }
+                            }
+                        }
                         float4* mine = reinterpret_cast<float4*>(smem + C::kPanels + kGroups * C::kBuffers * C::kBuffer +
                                                                  group * C::kSwap) + etid;
                         const float4* theirs = mine + (((etid >> 5) ^ 2) - (etid >> 5)) * 32;
@@ -429,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
                                                   __uint_as_float(l[3]));
                             mine[kGroupThreads] = make_float4(__uint_as_float(h[0]), __uint_as_float(h[1]),
                                                               __uint_as_float(h[2]), __uint_as_float(h[3]));
-                            if (p.out[0]) {  // g or u of 16 rows, beside the swap
+                            if (!PACKED && p.out[0]) {  // g or u of 16 rows, beside the swap
 #pragma unroll
                                 for (int b = 2 * i; b < 2 * i + 2; ++b)
                                     stmatrix_x4_trans(at + (is_u ? kBox : 0) + b * 1024, pack_f(lo[4 * b], lo[4 * b + 1]),
@@ -453,11 +530,11 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
                                 w[2 * z] = pack_bf16x2(v[0], v[1]);
                                 w[2 * z + 1] = pack_bf16x2(v[2], v[3]);
                             }
-                            stmatrix_x4_trans(at + 2 * kBox + ((is_u ? 2 : 0) + i) * 1024, w[0], w[1], w[2], w[3]);
+                            stmatrix_x4_trans(at + (PACKED ? 0 : 2 * kBox) + ((is_u ? 2 : 0) + i) * 1024, w[0], w[1], w[2], w[3]);
                         }
                     } else {
                         const uint32_t at = buf + my_box * kBox + mr * 128 + (((my_chunk + mj) ^ mr) << 4);
-                        if constexpr (FORM == kFormDh) {
+                        if constexpr (FORM == kFormDh && !PACKED) {
                             if (lane == 0)
                                 (void)wait<false>(&in_bar[pn % C::kBuffers], (in_phase >> (pn % C::kBuffers)) & 1, abort_flag, p.err, 7, false);
                             __syncwarp();
@@ -466,7 +543,37 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {  // 8 rows, 32 channels
                             const uint32_t* h[4] = {lo + 4 * i, lo + 4 * i + 2, hi + 4 * i, hi + 4 * i + 2};
-                            if constexpr (FORM == kFormDh) {
+                            if constexpr (FORM == kFormDh && PACKED) {
+                                uint32_t a[4], b[4], hh[4];
+                                float sg[2], su[2];
+                                uint32_t gw[2], uw[2];
+#pragma unroll
+                                for (int z = 0; z < 2; ++z) {
+                                    const int r = i * 8 + (lane & 3) * 2 + z;
+                                    sg[z] = __shfl_sync(0xffffffffu, in.sg, r);
+                                    su[z] = __shfl_sync(0xffffffffu, in.su, r);
+                                    gw[z] = pack8::biased(in.g[2 * i + z]);
+                                    uw[z] = pack8::biased(in.u[2 * i + z]);
+                                }
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    float da[2], db[2], hv[2];
+#pragma unroll
+                                    for (int z = 0; z < 2; ++z) {
+                                        const float gf = pack8::value(gw[z], j) * sg[z], uf = pack8::value(uw[z], j) * su[z];
+                                        const float dh = __uint_as_float(h[j][z]), s = fast_sigmoid(gf), silu = gf * s;
+                                        da[z] = dh * uf * s * (1.f + gf * (1.f - s));
+                                        db[z] = dh * silu;
+                                        hv[z] = silu * uf;
+                                    }
+                                    a[j] = pack_bf16x2(da[0], da[1]);
+                                    b[j] = pack_bf16x2(db[0], db[1]);
+                                    hh[j] = pack_bf16x2(hv[0], hv[1]);
+                                }
+                                stmatrix_x4_trans(at + i * 1024, a[0], a[1], a[2], a[3]);
+                                stmatrix_x4_trans(at + 2 * kBox + i * 1024, b[0], b[1], b[2], b[3]);
+                                stmatrix_x4_trans(at + 4 * kBox + i * 1024, hh[0], hh[1], hh[2], hh[3]);
+                            } else if constexpr (FORM == kFormDh) {
                                 uint32_t g[4], u[4], a[4], b[4];
                                 ldmatrix_x4_trans(at + i * 1024, g[0], g[1], g[2], g[3]);
                                 ldmatrix_x4_trans(at + 2 * kBox + i * 1024, u[0], u[1], u[2], u[3]);
@@ -497,10 +604,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
                     }
                     fence_proxy_async();
                     // the next panel's buffer is free once the store that last used it has read it
-                    if (FORM != kFormDh && C::kBuffers == 2 && boss) stores_read<0>();
+                    if ((FORM != kFormDh || PACKED) && C::kBuffers == 2 && boss) stores_read<0>();
                     bar_sync(bar_id, kGroupThreads);
                     // box b of the buffer: which output, and its first channel
-                    auto out_of = [&](int b) { return FORM == kFormUp ? b : FORM == kFormDh ? b >> 1 : 0; };
+                    auto out_of = [&](int b) { return FORM == kFormUp ? (PACKED ? 2 : b) : FORM == kFormDh ? b >> 1 : 0; };
                     auto col_of = [&](int b) { return ch + (FORM == kFormUp ? 0 : (b & 1) * 64); };
                     const int n_rows = x.rows - q0;
                     if (n_rows >= kPanel) {
@@ -548,10 +655,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_rows_kernel(const __grid_
 
 // ---------------------------------------------------------------- host
 
-template <int FORM, int MAXN>
+template <int FORM, int MAXN, bool PACKED>
 cudaError_t launch_form(const RowsParams& p, int64_t units, int sms, cudaStream_t st) {
-    auto kern = grouped_rows_kernel<FORM, MAXN>;
-    constexpr uint32_t kSmem = Cfg<FORM, MAXN>::kSmem;
+    auto kern = grouped_rows_kernel<FORM, MAXN, PACKED>;
+    constexpr uint32_t kSmem = Cfg<FORM, MAXN, PACKED>::kSmem;
     cudaError_t e = allow_max_smem(kern);
     if (e != cudaSuccess) return e;
     int most = 0;
@@ -563,9 +670,9 @@ cudaError_t launch_form(const RowsParams& p, int64_t units, int sms, cudaStream_
                        launch_units(kern, p, (int)units, 2, kThreads, kSmem, st));
 }
 
-template <int FORM>
+template <int FORM, bool PACKED = false>
 cudaError_t launch_rows(const RowsParams& p, bool few, int64_t units, int sms, cudaStream_t st) {
-    return few ? launch_form<FORM, 64>(p, units, sms, st) : launch_form<FORM, 256>(p, units, sms, st);
+    return few ? launch_form<FORM, 64, PACKED>(p, units, sms, st) : launch_form<FORM, 256, PACKED>(p, units, sms, st);
 }
 
 }  // namespace
@@ -576,7 +683,7 @@ bool grouped_tc_shapes(bool bf16, int d, int I) {
 }
 
 bool grouped_tc_usable(const GroupedArgs& a) {
-    if (!grouped_tc_shapes(a.bf16, a.d, a.I) || a.M == 0 || a.packed) return false;
+    if (!grouped_tc_shapes(a.bf16, a.d, a.I) || a.M == 0) return false;
     for (const void* q : {a.a0, a.a1, a.b0, a.b1, a.g, a.u, (const void*)a.o0, (const void*)a.o1, (const void*)a.o2})
         if (reinterpret_cast<uintptr_t>(q) & 15u) return false;
     return true;
@@ -629,6 +736,16 @@ cudaError_t launch_grouped_rows_tc(const GroupedArgs& a, const GroupedArgs* dw, 
     const void* weights[2] = {a.b0, a.b1};
     const void* in[2] = {a.g, a.u};
     void* outs[3] = {a.o0, a.o1, a.o2};
+    if (a.packed) {  // g and u without tensor maps
+        const bool up = a.form == kFormUp;
+        p.nb = pack_blocks(a.I);
+        for (int i = 0; i < 2; ++i) {
+            p.q[i] = static_cast<int8_t*>(up ? outs[i] : const_cast<void*>(in[i]));
+            p.scale[i] = up ? (i ? a.s1 : a.s0) : const_cast<uint8_t*>(i ? a.us : a.gs);
+            in[i] = nullptr;
+            if (up) outs[i] = nullptr;
+        }
+    }
     auto rows_map = [&](CUtensorMap* m, const void* base, uint64_t width, uint32_t box_rows) {
         ok = ok && encode_bf16_2d(m, base, width, M, width * 2, 64, box_rows) == MOE_OK;
     };
@@ -651,9 +768,9 @@ cudaError_t launch_grouped_rows_tc(const GroupedArgs& a, const GroupedArgs* dw, 
     // an upper bound of the tiles, each cut into up to eight parts where there are few
     const int64_t units = ((int64_t)a.M / max_n + (a.N < a.M ? a.N : a.M)) * col_tiles * 8;
     switch (a.form) {
-        case kFormUp: return launch_rows<kFormUp>(p, few, units, a.sms, st);
+        case kFormUp: return a.packed ? launch_rows<kFormUp, true>(p, few, units, a.sms, st) : launch_rows<kFormUp>(p, few, units, a.sms, st);
         case kFormDown: return launch_rows<kFormDown>(p, few, units, a.sms, st);
-        case kFormDh: return launch_rows<kFormDh>(p, few, units, a.sms, st);
+        case kFormDh: return a.packed ? launch_rows<kFormDh, true>(p, few, units, a.sms, st) : launch_rows<kFormDh>(p, few, units, a.sms, st);
         case kFormDx: return launch_rows<kFormDx>(p, few, units, a.sms, st);
         case kFormDw: break;
     }
