@@ -38,92 +38,125 @@ __device__ __forceinline__ float rstd_of(Sums& sums, float ss, int d, float eps,
     return 1.f / sqrtf(s[0] / (float)d + eps);
 }
 
-template <typename W, typename Y, int E>
+// E values a vector; C > 0: a thread's C vectors of a row stay in registers,
+// C = 0: a row of any length, read again for each sum and for the result.
+template <typename W, typename Y, int E, int C>
 __global__ void __launch_bounds__(kMaxGroup) block_out_kernel(const BlockOutParams p) {
     constexpr bool kY = !std::is_same_v<Y, None>;
+    constexpr int kN = C > 0 ? C : 1;
     __shared__ float red[kBlock / 32][2][kMaxGroupWarps][4];
     const int tid = threadIdx.x % p.group, g = threadIdx.x / p.group;
     Sums sums = {red[g], p.group / 32, tid / 32, 1 + g, p.group, 0};
+    // f(slot, i) for the vectors i of this thread
+    auto each = [&](auto f) {
+        if constexpr (C > 0) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (tid + c * p.group < p.n_vec) f(c, tid + c * p.group);
+        } else
+            for (int i = tid; i < p.n_vec; i += p.group) f(0, i);
+    };
+    Raw<W, E> r[kN], wp[kN], wn[kN], gate[kN];
+    Raw<Y, E> y[kN];
+    auto load_weights = [&](int c, int i) {
+        wp[c].zero();
+        wn[c].zero();
+        if (kY && p.w_post) wp[c].load(p.w_post, i);
+        if (p.w_next) wn[c].load(p.w_next, i);
+        if (kY && p.gate_kind == MOE_GATE_CHANNEL) gate[c].load(p.gate, i);
+    };
     grid_dep_wait();
+    if (C > 0) each(load_weights);
     for (int64_t t = (int64_t)blockIdx.x * p.rows + g; t < p.T; t += (int64_t)gridDim.x * p.rows) {
-        const char *yrow = p.y + t * p.ldy, *rrow = p.r + t * p.ldr;
+        auto load_row = [&](int c, int i) {
+            y[c].load(p.y + t * p.ldy, i);
+            r[c].load(p.r + t * p.ldr, i);
+            if (kY && p.gate_kind == MOE_GATE_FULL) gate[c].load(static_cast<const char*>(p.gate) + t * p.d * (int64_t)sizeof(W), i);
+        };
+        if (C > 0) each(load_row);
         float a = 1.f, gt = p.scale;
         if (kY && p.gate_kind == MOE_GATE_TOKEN) gt *= static_cast<const float*>(p.gate)[t];
         if (kY && p.post) {
             auto squares = [&](float s) {
                 float ss = 0.f;
-                for (int i = tid; i < p.n_vec; i += p.group) {
-                    Raw<Y, E> y;
-                    y.load(yrow, i);
+                each([&](int c, int i) {
+                    if (C == 0) y[c].load(p.y + t * p.ldy, i);
 #pragma unroll
-                    for (int j = 0; j < E; ++j) ss = fmaf(y[j] * s, y[j] * s, ss);
-                }
+                    for (int j = 0; j < E; ++j) ss = fmaf(y[c][j] * s, y[c][j] * s, ss);
+                });
                 return ss;
             };
             a = rstd_of(sums, squares(1.f), p.d, p.eps, [&] { return squares(0x1p-80f); });
             if (tid == 0 && p.rstd_post) p.rstd_post[t] = a;
         }
-        // vector i of out, before its rounding
-        auto value = [&](int i, float (&v)[E]) {
-            Raw<W, E> r, w, gate;
-            Raw<Y, E> y;
-            r.load(rrow, i);
-            y.load(yrow, i);
-            w.zero();
-            if (kY && p.w_post) w.load(p.w_post, i);
-            if (kY && p.gate_kind == MOE_GATE_CHANNEL) gate.load(p.gate, i);
-            if (kY && p.gate_kind == MOE_GATE_FULL) gate.load(static_cast<const char*>(p.gate) + t * p.d * (int64_t)sizeof(W), i);
+        float v[kN][E];  // out before its rounding
+        auto value = [&](int c, int i) {
+            if (C == 0) {
+                load_weights(c, i);
+                load_row(c, i);
+            }
 #pragma unroll
             for (int j = 0; j < E; ++j) {
-                v[j] = r[j];
+                v[c][j] = r[c][j];
                 if constexpr (kY) {
-                    float b = y[j];
-                    if (p.post) b = b * a * (p.offset + w[j]);
-                    if (p.gate_kind >= MOE_GATE_CHANNEL) b *= gate[j];
-                    v[j] = fmaf(gt, b, v[j]);
+                    float b = y[c][j];
+                    if (p.post) b = b * a * (p.offset + wp[c][j]);
+                    if (p.gate_kind >= MOE_GATE_CHANNEL) b *= gate[c][j];
+                    v[c][j] = fmaf(gt, b, v[c][j]);
                 }
             }
         };
+        if (C > 0) {
+            each([&](int c, int i) {
+                value(c, i);
+                if (p.out) store<W, E>(p.out + t * p.ldo, i, v[c]);
+            });
+        }
         float b = 1.f;
         if (p.next) {
             auto squares = [&](float s) {
                 float ss = 0.f;
-                for (int i = tid; i < p.n_vec; i += p.group) {
-                    float v[E];
-                    value(i, v);
+                each([&](int c, int i) {
+                    if (C == 0) value(c, i);
 #pragma unroll
-                    for (int j = 0; j < E; ++j) ss = fmaf(v[j] * s, v[j] * s, ss);
-                }
+                    for (int j = 0; j < E; ++j) ss = fmaf(v[c][j] * s, v[c][j] * s, ss);
+                });
                 return ss;
             };
             b = rstd_of(sums, squares(1.f), p.d, p.eps, [&] { return squares(0x1p-80f); });
             if (tid == 0 && p.rstd_next) p.rstd_next[t] = b;
         }
-        for (int i = tid; i < p.n_vec; i += p.group) {
-            float v[E];
-            value(i, v);
-            if (p.out) store<W, E>(p.out + t * p.ldo, i, v);
-            if (p.next) {
-                Raw<W, E> w;
-                w.zero();
-                if (p.w_next) w.load(p.w_next, i);
+        if (C == 0 || p.next)
+            each([&](int c, int i) {
+                if (C == 0) {
+                    value(c, i);
+                    if (p.out) store<W, E>(p.out + t * p.ldo, i, v[c]);
+                }
+                if (p.next) {
 #pragma unroll
-                for (int j = 0; j < E; ++j) v[j] = v[j] * b * (p.offset + w[j]);
-                store<W, E>(p.next + t * p.ldn, i, v);
-            }
-        }
+                    for (int j = 0; j < E; ++j) v[c][j] = v[c][j] * b * (p.offset + wn[c][j]);
+                    store<W, E>(p.next + t * p.ldn, i, v[c]);
+                }
+            });
     }
     grid_dep_launch();
 }
 
-template <typename W, typename Y, int E>
+template <typename W, typename Y, int E, int C>
 cudaError_t launch(BlockOutParams p, int sms, cudaStream_t st) {
     p.n_vec = p.d / E;
-    const Shape s = shape_of(p.n_vec, 0);
+    const Shape s = shape_of(p.n_vec, C);
     p.group = s.group; p.rows = s.rows;
     int64_t blocks = ((int64_t)p.T + s.rows - 1) / s.rows;
-    if (blocks > (int64_t)sms * 8) blocks = (int64_t)sms * 8;
-    return launch_pdl(block_out_kernel<W, Y, E>, dim3((unsigned)blocks), dim3(s.threads()), 0, st, p);
+    const int64_t most = (int64_t)sms * (s.threads() > 256 ? 2 : 4);
+    if (blocks > most) blocks = most;
+    return launch_pdl(block_out_kernel<W, Y, E, C>, dim3((unsigned)blocks), dim3(s.threads()), 0, st, p);
+}
+
+template <typename W, typename Y>
+cudaError_t launch_vectors(const BlockOutParams& p, int e, int sms, cudaStream_t st) {
+    constexpr int kWide = 16 / (int)sizeof(W);
+    return with_chunks<kWide>(p.d, e, [&](auto E, auto C) { return launch<W, Y, E, C>(p, sms, st); });
 }
 
 }  // namespace
@@ -138,10 +171,12 @@ cudaError_t launch_block_out(const NormArgs& a, cudaStream_t st) {
     p.next = static_cast<char*>(a.next); p.ldn = a.ldn * es;
     p.rstd_post = a.rstd_post; p.rstd_next = a.rstd_next;
     p.T = a.T; p.d = a.d; p.post = a.post; p.eps = a.eps; p.offset = a.offset; p.scale = a.scale;
-    if (!a.bf16) return a.y ? launch<float, float, 1>(p, a.sms, st) : launch<float, None, 1>(p, a.sms, st);
-    return !a.y     ? launch<__nv_bfloat16, None, 1>(p, a.sms, st)
-         : a.y_f32 ? launch<__nv_bfloat16, float, 1>(p, a.sms, st)
-                   : launch<__nv_bfloat16, __nv_bfloat16, 1>(p, a.sms, st);
+    const int e = vector_values(a.bf16, a.d, {{a.y, p.ldy}, {a.residual, p.ldr}, {a.out, p.ldo}, {a.next, p.ldn},
+                                              {a.gate_kind == MOE_GATE_TOKEN ? nullptr : a.gate, 0}, {a.w_post, 0}, {a.w_next, 0}});
+    if (!a.bf16) return a.y ? launch_vectors<float, float>(p, e, a.sms, st) : launch_vectors<float, None>(p, e, a.sms, st);
+    return !a.y     ? launch_vectors<__nv_bfloat16, None>(p, e, a.sms, st)
+         : a.y_f32 ? launch_vectors<__nv_bfloat16, float>(p, e, a.sms, st)
+                   : launch_vectors<__nv_bfloat16, __nv_bfloat16>(p, e, a.sms, st);
 }
 
 }  // namespace moe

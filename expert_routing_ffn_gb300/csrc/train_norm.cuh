@@ -4,6 +4,9 @@
 
 #include <cuda_bf16.h>
 
+#include <initializer_list>
+#include <type_traits>
+
 #include "common.cuh"
 #include "train.h"
 
@@ -116,6 +119,38 @@ inline Shape shape_of(int n_vec, int chunks) {
     if (s.group > kMaxGroup) s.group = kMaxGroup;  // with chunks > 0 the caller has seen to it
     s.rows = s.group >= kBlock ? 1 : kBlock / s.group;
     return s;
+}
+
+// Values of a vector that every row of these tensors allows: 16 bytes of the
+// layer's type, or a single value.  A place: address (NULL = not there) and row
+// stride in bytes.
+struct Place {
+    const void* p;
+    int64_t stride;
+};
+inline int vector_values(bool bf16, int d, std::initializer_list<Place> places) {
+    const int wide = bf16 ? 8 : 4;
+    if (d % wide) return 1;
+    for (const Place& x : places)
+        if (x.p && ((reinterpret_cast<uintptr_t>(x.p) | (uintptr_t)x.stride) & 15u)) return 1;
+    return wide;
+}
+
+// f(E, C) with the values of a vector and the vectors of a thread for rows of d
+// values: up to 16 values a thread in registers, else C = 0.
+template <int WIDE, typename F>
+inline cudaError_t with_chunks(int d, int e, F f) {
+    using std::integral_constant;
+    const int n = d / e;
+    if (e == WIDE) {
+        if (n <= kMaxGroup) return f(integral_constant<int, WIDE>(), integral_constant<int, 1>());
+        if (n <= 2 * kMaxGroup) return f(integral_constant<int, WIDE>(), integral_constant<int, 2>());
+        if constexpr (WIDE == 4)
+            if (n <= 4 * kMaxGroup) return f(integral_constant<int, WIDE>(), integral_constant<int, 4>());
+        return f(integral_constant<int, WIDE>(), integral_constant<int, 0>());
+    }
+    if (n <= 8 * kMaxGroup) return f(integral_constant<int, 1>(), integral_constant<int, 8>());
+    return f(integral_constant<int, 1>(), integral_constant<int, 0>());
 }
 
 }  // namespace norm

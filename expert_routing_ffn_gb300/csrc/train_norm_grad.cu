@@ -32,78 +32,104 @@ struct BlockGradParams {
     float* part;                                     // [groups][2][d]
 };
 
-template <typename W, typename Y, int E>
+// E values a vector; C > 0: a thread's C vectors of a row, and its columns' sums,
+// stay in registers; C = 0: a row of any length, read twice, and sums that grow in
+// the workspace.
+template <typename W, typename Y, int E, int C>
 __global__ void __launch_bounds__(kMaxGroup) block_grad_kernel(const BlockGradParams p) {
     constexpr bool kY = !std::is_same_v<Y, None>;
+    constexpr int kN = C > 0 ? C : 1;
     __shared__ float red[kBlock / 32][2][kMaxGroupWarps][4];
     const int tid = threadIdx.x % p.group, grp = threadIdx.x / p.group;
     Sums sums = {red[grp], p.group / 32, tid / 32, 1 + grp, p.group, 0};
+    // f(slot, i) for the vectors i of this thread
+    auto each = [&](auto f) {
+        if constexpr (C > 0) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (tid + c * p.group < p.n_vec) f(c, tid + c * p.group);
+        } else
+            for (int i = tid; i < p.n_vec; i += p.group) f(0, i);
+    };
+    Raw<W, E> dout[kN], dnext[kN], xo_[kN], wn[kN], wp[kN], gate[kN];
+    Raw<Y, E> y[kN];
+    float cn[kN][E], cp[kN][E];  // the columns' sums
+#pragma unroll
+    for (int c = 0; c < kN; ++c) {
+        dout[c].zero(); dnext[c].zero(); xo_[c].zero(); wn[c].zero(); wp[c].zero();
+#pragma unroll
+        for (int j = 0; j < E; ++j) cn[c][j] = cp[c][j] = 0.f;
+    }
+    auto load_weights = [&](int c, int i) {
+        if (p.w_next) wn[c].load(p.w_next, i);
+        if (kY && p.w_post) wp[c].load(p.w_post, i);
+        if (kY && p.gate_kind == MOE_GATE_CHANNEL) gate[c].load(p.gate, i);
+    };
     grid_dep_wait();
+    if (C > 0) each(load_weights);
     const int64_t groups = (int64_t)gridDim.x * p.rows, first = (int64_t)blockIdx.x * p.rows + grp;
     float *col_next = p.part + first * 2 * p.d, *col_post = col_next + p.d;
     for (int64_t t = first; t < p.T; t += groups) {
-        const float a = kY && p.post ? p.rstd_post[t] : 1.f, b = p.dnext ? p.rstd_next[t] : 0.f;
-        const float gt = kY && p.gate_kind == MOE_GATE_TOKEN ? static_cast<const float*>(p.gate)[t] : 1.f;
-        struct Vector {
-            Raw<W, E> dout, dnext, xo, wn, wp, gate;
-            Raw<Y, E> y;
-        };
-        auto load = [&](int i, Vector& q) {
-            q.dout.zero(); q.dnext.zero(); q.xo.zero(); q.wn.zero(); q.wp.zero();
-            if (p.dout) q.dout.load(p.dout + t * p.lddout, i);
+        auto load_row = [&](int c, int i) {
+            if (p.dout) dout[c].load(p.dout + t * p.lddout, i);
             if (p.dnext) {
-                q.dnext.load(p.dnext + t * p.lddnext, i);
-                q.xo.load(p.out + t * p.ldo, i);
-                if (p.w_next) q.wn.load(p.w_next, i);
+                dnext[c].load(p.dnext + t * p.lddnext, i);
+                xo_[c].load(p.out + t * p.ldo, i);
             }
             if constexpr (kY) {
-                q.y.load(p.y + t * p.ldy, i);
-                if (p.w_post) q.wp.load(p.w_post, i);
-                if (p.gate_kind == MOE_GATE_CHANNEL) q.gate.load(p.gate, i);
-                if (p.gate_kind == MOE_GATE_FULL) q.gate.load(static_cast<const char*>(p.gate) + t * p.d * (int64_t)sizeof(W), i);
+                y[c].load(p.y + t * p.ldy, i);
+                if (p.gate_kind == MOE_GATE_FULL) gate[c].load(static_cast<const char*>(p.gate) + t * p.d * (int64_t)sizeof(W), i);
             }
         };
+        if (C > 0) each(load_row);
+        const float a = kY && p.post ? p.rstd_post[t] : 1.f, b = p.dnext ? p.rstd_next[t] : 0.f;
+        const float gt = kY && p.gate_kind == MOE_GATE_TOKEN ? static_cast<const float*>(p.gate)[t] : 1.f;
         float s[3] = {0.f, 0.f, 0.f};
         if (p.dnext || kY) {
-            for (int i = tid; i < p.n_vec; i += p.group) {
-                Vector q;
-                load(i, q);
+            each([&](int c, int i) {
+                if (C == 0) {
+                    load_weights(c, i);
+                    load_row(c, i);
+                }
 #pragma unroll
                 for (int j = 0; j < E; ++j) {
-                    const float xo = q.xo[j] * b, g = q.dnext[j] * (p.offset + q.wn[j]);
+                    const float xo = xo_[c][j] * b, g = dnext[c][j] * (p.offset + wn[c][j]);
                     s[0] = fmaf(g, xo, s[0]);
                     if constexpr (kY) {
-                        float v = q.y[j] * a;
-                        if (p.post) v *= p.offset + q.wp[j];
-                        if (p.gate_kind >= MOE_GATE_CHANNEL) v *= q.gate[j];
-                        s[1] = fmaf(fmaf(b, g, q.dout[j]), v, s[1]);
+                        float v = y[c][j] * a;
+                        if (p.post) v *= p.offset + wp[c][j];
+                        if (p.gate_kind >= MOE_GATE_CHANNEL) v *= gate[c][j];
+                        s[1] = fmaf(fmaf(b, g, dout[c][j]), v, s[1]);
                         s[2] = fmaf(xo, v, s[2]);
                     }
                 }
-            }
+            });
             sums.sum(s);
         }
-        const float c = b * (s[0] / (float)p.d);
-        const float dv = s[1] - c * s[2];                        // sum D v
+        const float cc = b * (s[0] / (float)p.d);
+        const float dv = s[1] - cc * s[2];                       // sum D v
         const float m = p.scale * gt * (dv / (float)p.d);        // mean(dp w_post' yn)
         if (kY && p.gate_kind == MOE_GATE_TOKEN && p.dgate && tid == 0) static_cast<float*>(p.dgate)[t] = p.scale * dv;
-        for (int i = tid; i < p.n_vec; i += p.group) {
-            Vector q;
-            load(i, q);
-            float D[E], dyv[E], dg[E], cn[E], cp[E];
+        each([&](int c, int i) {
+            if (C == 0) {
+                load_weights(c, i);
+                load_row(c, i);
+            }
+            float D[E], dyv[E], dg[E];
 #pragma unroll
             for (int j = 0; j < E; ++j) {
-                const float xo = q.xo[j] * b, g = q.dnext[j] * (p.offset + q.wn[j]);
-                D[j] = fmaf(b, g, q.dout[j]) - xo * c;
-                cn[j] = q.dnext[j] * xo;
+                const float xo = xo_[c][j] * b, g = dnext[c][j] * (p.offset + wn[c][j]);
+                D[j] = fmaf(b, g, dout[c][j]) - xo * cc;
+                if (C == 0) cn[c][j] = cp[c][j] = 0.f;
+                cn[c][j] = fmaf(dnext[c][j], xo, cn[c][j]);
                 if constexpr (kY) {
-                    const float yn = q.y[j] * a, w = p.post ? p.offset + q.wp[j] : 1.f;
-                    const float gate = p.gate_kind >= MOE_GATE_CHANNEL ? q.gate[j] : gt, dq = p.scale * D[j];
+                    const float yn = y[c][j] * a, w = p.post ? p.offset + wp[c][j] : 1.f;
+                    const float ga = p.gate_kind >= MOE_GATE_CHANNEL ? gate[c][j] : gt, dq = p.scale * D[j];
                     dg[j] = dq * yn * w;
-                    dyv[j] = dq * gate * w;
+                    dyv[j] = dq * ga * w;
                     if (p.post) dyv[j] = a * (dyv[j] - yn * m);
-                    cp[j] = D[j] * yn;
-                    if (p.gate_kind == MOE_GATE_TOKEN || p.gate_kind == MOE_GATE_FULL) cp[j] *= gate;
+                    const bool gated = p.gate_kind == MOE_GATE_TOKEN || p.gate_kind == MOE_GATE_FULL;
+                    cp[c][j] = fmaf(D[j] * yn, gated ? ga : 1.f, cp[c][j]);
                 }
             }
             if (p.dr) store<W, E>(p.dr + t * p.lddr, i, D);
@@ -112,16 +138,21 @@ __global__ void __launch_bounds__(kMaxGroup) block_grad_kernel(const BlockGradPa
                 if (p.gate_kind == MOE_GATE_FULL && p.dgate)
                     store<W, E>(static_cast<char*>(p.dgate) + t * p.d * (int64_t)sizeof(W), i, dg);
             }
-            if (p.columns) {
+            if (C == 0 && p.columns) {
 #pragma unroll
                 for (int j = 0; j < E; ++j) {
                     const int col = i * E + j;
-                    col_next[col] = t == first ? cn[j] : col_next[col] + cn[j];
-                    if constexpr (kY) col_post[col] = t == first ? cp[j] : col_post[col] + cp[j];
+                    col_next[col] = t == first ? cn[c][j] : col_next[col] + cn[c][j];
+                    if constexpr (kY) col_post[col] = t == first ? cp[c][j] : col_post[col] + cp[c][j];
                 }
             }
-        }
+        });
     }
+    if (C > 0 && p.columns && first < p.T)
+        each([&](int c, int i) {
+            store<float, E>(col_next, i, cn[c]);
+            if constexpr (kY) store<float, E>(col_post, i, cp[c]);
+        });
     grid_dep_launch();
 }
 
@@ -166,10 +197,10 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const ColumnParams p) 
     grid_dep_launch();
 }
 
-template <typename W, typename Y, int E>
+template <typename W, typename Y, int E, int C>
 cudaError_t launch(BlockGradParams p, int parts, int sms, int* groups, cudaStream_t st) {
     p.n_vec = p.d / E;
-    const Shape s = shape_of(p.n_vec, 0);
+    const Shape s = shape_of(p.n_vec, C);
     p.group = s.group; p.rows = s.rows;
     int64_t blocks = ((int64_t)p.T + s.rows - 1) / s.rows, most = (int64_t)sms * 2;
     if (p.columns && most > parts / s.rows) most = parts / s.rows;
@@ -177,7 +208,13 @@ cudaError_t launch(BlockGradParams p, int parts, int sms, int* groups, cudaStrea
     if (blocks > most) blocks = most;
     const int64_t all = blocks * p.rows;
     *groups = (int)(all < p.T ? all : p.T);
-    return launch_pdl(block_grad_kernel<W, Y, E>, dim3((unsigned)blocks), dim3(p.group * p.rows), 0, st, p);
+    return launch_pdl(block_grad_kernel<W, Y, E, C>, dim3((unsigned)blocks), dim3(p.group * p.rows), 0, st, p);
+}
+
+template <typename W, typename Y>
+cudaError_t launch_vectors(const BlockGradParams& p, int e, int parts, int sms, int* groups, cudaStream_t st) {
+    constexpr int kWide = 16 / (int)sizeof(W);
+    return with_chunks<kWide>(p.d, e, [&](auto E, auto C) { return launch<W, Y, E, C>(p, parts, sms, groups, st); });
 }
 
 }  // namespace
@@ -201,10 +238,13 @@ cudaError_t launch_block_out_grad(const NormGradArgs& a, cudaStream_t st, int* l
     int groups = 0;
     *launches = 1;
     cudaError_t e;
-    if (!a.bf16) e = a.y ? launch<float, float, 1>(p, parts, a.sms, &groups, st) : launch<float, None, 1>(p, parts, a.sms, &groups, st);
-    else if (!a.y) e = launch<__nv_bfloat16, None, 1>(p, parts, a.sms, &groups, st);
-    else if (a.y_f32) e = launch<__nv_bfloat16, float, 1>(p, parts, a.sms, &groups, st);
-    else e = launch<__nv_bfloat16, __nv_bfloat16, 1>(p, parts, a.sms, &groups, st);
+    const int v = vector_values(a.bf16, a.d, {{a.dout, p.lddout}, {a.dnext, p.lddnext}, {a.y, p.ldy}, {a.dnext ? a.out : nullptr, p.ldo},
+                                              {a.gate_kind == MOE_GATE_TOKEN ? nullptr : a.gate, 0}, {a.w_post, 0}, {a.w_next, 0},
+                                              {a.dresidual, p.lddr}, {a.dy, p.lddy}, {a.gate_kind == MOE_GATE_FULL ? a.dgate : nullptr, 0}});
+    if (!a.bf16) e = a.y ? launch_vectors<float, float>(p, v, parts, a.sms, &groups, st) : launch_vectors<float, None>(p, v, parts, a.sms, &groups, st);
+    else if (!a.y) e = launch_vectors<__nv_bfloat16, None>(p, v, parts, a.sms, &groups, st);
+    else if (a.y_f32) e = launch_vectors<__nv_bfloat16, float>(p, v, parts, a.sms, &groups, st);
+    else e = launch_vectors<__nv_bfloat16, __nv_bfloat16>(p, v, parts, a.sms, &groups, st);
     if (e != cudaSuccess || !p.columns) return e;
     ColumnParams c;
     c.part = a.part; c.groups = groups; c.d = a.d; c.gate_kind = a.gate_kind; c.post = a.post; c.accumulate = a.accumulate;
