@@ -87,7 +87,7 @@ struct NormArgs {
 };
 cudaError_t launch_block_out(const NormArgs& a, cudaStream_t st);
 
-constexpr int kNormMaxParts = 1024;              // column sums of so many row groups
+constexpr int kNormMaxParts = 2048;              // column sums of so many row groups
 constexpr size_t kNormPartBytes = 12u << 20;     // and in so much of the workspace
 // row groups whose column sums (two float32 [d]) the workspace holds
 inline int norm_parts(int T, int d) {

@@ -121,6 +121,107 @@ inline Shape shape_of(int n_vec, int chunks) {
     return s;
 }
 
+// ---------------------------------------------------------------- rows through shared memory
+// Long batches: one block an SM, and a ring of stages for each of its groups,
+// each stage a row of every input, brought by bulk copies that the group's first
+// thread issues `stages` rows ahead.  A group reads its row into registers, and
+// the barrier of the row's first sum tells that thread that the stage is free.
+constexpr int kMaxInputs = 5, kMaxStages = 8, kMaxGroups = 12;
+struct RingParams {
+    const char* src[kMaxInputs];  // rows, NULL: not there
+    int64_t stride[kMaxInputs];   // bytes
+    uint32_t bytes[kMaxInputs], at[kMaxInputs];  // of a row; its place in a stage
+    uint32_t stage_bytes;
+    int stages;
+    uint32_t rings, barriers;     // offsets in shared memory (the weights come first)
+};
+struct Ring {
+    const RingParams& p;
+    char* base;
+    uint64_t* full;
+    int64_t T, first, step;
+    uint64_t policy;
+    int slot, issue_slot;
+    uint32_t phase;
+    int64_t ahead;  // the next row to fetch
+
+    __device__ __forceinline__ Ring(const RingParams& p, char* smem, int group, int64_t T, int64_t first, int64_t step)
+        : p(p), base(smem + p.rings + (size_t)group * p.stages * p.stage_bytes),
+          full(reinterpret_cast<uint64_t*>(smem + p.barriers) + group * kMaxStages), T(T), first(first), step(step),
+          policy(l2_evict_first_policy()), slot(0), issue_slot(0), phase(0), ahead(first) {}
+    __device__ __forceinline__ void init() {
+        for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
+    }
+    // one row more, by one thread
+    __device__ __forceinline__ void issue() {
+        if (ahead < T) {
+            mbar_arrive_expect_tx(&full[issue_slot], p.stage_bytes);
+            char* dst = base + (size_t)issue_slot * p.stage_bytes;
+#pragma unroll
+            for (int i = 0; i < kMaxInputs; ++i)
+                if (p.src[i]) bulk_g2s(dst + p.at[i], p.src[i] + ahead * p.stride[i], p.bytes[i], &full[issue_slot], policy);
+        }
+        ahead += step;
+        if (++issue_slot == p.stages) issue_slot = 0;
+    }
+    // the current row's stage has arrived (false: given up)
+    __device__ __forceinline__ bool wait() { return mbar_wait(&full[slot], phase); }
+    __device__ __forceinline__ const char* input(int i) const { return base + (size_t)slot * p.stage_bytes + p.at[i]; }
+    __device__ __forceinline__ void next() {
+        if (++slot == p.stages) { slot = 0; phase ^= 1; }
+    }
+    // after a wait that gave up: nothing of this thread's copies may land once the block is gone
+    __device__ __forceinline__ void drain(int64_t t) {
+        for (int64_t r = t; r < ahead && r < T; r += step) {
+            (void)wait();
+            next();
+        }
+    }
+};
+
+// float32 factors of a row's columns in shared memory, so that a warp's 16-byte
+// reads of them do not meet: part h of vector i at 4 (h n_vec + i)
+template <int E>
+__device__ __forceinline__ void put_factor(float* f, int n_vec, int col, float v) {
+    f[4 * (col % E / 4 * n_vec + col / E) + col % 4] = v;
+}
+template <int E>
+__device__ __forceinline__ void get_factors(const float* f, int n_vec, int i, float (&v)[E]) {
+#pragma unroll
+    for (int h = 0; h < E / 4; ++h) *reinterpret_cast<float4*>(v + 4 * h) = *reinterpret_cast<const float4*>(f + 4 * (h * n_vec + i));
+}
+
+// Whether a batch takes the ring, and its geometry: `groups` rows at a time of
+// `group` threads each, at most `threads` and `most` groups in all; at least
+// four rows a group.
+struct RingShape {
+    int group, groups, blocks;
+    uint32_t smem;
+};
+inline bool ring_shape(RingParams& r, int T, int n_vec, int chunks, int threads, int most, uint32_t weights, int sms, RingShape& s) {
+    constexpr uint32_t kLimit = 232448 - kMaxGroups * 2 * kMaxGroupWarps * 16;  // shared memory of a block, less the sums'
+    s.group = 32 * ((n_vec + 32 * chunks - 1) / (32 * chunks));
+    r.stage_bytes = 0;
+    for (int i = 0; i < kMaxInputs; ++i)
+        if (r.src[i]) {
+            r.at[i] = r.stage_bytes;
+            r.stage_bytes += r.bytes[i];
+        }
+    const uint32_t bars = kMaxGroups * kMaxStages * 8;
+    r.rings = (weights + 127) / 128 * 128;
+    if (most > kMaxGroups) most = kMaxGroups;
+    for (s.groups = threads / s.group < most ? threads / s.group : most; s.groups > 0; --s.groups) {
+        const int64_t stages = ((int64_t)kLimit - r.rings - bars) / ((int64_t)s.groups * r.stage_bytes);
+        r.stages = (int)(stages < kMaxStages ? stages : kMaxStages);
+        if (r.stages >= 3 || (s.groups == 1 && r.stages == 2)) break;
+    }
+    if (s.groups <= 0 || T < 4LL * sms * s.groups) return false;
+    r.barriers = r.rings + (uint32_t)s.groups * r.stages * r.stage_bytes;
+    s.smem = r.barriers + bars;
+    s.blocks = sms;
+    return true;
+}
+
 // Values of a vector that every row of these tensors allows: 16 bytes of the
 // layer's type, or a single value.  A place: address (NULL = not there) and row
 // stride in bytes.

@@ -156,6 +156,153 @@ __global__ void __launch_bounds__(kMaxGroup) block_grad_kernel(const BlockGradPa
     grid_dep_launch();
 }
 
+// The same for long batches, rows coming through shared memory.  The factors of
+// the columns wait there too, in float32: w_next' and w_post' times the gate of a
+// channel.  A row's values pass through registers once; of what the sums need,
+// D without its projection (t), out and y stay.
+enum { kInDout, kInDnext, kInOut, kInY, kInGate };
+
+template <typename W, typename Y, int C>
+__global__ void __launch_bounds__(std::is_same_v<Y, None> ? 768 : 512, 1)
+    block_grad_ring_kernel(const __grid_constant__ BlockGradParams p, const __grid_constant__ RingParams rp) {
+    constexpr bool kY = !std::is_same_v<Y, None>;
+    constexpr int E = 16 / (int)sizeof(W);
+    extern __shared__ __align__(128) char smem[];
+    __shared__ float red[kMaxGroups][2][kMaxGroupWarps][4];
+    const int tid = threadIdx.x % p.group, grp = threadIdx.x / p.group;
+    Sums sums = {red[grp], p.group / 32, tid / 32, 1 + grp, p.group, 0};
+    const int64_t groups = (int64_t)gridDim.x * p.rows, first = (int64_t)blockIdx.x * p.rows + grp;
+    float *f_next = reinterpret_cast<float*>(smem), *f_post = f_next + (p.dnext ? p.d : 0);
+    Ring ring(rp, smem, grp, p.T, first, groups);
+    if (tid == 0) ring.init();
+    fence_mbar_init();
+    grid_dep_wait();
+    __syncthreads();
+    if (tid == 0)
+        for (int s = 0; s < rp.stages; ++s) ring.issue();
+    for (int c = threadIdx.x; c < p.d; c += blockDim.x) {
+        if (p.dnext) put_factor<E>(f_next, p.n_vec, c, p.offset + (p.w_next ? to_f32(static_cast<const W*>(p.w_next)[c]) : 0.f));
+        if constexpr (kY) {
+            float w = p.post ? p.offset + (p.w_post ? to_f32(static_cast<const W*>(p.w_post)[c]) : 0.f) : 1.f;
+            if (p.gate_kind == MOE_GATE_CHANNEL) w *= to_f32(static_cast<const W*>(p.gate)[c]);
+            put_factor<E>(f_post, p.n_vec, c, w);
+        }
+    }
+    __syncthreads();
+    const bool full = kY && p.gate_kind == MOE_GATE_FULL;
+    float cn[C][E], cp[C][E];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int j = 0; j < E; ++j) cn[c][j] = cp[c][j] = 0.f;
+    int64_t t = first;
+    for (; t < p.T; t += groups) {
+        const float a = kY && p.post ? p.rstd_post[t] : 1.f, b = p.dnext ? p.rstd_next[t] : 0.f;
+        const float gt = kY && p.gate_kind == MOE_GATE_TOKEN ? static_cast<const float*>(p.gate)[t] : 1.f;
+        if (!ring.wait()) break;
+        float s[3] = {0.f, 0.f, 0.f};
+        float dt[C][E];  // dout + b dnext w_next'
+        Raw<W, E> out[C], gate[C];
+        Raw<Y, E> y[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int i = tid + c * p.group;
+            if (i >= p.n_vec) continue;
+#pragma unroll
+            for (int j = 0; j < E; ++j) dt[c][j] = 0.f;
+            if (p.dout) {
+                Raw<W, E> v;
+                v.load(ring.input(kInDout), i);
+#pragma unroll
+                for (int j = 0; j < E; ++j) dt[c][j] = v[j];
+            }
+            if (p.dnext) {
+                Raw<W, E> v;
+                v.load(ring.input(kInDnext), i);
+                out[c].load(ring.input(kInOut), i);
+                float w[E];
+                get_factors<E>(f_next, p.n_vec, i, w);
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const float xo = out[c][j] * b, g = v[j] * w[j];
+                    s[0] = fmaf(g, xo, s[0]);
+                    cn[c][j] = fmaf(v[j], xo, cn[c][j]);
+                    dt[c][j] = fmaf(b, g, dt[c][j]);
+                }
+            } else out[c].zero();
+            if constexpr (kY) {
+                y[c].load(ring.input(kInY), i);
+                float w[E];
+                get_factors<E>(f_post, p.n_vec, i, w);
+                if (full) {
+                    gate[c].load(ring.input(kInGate), i);
+#pragma unroll
+                    for (int j = 0; j < E; ++j) w[j] *= gate[c][j];
+                }
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const float v = y[c][j] * a * w[j];
+                    s[1] = fmaf(dt[c][j], v, s[1]);
+                    s[2] = fmaf(out[c][j] * b, v, s[2]);
+                }
+            }
+        }
+        sums.sum(s);
+        if (p.group == 32) __syncwarp();
+        if (tid == 0) ring.issue();  // into the stage that every thread has read
+        ring.next();
+        const float cc = b * (s[0] / (float)p.d);
+        const float dv = s[1] - cc * s[2];
+        const float k2 = a * p.scale * gt, k3 = a * (p.scale * gt * (dv / (float)p.d));
+        if (kY && p.gate_kind == MOE_GATE_TOKEN && p.dgate && tid == 0) static_cast<float*>(p.dgate)[t] = p.scale * dv;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int i = tid + c * p.group;
+            if (i >= p.n_vec) continue;
+            float (&D)[E] = dt[c];
+#pragma unroll
+            for (int j = 0; j < E; ++j) D[j] = fmaf(out[c][j] * b, -cc, D[j]);
+            if (p.dr) store<W, E>(p.dr + t * p.lddr, i, D);
+            if constexpr (kY) {
+                float w[E], dyv[E];
+                get_factors<E>(f_post, p.n_vec, i, w);
+                if (full) {
+                    float dg[E];
+#pragma unroll
+                    for (int j = 0; j < E; ++j) {
+                        const float yn = y[c][j] * a;
+                        dg[j] = p.scale * D[j] * yn * w[j];
+                        w[j] *= gate[c][j];
+                        cp[c][j] = fmaf(D[j] * yn, gate[c][j], cp[c][j]);
+                        dyv[j] = fmaf(D[j] * w[j], k2, p.post ? -yn * k3 : 0.f);
+                    }
+                    if (p.dgate) store<W, E>(static_cast<char*>(p.dgate) + t * p.d * (int64_t)sizeof(W), i, dg);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < E; ++j) {
+                        const float yn = y[c][j] * a;
+                        cp[c][j] = fmaf(D[j] * yn, gt, cp[c][j]);
+                        dyv[j] = fmaf(D[j] * w[j], k2, p.post ? -yn * k3 : 0.f);
+                    }
+                }
+                if (p.dy) store<Y, E>(p.dy + t * p.lddy, i, dyv);
+            }
+        }
+    }
+    if (tid == 0 && t < p.T) ring.drain(t);
+    if (p.columns && first < p.T) {
+        float *col_next = p.part + first * 2 * p.d, *col_post = col_next + p.d;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int i = tid + c * p.group;
+            if (i >= p.n_vec) continue;
+            store<float, E>(col_next, i, cn[c]);
+            if constexpr (kY) store<float, E>(col_post, i, cp[c]);
+        }
+    }
+    grid_dep_launch();
+}
+
 // The groups' sums of 32 columns, added by eight warps, each in the groups'
 // order, then in the warps'.
 struct ColumnParams {
@@ -214,6 +361,30 @@ cudaError_t launch(BlockGradParams p, int parts, int sms, int* groups, cudaStrea
 template <typename W, typename Y>
 cudaError_t launch_vectors(const BlockGradParams& p, int e, int parts, int sms, int* groups, cudaStream_t st) {
     constexpr int kWide = 16 / (int)sizeof(W);
+    constexpr bool kY = !std::is_same_v<Y, None>;
+    if (e == kWide) {
+        constexpr int C = 16 / kWide;  // 16 values a thread
+        BlockGradParams q = p;
+        q.n_vec = p.d / e;
+        RingParams r = {};
+        const uint32_t row = (uint32_t)p.d * (uint32_t)sizeof(W);
+        auto input = [&](int i, const char* src, int64_t stride, uint32_t bytes) { r.src[i] = src; r.stride[i] = stride; r.bytes[i] = bytes; };
+        input(kInDout, p.dout, p.lddout, row);
+        input(kInDnext, p.dnext, p.lddnext, row);
+        input(kInOut, p.dnext ? p.out : nullptr, p.ldo, row);
+        if constexpr (kY) input(kInY, p.y, p.ldy, (uint32_t)p.d * (uint32_t)sizeof(Y));
+        if (kY && p.gate_kind == MOE_GATE_FULL) input(kInGate, static_cast<const char*>(p.gate), row, row);
+        RingShape s;
+        const uint32_t weights = ((p.dnext ? 1u : 0u) + (kY ? 1u : 0u)) * (uint32_t)p.d * 4;
+        if (q.n_vec <= kMaxGroup * C && ring_shape(r, p.T, q.n_vec, C, kY ? 512 : 768, p.columns ? parts / sms : kMaxGroups, weights, sms, s)) {
+            q.group = s.group; q.rows = s.groups;
+            auto kern = block_grad_ring_kernel<W, Y, C>;
+            cudaError_t err = allow_max_smem(kern);
+            if (err != cudaSuccess) return err;
+            *groups = s.blocks * s.groups;
+            return launch_pdl(kern, dim3((unsigned)s.blocks), dim3(s.group * s.groups), s.smem, st, q, r);
+        }
+    }
     return with_chunks<kWide>(p.d, e, [&](auto E, auto C) { return launch<W, Y, E, C>(p, parts, sms, groups, st); });
 }
 

@@ -19,7 +19,10 @@ EPS = float(np.float32(1e-6))
 SIZES = [(1, 1, "bf16"), (1, 1, "f32"), (3, 8, "bf16"), (2, 7, "f32"), (5, 100, "bf16"), (33, 256, "f32"), (33, 257, "bf16"),
          (9, 258, "bf16"), (1, 2048, "bf16"), (8, 4096, "bf16"), (4, 4097, "bf16"), (7, 1001, "f32"), (700, 64, "bf16"), (1300, 72, "f32"),
          (3, 8192, "bf16"), (2, 8192, "f32"), (3, 8200, "bf16"), (2, 9001, "f32"), (2, 20000, "bf16"), (1, 65536, "bf16"), (2, 65535, "f32"),
-         (1030, 1536, "bf16"), (400, 3584, "bf16"), (257, 2050, "bf16"), (3000, 33, "f32")]
+         (1030, 1536, "bf16"), (400, 3584, "bf16"), (257, 2050, "bf16"), (3000, 33, "f32"),
+         # long batches: rows that come through shared memory, from one group of threads an SM to twelve
+         (8000, 64, "bf16"), (7400, 264, "f32"), (3500, 1536, "bf16"), (1300, 3584, "bf16"), (1250, 4096, "f32"), (650, 8192, "bf16"),
+         (620, 8192, "f32"), (2600, 2056, "bf16")]
 
 
 def dims(T, d, kind):
