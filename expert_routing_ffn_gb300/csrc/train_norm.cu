@@ -44,7 +44,7 @@ template <typename W, typename Y, int E, int C>
 __global__ void __launch_bounds__(kMaxGroup) block_out_kernel(const BlockOutParams p) {
     constexpr bool kY = !std::is_same_v<Y, None>;
     constexpr int kN = C > 0 ? C : 1;
-    __shared__ float red[kBlock / 32][2][kMaxGroupWarps][4];
+    __shared__ __align__(16) float red[kBlock / 32][2][kMaxGroupWarps][4];
     const int tid = threadIdx.x % p.group, g = threadIdx.x / p.group;
     Sums sums = {red[g], p.group / 32, tid / 32, 1 + g, p.group, 0};
     // f(slot, i) for the vectors i of this thread

@@ -17,6 +17,36 @@ constexpr int kMaxGroup = 512, kMaxGroupWarps = kMaxGroup / 32, kBlock = 256;
 
 struct None {};  // the type of a y that is not there
 
+// ---------------------------------------------------------------- pairs of float32
+// The long batches' kernels are close to the issue rate: their arithmetic runs on
+// pairs, two values an instruction.
+typedef unsigned long long Pair;
+__device__ __forceinline__ Pair pair(float a, float b) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ Pair pair(float a) { return pair(a, a); }
+__device__ __forceinline__ float2 halves(Pair p) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ float both(Pair p) {
+    const float2 h = halves(p);
+    return h.x + h.y;
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 // E consecutive values of type W, as they lie in memory
 template <typename W, int E>
 struct Raw {
@@ -41,6 +71,10 @@ struct Raw {
         const uint4& q = v[i / 4];
         return i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
     }
+    __device__ __forceinline__ Pair pair_of(int i) const {  // values 2 i and 2 i + 1
+        if constexpr (sizeof(W) == 4) return pair(__uint_as_float(word(2 * i)), __uint_as_float(word(2 * i + 1)));
+        else return pair(bf16_lo(word(i)), bf16_hi(word(i)));
+    }
     __device__ __forceinline__ float operator[](int i) const {
         if constexpr (sizeof(W) == 4) return __uint_as_float(word(i));
         else return i % 2 ? bf16_hi(word(i / 2)) : bf16_lo(word(i / 2));
@@ -50,6 +84,7 @@ template <int E>
 struct Raw<None, E> {
     __device__ __forceinline__ void load(const void*, int) {}
     __device__ __forceinline__ void zero() {}
+    __device__ __forceinline__ Pair pair_of(int) const { return 0; }
     __device__ __forceinline__ float operator[](int) const { return 0.f; }
 };
 
@@ -79,6 +114,19 @@ __device__ __forceinline__ void store(void* row, int i, const float (&f)[E]) {
     }
 }
 
+// the same from pairs
+template <typename W, int E>
+__device__ __forceinline__ void store(void* row, int i, const Pair (&f)[E]) {
+    float v[2 * E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+        const float2 h = halves(f[j]);
+        v[2 * j] = h.x;
+        v[2 * j + 1] = h.y;
+    }
+    store<W, 2 * E>(row, i, v);
+}
+
 // Sums over the threads of a row: a group of G threads (whole warps), beside
 // other groups of the block.  Every thread gets them, in an order that does not
 // change.  Two buffers: a group's barrier for one sum also frees the buffer of
@@ -95,14 +143,17 @@ struct Sums {
         float(*b)[4] = buf[at];
         at ^= 1;
         if ((threadIdx.x & 31) == 0)
-#pragma unroll
-            for (int i = 0; i < N; ++i) b[warp][i] = v[i];
+            *reinterpret_cast<float4*>(b[warp]) = make_float4(v[0], N > 1 ? v[N > 1] : 0.f, N > 2 ? v[N > 2 ? 2 : 0] : 0.f, 0.f);
         sync();
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = 0.f;
-        for (int w = 0; w < warps; ++w)
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] += b[w][i];
+#pragma unroll 4
+        for (int w = 0; w < warps; ++w) {
+            const float4 q = *reinterpret_cast<const float4*>(b[w]);
+            v[0] += q.x;
+            if constexpr (N > 1) v[1] += q.y;
+            if constexpr (N > 2) v[2] += q.z;
+        }
     }
 };
 
@@ -186,9 +237,13 @@ __device__ __forceinline__ void put_factor(float* f, int n_vec, int col, float v
     f[4 * (col % E / 4 * n_vec + col / E) + col % 4] = v;
 }
 template <int E>
-__device__ __forceinline__ void get_factors(const float* f, int n_vec, int i, float (&v)[E]) {
+__device__ __forceinline__ void get_factors(const float* f, int n_vec, int i, Pair (&v)[E / 2]) {
 #pragma unroll
-    for (int h = 0; h < E / 4; ++h) *reinterpret_cast<float4*>(v + 4 * h) = *reinterpret_cast<const float4*>(f + 4 * (h * n_vec + i));
+    for (int h = 0; h < E / 4; ++h) {
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(f + 4 * (h * n_vec + i));
+        v[2 * h] = q.x;
+        v[2 * h + 1] = q.y;
+    }
 }
 
 // Whether a batch takes the ring, and its geometry: `groups` rows at a time of

@@ -28,7 +28,7 @@ struct BlockGradParams {
     char* dr; int64_t lddr; char* dy; int64_t lddy;  // strides in bytes
     void* dgate;
     int T, d, n_vec, post, group, rows, columns;     // columns: sums over the tokens are asked for
-    float offset, scale;
+    float offset, scale, inv_d;
     float* part;                                     // [groups][2][d]
 };
 
@@ -39,7 +39,7 @@ template <typename W, typename Y, int E, int C>
 __global__ void __launch_bounds__(kMaxGroup) block_grad_kernel(const BlockGradParams p) {
     constexpr bool kY = !std::is_same_v<Y, None>;
     constexpr int kN = C > 0 ? C : 1;
-    __shared__ float red[kBlock / 32][2][kMaxGroupWarps][4];
+    __shared__ __align__(16) float red[kBlock / 32][2][kMaxGroupWarps][4];
     const int tid = threadIdx.x % p.group, grp = threadIdx.x / p.group;
     Sums sums = {red[grp], p.group / 32, tid / 32, 1 + grp, p.group, 0};
     // f(slot, i) for the vectors i of this thread
@@ -162,16 +162,16 @@ __global__ void __launch_bounds__(kMaxGroup) block_grad_kernel(const BlockGradPa
 // D without its projection (t), out and y stay.
 enum { kInDout, kInDnext, kInOut, kInY, kInGate };
 
-template <typename W, typename Y, int C>
+template <typename W, typename Y, int C, bool FULL>
 __global__ void __launch_bounds__(std::is_same_v<Y, None> ? 768 : 512, 1)
     block_grad_ring_kernel(const __grid_constant__ BlockGradParams p, const __grid_constant__ RingParams rp) {
     constexpr bool kY = !std::is_same_v<Y, None>;
-    constexpr int E = 16 / (int)sizeof(W);
+    constexpr int E = 16 / (int)sizeof(W), P = E / 2;
     extern __shared__ __align__(128) char smem[];
-    __shared__ float red[kMaxGroups][2][kMaxGroupWarps][4];
+    __shared__ __align__(16) float red[kMaxGroups][2][kMaxGroupWarps][4];
     const int tid = threadIdx.x % p.group, grp = threadIdx.x / p.group;
     Sums sums = {red[grp], p.group / 32, tid / 32, 1 + grp, p.group, 0};
-    const int64_t groups = (int64_t)gridDim.x * p.rows, first = (int64_t)blockIdx.x * p.rows + grp;
+    const int groups = (int)gridDim.x * p.rows, first = (int)blockIdx.x * p.rows + grp;
     float *f_next = reinterpret_cast<float*>(smem), *f_post = f_next + (p.dnext ? p.d : 0);
     Ring ring(rp, smem, grp, p.T, first, groups);
     if (tid == 0) ring.init();
@@ -188,20 +188,28 @@ __global__ void __launch_bounds__(std::is_same_v<Y, None> ? 768 : 512, 1)
             put_factor<E>(f_post, p.n_vec, c, w);
         }
     }
+    // a row's own numbers, fetched a row ahead
+    float a1 = 1.f, b1 = 0.f, gt1 = 1.f;
+    auto fetch = [&](int t) {
+        if (t >= p.T) return;
+        if (kY && p.post) a1 = __ldg(p.rstd_post + t);
+        if (p.dnext) b1 = __ldg(p.rstd_next + t);
+        if (kY && p.gate_kind == MOE_GATE_TOKEN) gt1 = __ldg(static_cast<const float*>(p.gate) + t);
+    };
+    fetch(first);
     __syncthreads();
-    const bool full = kY && p.gate_kind == MOE_GATE_FULL;
-    float cn[C][E], cp[C][E];
+    Pair cn[C][P], cp[C][P];
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int j = 0; j < E; ++j) cn[c][j] = cp[c][j] = 0.f;
-    int64_t t = first;
+        for (int j = 0; j < P; ++j) cn[c][j] = cp[c][j] = 0;
+    int t = first;
     for (; t < p.T; t += groups) {
-        const float a = kY && p.post ? p.rstd_post[t] : 1.f, b = p.dnext ? p.rstd_next[t] : 0.f;
-        const float gt = kY && p.gate_kind == MOE_GATE_TOKEN ? static_cast<const float*>(p.gate)[t] : 1.f;
+        const float a = a1, b = b1, gt = gt1;
         if (!ring.wait()) break;
-        float s[3] = {0.f, 0.f, 0.f};
-        float dt[C][E];  // dout + b dnext w_next'
+        fetch(t + groups);
+        Pair s0 = 0, s1 = 0, s2 = 0;
+        Pair dt[C][P];  // dout + b dnext w_next'
         Raw<W, E> out[C], gate[C];
         Raw<Y, E> y[C];
 #pragma unroll
@@ -209,95 +217,106 @@ __global__ void __launch_bounds__(std::is_same_v<Y, None> ? 768 : 512, 1)
             const int i = tid + c * p.group;
             if (i >= p.n_vec) continue;
 #pragma unroll
-            for (int j = 0; j < E; ++j) dt[c][j] = 0.f;
+            for (int j = 0; j < P; ++j) dt[c][j] = 0;
             if (p.dout) {
                 Raw<W, E> v;
                 v.load(ring.input(kInDout), i);
 #pragma unroll
-                for (int j = 0; j < E; ++j) dt[c][j] = v[j];
+                for (int j = 0; j < P; ++j) dt[c][j] = v.pair_of(j);
             }
+            out[c].zero();
             if (p.dnext) {
                 Raw<W, E> v;
                 v.load(ring.input(kInDnext), i);
                 out[c].load(ring.input(kInOut), i);
-                float w[E];
+                Pair w[P];
                 get_factors<E>(f_next, p.n_vec, i, w);
 #pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    const float xo = out[c][j] * b, g = v[j] * w[j];
-                    s[0] = fmaf(g, xo, s[0]);
-                    cn[c][j] = fmaf(v[j], xo, cn[c][j]);
-                    dt[c][j] = fmaf(b, g, dt[c][j]);
+                for (int j = 0; j < P; ++j) {
+                    const Pair dn = v.pair_of(j), xo = mul(out[c].pair_of(j), pair(b)), g = mul(dn, w[j]);
+                    s0 = fma(g, xo, s0);
+                    cn[c][j] = fma(dn, xo, cn[c][j]);
+                    dt[c][j] = fma(pair(b), g, dt[c][j]);
                 }
-            } else out[c].zero();
+            }
             if constexpr (kY) {
                 y[c].load(ring.input(kInY), i);
-                float w[E];
+                Pair w[P];
                 get_factors<E>(f_post, p.n_vec, i, w);
-                if (full) {
+                if constexpr (FULL) {
                     gate[c].load(ring.input(kInGate), i);
 #pragma unroll
-                    for (int j = 0; j < E; ++j) w[j] *= gate[c][j];
+                    for (int j = 0; j < P; ++j) w[j] = mul(w[j], gate[c].pair_of(j));
                 }
 #pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    const float v = y[c][j] * a * w[j];
-                    s[1] = fmaf(dt[c][j], v, s[1]);
-                    s[2] = fmaf(out[c][j] * b, v, s[2]);
+                for (int j = 0; j < P; ++j) {
+                    const Pair v = mul(mul(y[c].pair_of(j), pair(a)), w[j]);
+                    s1 = fma(dt[c][j], v, s1);
+                    s2 = fma(mul(out[c].pair_of(j), pair(b)), v, s2);
                 }
             }
         }
-        sums.sum(s);
+        float cc, dv = 0.f;
+        if constexpr (kY) {
+            float s[3] = {both(s0), both(s1), both(s2)};
+            sums.sum(s);
+            cc = b * (s[0] * p.inv_d);
+            dv = s[1] - cc * s[2];
+        } else {
+            float s[1] = {both(s0)};
+            sums.sum(s);
+            cc = b * (s[0] * p.inv_d);
+        }
         if (p.group == 32) __syncwarp();
         if (tid == 0) ring.issue();  // into the stage that every thread has read
         ring.next();
-        const float cc = b * (s[0] / (float)p.d);
-        const float dv = s[1] - cc * s[2];
-        const float k2 = a * p.scale * gt, k3 = a * (p.scale * gt * (dv / (float)p.d));
+        const float k2 = a * p.scale * gt, k3 = p.post ? -a * (p.scale * gt * (dv * p.inv_d)) : 0.f;
         if (kY && p.gate_kind == MOE_GATE_TOKEN && p.dgate && tid == 0) static_cast<float*>(p.dgate)[t] = p.scale * dv;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int i = tid + c * p.group;
             if (i >= p.n_vec) continue;
-            float (&D)[E] = dt[c];
+            Pair (&D)[P] = dt[c];
 #pragma unroll
-            for (int j = 0; j < E; ++j) D[j] = fmaf(out[c][j] * b, -cc, D[j]);
-            if (p.dr) store<W, E>(p.dr + t * p.lddr, i, D);
+            for (int j = 0; j < P; ++j) D[j] = fma(mul(out[c].pair_of(j), pair(b)), pair(-cc), D[j]);
+            if (p.dr) store<W, P>(p.dr + t * p.lddr, i, D);
             if constexpr (kY) {
-                float w[E], dyv[E];
+                Pair w[P], dyv[P];
                 get_factors<E>(f_post, p.n_vec, i, w);
-                if (full) {
-                    float dg[E];
+                if constexpr (FULL) {
+                    Pair dg[P];
 #pragma unroll
-                    for (int j = 0; j < E; ++j) {
-                        const float yn = y[c][j] * a;
-                        dg[j] = p.scale * D[j] * yn * w[j];
-                        w[j] *= gate[c][j];
-                        cp[c][j] = fmaf(D[j] * yn, gate[c][j], cp[c][j]);
-                        dyv[j] = fmaf(D[j] * w[j], k2, p.post ? -yn * k3 : 0.f);
+                    for (int j = 0; j < P; ++j) {
+                        const Pair yn = mul(y[c].pair_of(j), pair(a)), Dy = mul(D[j], yn), ga = gate[c].pair_of(j);
+                        dg[j] = mul(mul(Dy, w[j]), pair(p.scale));
+                        w[j] = mul(w[j], ga);
+                        cp[c][j] = fma(Dy, ga, cp[c][j]);
+                        dyv[j] = mul(mul(D[j], w[j]), pair(k2));
+                        if (p.post) dyv[j] = fma(yn, pair(k3), dyv[j]);
                     }
-                    if (p.dgate) store<W, E>(static_cast<char*>(p.dgate) + t * p.d * (int64_t)sizeof(W), i, dg);
+                    if (p.dgate) store<W, P>(static_cast<char*>(p.dgate) + (int64_t)t * p.d * (int64_t)sizeof(W), i, dg);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < E; ++j) {
-                        const float yn = y[c][j] * a;
-                        cp[c][j] = fmaf(D[j] * yn, gt, cp[c][j]);
-                        dyv[j] = fmaf(D[j] * w[j], k2, p.post ? -yn * k3 : 0.f);
+                    for (int j = 0; j < P; ++j) {
+                        const Pair yn = mul(y[c].pair_of(j), pair(a));
+                        cp[c][j] = fma(mul(D[j], yn), pair(gt), cp[c][j]);
+                        dyv[j] = mul(mul(D[j], w[j]), pair(k2));
+                        if (p.post) dyv[j] = fma(yn, pair(k3), dyv[j]);
                     }
                 }
-                if (p.dy) store<Y, E>(p.dy + t * p.lddy, i, dyv);
+                if (p.dy) store<Y, P>(p.dy + t * p.lddy, i, dyv);
             }
         }
     }
     if (tid == 0 && t < p.T) ring.drain(t);
     if (p.columns && first < p.T) {
-        float *col_next = p.part + first * 2 * p.d, *col_post = col_next + p.d;
+        float *col_next = p.part + (int64_t)first * 2 * p.d, *col_post = col_next + p.d;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int i = tid + c * p.group;
             if (i >= p.n_vec) continue;
-            store<float, E>(col_next, i, cn[c]);
-            if constexpr (kY) store<float, E>(col_post, i, cp[c]);
+            store<float, P>(col_next, i, cn[c]);
+            if constexpr (kY) store<float, P>(col_post, i, cp[c]);
         }
     }
     grid_dep_launch();
@@ -378,7 +397,9 @@ cudaError_t launch_vectors(const BlockGradParams& p, int e, int parts, int sms, 
         const uint32_t weights = ((p.dnext ? 1u : 0u) + (kY ? 1u : 0u)) * (uint32_t)p.d * 4;
         if (q.n_vec <= kMaxGroup * C && ring_shape(r, p.T, q.n_vec, C, kY ? 512 : 768, p.columns ? parts / sms : kMaxGroups, weights, sms, s)) {
             q.group = s.group; q.rows = s.groups;
-            auto kern = block_grad_ring_kernel<W, Y, C>;
+            auto kern = block_grad_ring_kernel<W, Y, C, false>;
+            if constexpr (kY)
+                if (p.gate_kind == MOE_GATE_FULL) kern = block_grad_ring_kernel<W, Y, C, true>;
             cudaError_t err = allow_max_smem(kern);
             if (err != cudaSuccess) return err;
             *groups = s.blocks * s.groups;
@@ -404,6 +425,7 @@ cudaError_t launch_block_out_grad(const NormGradArgs& a, cudaStream_t st, int* l
     const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
     p.dgate = channel ? nullptr : a.dgate;
     p.T = a.T; p.d = a.d; p.post = a.post; p.offset = a.offset; p.scale = a.scale; p.part = a.part;
+    p.inv_d = 1.f / (float)a.d;
     p.columns = a.dw_post || a.dw_next || (channel && a.dgate);
     const int parts = norm_parts(a.T, a.d);
     int groups = 0;
