@@ -118,6 +118,33 @@ __device__ __forceinline__ void store8(W* row, int c, int cols, const float (&f)
     }
 }
 
+// The eight values of a row whose packed bytes lie in a lane's two words: with j the
+// lane of four and c its first column in load8's order, columns 2 j + 8 m and
+// 2 j + 1 + 8 m of the block, m = 0 .. 3, at f[2 m] and f[2 m + 1].
+template <typename W, bool VEC>
+__device__ __forceinline__ void load_interleaved(const W* row, int c, int cols, float (&f)[8]) {
+    const int first = (c & ~31) + (c >> 3 & 3) * 2;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const int at = first + 8 * m;
+        f[2 * m] = f[2 * m + 1] = 0.f;
+        if constexpr (VEC) {  // whole vectors: both values or none
+            if (at < cols) {
+                if constexpr (sizeof(W) == 2) {
+                    const uint32_t v = *reinterpret_cast<const uint32_t*>(row + at);
+                    f[2 * m] = bf16_lo(v); f[2 * m + 1] = bf16_hi(v);
+                } else {
+                    const float2 v = *reinterpret_cast<const float2*>(row + at);
+                    f[2 * m] = v.x; f[2 * m + 1] = v.y;
+                }
+            }
+        } else {
+            if (at < cols) f[2 * m] = to_f32(row[at]);
+            if (at + 1 < cols) f[2 * m + 1] = to_f32(row[at + 1]);
+        }
+    }
+}
+
 // one value of packed rows of nb blocks
 __device__ __forceinline__ float value_at(const int8_t* q, const uint8_t* scale, int64_t row, int col, int nb) {
     const int64_t block = row * nb + col / 32;

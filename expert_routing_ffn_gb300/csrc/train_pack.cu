@@ -15,46 +15,68 @@ using namespace pack8;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32, kCols = 256;  // columns of a warp
 
+// A warp takes up to kPieces pieces of kCols columns of a row at a time, all
+// their loads before any use.
+constexpr int kPieces = 4;
+
 struct PackParams {
     const void* x; int64_t ldx;  // elements
     int8_t* q; uint8_t* scale;
     int64_t rows;
-    int cols, nb, pieces;        // pieces of kCols columns
+    int cols, nb, chunks;        // chunks of kPieces pieces in a row
     const int32_t* index; int divisor;
     int64_t src_rows;
 };
+
+// f(row, first column of the chunk) for the chunks of this warp, round robin
+template <typename F>
+__device__ __forceinline__ void each_chunk(const PackParams& p, F f) {
+    const int64_t first = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), stride = (int64_t)gridDim.x * kWarps;
+    const int64_t dr = stride / p.chunks;
+    const int dc = (int)(stride - dr * p.chunks);
+    int64_t r = first / p.chunks;
+    int c = (int)(first - r * p.chunks);
+    while (r < p.rows) {
+        f(r, c * kPieces * kCols);
+        r += dr;
+        c += dc;
+        if (c >= p.chunks) { c -= p.chunks; ++r; }
+    }
+}
 
 template <typename W, bool VEC>
 __global__ void __launch_bounds__(kThreads) pack_rows_kernel(const PackParams p) {
     const int lane = threadIdx.x & 31;
     grid_dep_wait();
-    const int64_t items = p.rows * p.pieces;
-    for (int64_t it = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); it < items; it += (int64_t)gridDim.x * kWarps) {
-        const int64_t r = it / p.pieces;
-        const int c = (int)(it - r * p.pieces) * kCols + lane * 8;
-        float f[8];
-        load8<W, VEC>(static_cast<const W*>(p.x) + r * p.ldx, c, p.cols, f);
-        uint32_t m = 0;
+    each_chunk(p, [&](int64_t r, int c0) {
+        float f[kPieces][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, magnitude(f[i]));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const uint32_t E = exponent(m);
-        const float inv = to_steps(E);
-        uint32_t b[8];
-        if (E == kTop)
+        for (int u = 0; u < kPieces; ++u) load8<W, VEC>(static_cast<const W*>(p.x) + r * p.ldx, c0 + u * kCols + lane * 8, p.cols, f[u]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = within(f[i], E);
+        for (int u = 0; u < kPieces; ++u) {
+            if (c0 + u * kCols >= p.cols) break;  // the same for the warp
+            uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = E == 255u ? 0u : quantise(f[i], inv);
-        const uint2 w = to_packed(bytes4(b[0], b[1], b[2], b[3]), bytes4(b[4], b[5], b[6], b[7]));
-        const int block = c / 32;
-        if (block < p.nb) {
-            const int64_t at = r * p.nb + block;
-            *reinterpret_cast<uint2*>(p.q + at * 32 + (lane & 3) * 8) = w;
-            if ((lane & 3) == 0) p.scale[at] = (uint8_t)E;
+            for (int i = 0; i < 8; ++i) m = max(m, magnitude(f[u][i]));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const uint32_t E = exponent(m);
+            const float inv = to_steps(E);
+            uint32_t b[8];
+            if (E == kTop)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[u][i] = within(f[u][i], E);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) b[i] = E == 255u ? 0u : quantise(f[u][i], inv);
+            const uint2 w = to_packed(bytes4(b[0], b[1], b[2], b[3]), bytes4(b[4], b[5], b[6], b[7]));
+            const int block = (c0 + u * kCols) / 32 + lane / 4;
+            if (block < p.nb) {
+                const int64_t at = r * p.nb + block;
+                *reinterpret_cast<uint2*>(p.q + at * 32 + (lane & 3) * 8) = w;
+                if ((lane & 3) == 0) p.scale[at] = (uint8_t)E;
+            }
         }
-    }
+    });
     grid_dep_launch();
 }
 
@@ -62,34 +84,45 @@ template <typename W, bool VEC>
 __global__ void __launch_bounds__(kThreads) unpack_rows_kernel(const PackParams p) {
     const int lane = threadIdx.x & 31;
     grid_dep_wait();
-    const int64_t items = p.rows * p.pieces;
-    for (int64_t it = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); it < items; it += (int64_t)gridDim.x * kWarps) {
-        const int64_t r = it / p.pieces;
-        const int c = (int)(it - r * p.pieces) * kCols + lane * 8, block = c / 32;
+    each_chunk(p, [&](int64_t r, int c0) {
         int64_t src = r;
         if (p.index) {
             const int i = p.index[r];
             src = i < 0 ? -1 : i / p.divisor;
         }
-        uint2 w = make_uint2(0, 0);
-        float s = 0.f;
-        if (src >= 0 && src < p.src_rows && block < p.nb) {
-            const int64_t at = src * p.nb + block;
-            w = *reinterpret_cast<const uint2*>(p.q + at * 32 + (lane & 3) * 8);
-            s = step(p.scale[at]);
+        const bool there = src >= 0 && src < p.src_rows;
+        uint2 w[kPieces];
+        uint32_t E[kPieces];
+#pragma unroll
+        for (int u = 0; u < kPieces; ++u) {
+            const int block = (c0 + u * kCols) / 32 + lane / 4;
+            w[u] = make_uint2(0, 0);
+            E[u] = 0;
+            if (there && block < p.nb) {
+                const int64_t at = src * p.nb + block;
+                w[u] = *reinterpret_cast<const uint2*>(p.q + at * 32 + (lane & 3) * 8);
+                E[u] = p.scale[at];
+            }
         }
-        w = to_columns(w);
-        const uint32_t lo = biased(w.x), hi = biased(w.y);
-        const float f[8] = {value<0>(lo) * s, value<1>(lo) * s, value<2>(lo) * s, value<3>(lo) * s,
-                            value<0>(hi) * s, value<1>(hi) * s, value<2>(hi) * s, value<3>(hi) * s};
-        store8<W, VEC>(static_cast<W*>(const_cast<void*>(p.x)) + r * p.ldx, c, p.cols, f);
-    }
+#pragma unroll
+        for (int u = 0; u < kPieces; ++u) {
+            if (c0 + u * kCols >= p.cols) break;  // the same for the warp
+            const float s = step(E[u]);
+            const uint2 v = to_columns(w[u]);
+            const uint32_t lo = biased(v.x), hi = biased(v.y);
+            const float f[8] = {value<0>(lo) * s, value<1>(lo) * s, value<2>(lo) * s, value<3>(lo) * s,
+                                value<0>(hi) * s, value<1>(hi) * s, value<2>(hi) * s, value<3>(hi) * s};
+            store8<W, VEC>(static_cast<W*>(const_cast<void*>(p.x)) + r * p.ldx, c0 + u * kCols + lane * 8, p.cols, f);
+        }
+    });
     grid_dep_launch();
 }
 
 // ---------------------------------------------------------------- combine, gradient
-// One block per token, as in combine_grad_kernel: dout's row once, every slot's
-// row of y in 8 bits for dgate, and its row of dy written.
+// One block per token, as in combine_grad_kernel: dout's row, every slot's row of
+// y in 8 bits for dgate, eight slots' loads before any use, and its row of dy
+// written.  A thread takes dout in two orders, by columns for dy and by the order
+// of its two words for the products, so the words need no exchange.
 constexpr int kGradThreads = 128, kGradWarps = kGradThreads / 32;
 
 struct GradParams {
@@ -119,34 +152,42 @@ __global__ void __launch_bounds__(kGradThreads) combine_grad_packed_kernel(const
     for (int s = 0; s < KB; ++s) dot[s] = 0.f;
     for (int c0 = warp * kCols; c0 < p.d; c0 += kGradWarps * kCols) {
         const int c = c0 + lane * 8, block = c / 32;
-        float g[8];
+        float g[8], h[8];
         load8<W, VEC>(dout, c, p.d, g);
+        load_interleaved<W, VEC>(dout, c, p.d, h);
 #pragma unroll
-        for (int s = 0; s < KB; ++s) {
-            const int row = row_s[s];
-            if (row == -1) continue;
-            if (row >= 0 && p.dgate) {
-                uint2 w = make_uint2(0, 0);
-                float e = 0.f;
-                if (block < p.nb) {
+        for (int s0 = 0; s0 < KB; s0 += 8) {
+            uint2 w[8];
+            uint32_t E[8];
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                w[s] = make_uint2(0, 0);
+                E[s] = 0;
+                const int row = row_s[s0 + s];
+                if (p.dgate && row >= 0 && block < p.nb) {
                     const int64_t at = (int64_t)row * p.nb + block;
-                    w = *reinterpret_cast<const uint2*>(p.q + at * 32 + (lane & 3) * 8);
-                    e = step(p.scale[at]);
+                    w[s] = *reinterpret_cast<const uint2*>(p.q + at * 32 + (lane & 3) * 8);
+                    E[s] = p.scale[at];
                 }
-                w = to_columns(w);
-                const uint32_t lo = biased(w.x), hi = biased(w.y);
-                float v = g[0] * value<0>(lo);
-                v = fmaf(g[1], value<1>(lo), v); v = fmaf(g[2], value<2>(lo), v); v = fmaf(g[3], value<3>(lo), v);
-                v = fmaf(g[4], value<0>(hi), v); v = fmaf(g[5], value<1>(hi), v);
-                v = fmaf(g[6], value<2>(hi), v); v = fmaf(g[7], value<3>(hi), v);
-                dot[s] = fmaf(v, e, dot[s]);
             }
-            if (p.dy) {
-                float f[8];
-                const float a = row >= 0 ? gate_s[s] : 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = row >= 0 ? a * g[i] : 0.f;
-                store8<W, VEC>(static_cast<W*>(p.dy) + (int64_t)(row >= 0 ? row : -2 - row) * p.d, c, p.d, f);
+            for (int s = 0; s < 8; ++s) {
+                const int row = row_s[s0 + s];
+                if (p.dgate && row >= 0) {
+                    const uint32_t lo = biased(w[s].x), hi = biased(w[s].y);
+                    float v = h[0] * value<0>(lo);
+                    v = fmaf(h[2], value<1>(lo), v); v = fmaf(h[4], value<2>(lo), v); v = fmaf(h[6], value<3>(lo), v);
+                    v = fmaf(h[1], value<0>(hi), v); v = fmaf(h[3], value<1>(hi), v);
+                    v = fmaf(h[5], value<2>(hi), v); v = fmaf(h[7], value<3>(hi), v);
+                    dot[s0 + s] = fmaf(v, step(E[s]), dot[s0 + s]);
+                }
+                if (p.dy && row != -1) {
+                    float f[8];
+                    const float a = gate_s[s0 + s];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = row >= 0 ? a * g[i] : 0.f;
+                    store8<W, VEC>(static_cast<W*>(p.dy) + (int64_t)(row >= 0 ? row : -2 - row) * p.d, c, p.d, f);
+                }
             }
         }
     }
@@ -184,8 +225,8 @@ cudaError_t launch_pack_rows(int64_t rows, int cols, const void* x, int64_t ldx,
                              int sms, cudaStream_t st) {
     PackParams p = {};
     p.x = x; p.ldx = ldx; p.q = q; p.scale = scale; p.rows = rows; p.cols = cols; p.nb = pack_blocks(cols);
-    p.pieces = (cols + kCols - 1) / kCols;
-    const dim3 grid(pack_grid(rows * p.pieces, sms)), block(kThreads);
+    p.chunks = (cols + kCols * kPieces - 1) / (kCols * kPieces);
+    const dim3 grid(pack_grid(rows * p.chunks, sms)), block(kThreads);
     const bool vec = vectors(x, ldx, cols, bf16);
     if (bf16)
         return vec ? launch_pdl(pack_rows_kernel<__nv_bfloat16, true>, grid, block, 0, st, p)
@@ -198,9 +239,9 @@ cudaError_t launch_unpack_rows(int64_t src_rows, int cols, const int8_t* q, cons
                                int divisor, int64_t rows, void* out, int64_t ldo, bool bf16, int sms, cudaStream_t st) {
     PackParams p = {};
     p.x = out; p.ldx = ldo; p.q = const_cast<int8_t*>(q); p.scale = const_cast<uint8_t*>(scale); p.rows = rows;
-    p.cols = cols; p.nb = pack_blocks(cols); p.pieces = (cols + kCols - 1) / kCols;
+    p.cols = cols; p.nb = pack_blocks(cols); p.chunks = (cols + kCols * kPieces - 1) / (kCols * kPieces);
     p.index = index; p.divisor = divisor; p.src_rows = src_rows;
-    const dim3 grid(pack_grid(rows * p.pieces, sms)), block(kThreads);
+    const dim3 grid(pack_grid(rows * p.chunks, sms)), block(kThreads);
     const bool vec = vectors(out, ldo, cols, bf16);
     if (bf16)
         return vec ? launch_pdl(unpack_rows_kernel<__nv_bfloat16, true>, grid, block, 0, st, p)
