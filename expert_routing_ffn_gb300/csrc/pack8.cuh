@@ -42,6 +42,10 @@ __device__ __forceinline__ float value(uint32_t biased_word, int i) {
 }
 template <int I>
 __device__ __forceinline__ float value(uint32_t biased_word) { return value(biased_word, I); }
+// the same before kRaw is taken off
+constexpr float kRaw = 8388736.f;
+template <int I>
+__device__ __forceinline__ float raw(uint32_t biased_word) { return __uint_as_float(__byte_perm(biased_word, 0x4b000000u, 0x7440 | I)); }
 
 __device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);

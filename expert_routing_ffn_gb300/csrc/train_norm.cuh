@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "pairs.cuh"
 #include "train.h"
 
 namespace moe {
@@ -16,36 +17,6 @@ namespace norm {
 constexpr int kMaxGroup = 512, kMaxGroupWarps = kMaxGroup / 32, kBlock = 256;
 
 struct None {};  // the type of a y that is not there
-
-// ---------------------------------------------------------------- pairs of float32
-// The long batches' kernels are close to the issue rate: their arithmetic runs on
-// pairs, two values an instruction.
-typedef unsigned long long Pair;
-__device__ __forceinline__ Pair pair(float a, float b) {
-    Pair r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ Pair pair(float a) { return pair(a, a); }
-__device__ __forceinline__ float2 halves(Pair p) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
-    return r;
-}
-__device__ __forceinline__ float both(Pair p) {
-    const float2 h = halves(p);
-    return h.x + h.y;
-}
-__device__ __forceinline__ Pair mul(Pair a, Pair b) {
-    Pair r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
-    Pair r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 
 // E consecutive values of type W, as they lie in memory
 template <typename W, int E>

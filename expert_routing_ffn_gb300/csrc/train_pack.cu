@@ -5,6 +5,7 @@
 // block of 32: its largest magnitude takes two shuffles, and the turn from
 // columns to the order of a matrix fragment two more.
 #include "pack8.cuh"
+#include "pairs.cuh"
 #include "train.h"
 
 namespace moe {
@@ -120,10 +121,10 @@ __global__ void __launch_bounds__(kThreads) unpack_rows_kernel(const PackParams 
 
 // ---------------------------------------------------------------- combine, gradient
 // One block per token, as in combine_grad_kernel: dout's row, every slot's row of
-// y in 8 bits for dgate, eight slots' loads before any use, and its row of dy
-// written.  A thread takes dout in two orders, by columns for dy and by the order
+// y in 8 bits for dgate, eight slots' loads before any use and without a branch, and
+// its row of dy written.  A thread takes dout in two orders, by columns for dy and by the order
 // of its two words for the products, so the words need no exchange.
-constexpr int kGradThreads = 128, kGradWarps = kGradThreads / 32;
+constexpr int kGradWarps = 8;  // at most
 
 struct GradParams {
     const void* dout; int64_t lddout; const int8_t* q; const uint8_t* scale; const float* gate; const int32_t* inv;
@@ -132,11 +133,11 @@ struct GradParams {
 };
 
 template <typename W, bool VEC, int KB>
-__global__ void __launch_bounds__(kGradThreads) combine_grad_packed_kernel(const GradParams p) {
+__global__ void __launch_bounds__(kGradWarps * 32, 3) combine_grad_packed_kernel(const GradParams p) {
     __shared__ float part[kGradWarps][KB];
     __shared__ int row_s[KB];
     __shared__ float gate_s[KB];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const int64_t t = blockIdx.x;
     grid_dep_wait();
     if (tid < KB) {
@@ -150,44 +151,48 @@ __global__ void __launch_bounds__(kGradThreads) combine_grad_packed_kernel(const
     float dot[KB];
 #pragma unroll
     for (int s = 0; s < KB; ++s) dot[s] = 0.f;
-    for (int c0 = warp * kCols; c0 < p.d; c0 += kGradWarps * kCols) {
-        const int c = c0 + lane * 8, block = c / 32;
+    for (int c0 = warp * kCols; c0 < p.d; c0 += warps * kCols) {
+        const int c = c0 + lane * 8, block = min(c / 32, p.nb - 1);  // past the last block dout has zeros
         float g[8], h[8];
         load8<W, VEC>(dout, c, p.d, g);
         load_interleaved<W, VEC>(dout, c, p.d, h);
+        if (p.dgate) {
 #pragma unroll
-        for (int s0 = 0; s0 < KB; s0 += 8) {
-            uint2 w[8];
-            uint32_t E[8];
+            for (int s0 = 0; s0 < KB; s0 += 8) {
+                uint2 w[8];
+                uint32_t E[8];
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                w[s] = make_uint2(0, 0);
-                E[s] = 0;
-                const int row = row_s[s0 + s];
-                if (p.dgate && row >= 0 && block < p.nb) {
-                    const int64_t at = (int64_t)row * p.nb + block;
+                for (int s = 0; s < 8; ++s) {  // a slot without a row reads row 0, and its sum is not used
+                    const int64_t at = (int64_t)max(row_s[s0 + s], 0) * p.nb + block;
                     w[s] = *reinterpret_cast<const uint2*>(p.q + at * 32 + (lane & 3) * 8);
                     E[s] = p.scale[at];
                 }
-            }
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                const int row = row_s[s0 + s];
-                if (p.dgate && row >= 0) {
+                for (int s = 0; s < 8; ++s) {
                     const uint32_t lo = biased(w[s].x), hi = biased(w[s].y);
-                    float v = h[0] * value<0>(lo);
-                    v = fmaf(h[2], value<1>(lo), v); v = fmaf(h[4], value<2>(lo), v); v = fmaf(h[6], value<3>(lo), v);
-                    v = fmaf(h[1], value<0>(hi), v); v = fmaf(h[3], value<1>(hi), v);
-                    v = fmaf(h[5], value<2>(hi), v); v = fmaf(h[7], value<3>(hi), v);
-                    dot[s0 + s] = fmaf(v, step(E[s]), dot[s0 + s]);
+                    Pair v = mul(pair(h[0], h[1]), add(pair(raw<0>(lo), raw<0>(hi)), pair(-kRaw)));
+                    v = fma(pair(h[2], h[3]), add(pair(raw<1>(lo), raw<1>(hi)), pair(-kRaw)), v);
+                    v = fma(pair(h[4], h[5]), add(pair(raw<2>(lo), raw<2>(hi)), pair(-kRaw)), v);
+                    v = fma(pair(h[6], h[7]), add(pair(raw<3>(lo), raw<3>(hi)), pair(-kRaw)), v);
+                    dot[s0 + s] = fmaf(both(v), step(E[s]), dot[s0 + s]);
                 }
-                if (p.dy && row != -1) {
-                    float f[8];
-                    const float a = gate_s[s0 + s];
+            }
+        }
+        if (p.dy) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = row >= 0 ? a * g[i] : 0.f;
-                    store8<W, VEC>(static_cast<W*>(p.dy) + (int64_t)(row >= 0 ? row : -2 - row) * p.d, c, p.d, f);
+            for (int s = 0; s < KB; ++s) {
+                const int row = row_s[s];
+                if (row == -1) continue;
+                float f[8] = {};
+                if (row >= 0) {
+                    const Pair a = pair(gate_s[s]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 v = halves(mul(pair(g[2 * i], g[2 * i + 1]), a));
+                        f[2 * i] = v.x; f[2 * i + 1] = v.y;
+                    }
                 }
+                store8<W, VEC>(static_cast<W*>(p.dy) + (int64_t)(row >= 0 ? row : -2 - row) * p.d, c, p.d, f);
             }
         }
     }
@@ -201,7 +206,8 @@ __global__ void __launch_bounds__(kGradThreads) combine_grad_packed_kernel(const
         if (tid < p.k) {
             float v = 0.f;
 #pragma unroll
-            for (int w = 0; w < kGradWarps; ++w) v += part[w][tid];
+            for (int w = 0; w < kGradWarps; ++w)
+                if (w < warps) v += part[w][tid];
             p.dgate[t * p.k + tid] = row_s[tid] >= 0 ? v : 0.f;
         }
     }
@@ -252,8 +258,11 @@ cudaError_t launch_unpack_rows(int64_t src_rows, int cols, const int8_t* q, cons
 
 template <typename W, bool VEC>
 static cudaError_t launch_grad(const GradParams& p, int T, cudaStream_t st) {
-    return p.k <= 8 ? launch_pdl(combine_grad_packed_kernel<W, VEC, 8>, dim3(T), dim3(kGradThreads), 0, st, p)
-                    : launch_pdl(combine_grad_packed_kernel<W, VEC, 16>, dim3(T), dim3(kGradThreads), 0, st, p);
+    // as many warps as share a row's pieces evenly
+    const int pieces = (p.d + kCols - 1) / kCols, turns = (pieces + kGradWarps - 1) / kGradWarps;
+    const dim3 block(32 * ((pieces + turns - 1) / turns));
+    return p.k <= 8 ? launch_pdl(combine_grad_packed_kernel<W, VEC, 8>, dim3(T), block, 0, st, p)
+                    : launch_pdl(combine_grad_packed_kernel<W, VEC, 16>, dim3(T), block, 0, st, p);
 }
 
 cudaError_t launch_combine_rows_grad_packed(const CombineRowsGradPackedArgs& a, cudaStream_t st) {
