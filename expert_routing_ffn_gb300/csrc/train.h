@@ -124,6 +124,7 @@ struct CombineRowsGradPackedArgs {
     void* dy; float* dgate;
     int T, k, d;
     bool bf16;
+    int sms;
 };
 cudaError_t launch_combine_rows_grad_packed(const CombineRowsGradPackedArgs& a, cudaStream_t st);
 

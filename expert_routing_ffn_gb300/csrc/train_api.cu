@@ -560,6 +560,7 @@ moe_status moe_combine_rows_grad_packed(const moe_dims* dims, const void* dout, 
     CombineRowsGradPackedArgs a;
     a.dout = dout; a.lddout = lddout; a.q = y_q; a.scale = y_scale; a.gate = gate; a.inv = inv_perm; a.dy = dy_perm;
     a.dgate = dgate; a.T = dims->T; a.k = dims->k; a.d = dims->d; a.bf16 = dims->wtype == MOE_DTYPE_BF16;
+    a.sms = device_sms();
     TRAIN_CUDA(launch_combine_rows_grad_packed(a, S(stream)));
     note_launches(1);
     return MOE_OK;

@@ -166,7 +166,7 @@ template <typename W, typename Y, int C, bool FULL>
 __global__ void __launch_bounds__(std::is_same_v<Y, None> ? 768 : 512, 1)
     block_grad_ring_kernel(const __grid_constant__ BlockGradParams p, const __grid_constant__ RingParams rp) {
     constexpr bool kY = !std::is_same_v<Y, None>;
-    constexpr int E = 16 / (int)sizeof(W), P = E / 2;
+    constexpr int E = 16 / (int)sizeof(W), P = E / 2, kSums = kY ? 2 : 1;  // sums of a column
     extern __shared__ __align__(128) char smem[];
     __shared__ __align__(16) float red[kMaxGroups][2][kMaxGroupWarps][4];
     const int tid = threadIdx.x % p.group, grp = threadIdx.x / p.group;
@@ -309,21 +309,31 @@ __global__ void __launch_bounds__(std::is_same_v<Y, None> ? 768 : 512, 1)
         }
     }
     if (tid == 0 && t < p.T) ring.drain(t);
-    if (p.columns && first < p.T) {
-        float *col_next = p.part + (int64_t)first * 2 * p.d, *col_post = col_next + p.d;
+    if (p.columns) {
+        // the groups' sums meet in shared memory, where the rings were, and leave as one
+        float* mine = reinterpret_cast<float*>(smem + rp.rings) + (size_t)grp * kSums * p.d;
+        __syncthreads();
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int i = tid + c * p.group;
             if (i >= p.n_vec) continue;
-            store<float, P>(col_next, i, cn[c]);
-            if constexpr (kY) store<float, P>(col_post, i, cp[c]);
+            store<float, P>(mine, i, cn[c]);
+            if constexpr (kY) store<float, P>(mine + p.d, i, cp[c]);
+        }
+        __syncthreads();
+        const float* all = reinterpret_cast<const float*>(smem + rp.rings);
+        for (int c = threadIdx.x; c < kSums * p.d; c += blockDim.x) {
+            float v = all[c];
+            for (int g = 1; g < p.rows; ++g) v += all[(size_t)g * kSums * p.d + c];
+            p.part[(int64_t)blockIdx.x * 2 * p.d + c] = v;
         }
     }
     grid_dep_launch();
 }
 
-// The groups' sums of 32 columns, added by eight warps, each in the groups'
-// order, then in the warps'.
+// The groups' sums of 32 columns, added by the block's warps, each in the groups'
+// order, then in the warps'.  A warp for every eight groups: 912 groups of 1536
+// columns took eight warps 13 us.
 struct ColumnParams {
     const float* part;
     int groups, d, gate_kind, post, accumulate;
@@ -333,20 +343,19 @@ struct ColumnParams {
 };
 
 template <typename W, typename G>
-__global__ void __launch_bounds__(256) column_sums_kernel(const ColumnParams p) {
-    __shared__ float red[8][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane, which = blockIdx.y;
+__global__ void __launch_bounds__(1024) column_sums_kernel(const ColumnParams p) {
+    __shared__ float red[32][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, col = blockIdx.x * 32 + lane, which = blockIdx.y;
     grid_dep_wait();
     float s = 0.f;
     if (col < p.d && (which || p.dw_next))
 #pragma unroll 8
-        for (int g = warp; g < p.groups; g += 8) s += __ldcg(p.part + ((int64_t)g * 2 + which) * p.d + col);
+        for (int g = warp; g < p.groups; g += warps) s += __ldcg(p.part + ((int64_t)g * 2 + which) * p.d + col);
     red[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && col < p.d) {
         s = 0.f;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) s += red[w][lane];
+        for (int w = 0; w < warps; ++w) s += red[w][lane];
         auto put = [&](void* to, float v) {
             G* o = static_cast<G*>(to) + col;
             if constexpr (sizeof(G) == 4) *o = p.accumulate ? *o + v : v;
@@ -395,14 +404,16 @@ cudaError_t launch_vectors(const BlockGradParams& p, int e, int parts, int sms, 
         if (kY && p.gate_kind == MOE_GATE_FULL) input(kInGate, static_cast<const char*>(p.gate), row, row);
         RingShape s;
         const uint32_t weights = ((p.dnext ? 1u : 0u) + (kY ? 1u : 0u)) * (uint32_t)p.d * 4;
-        if (q.n_vec <= kMaxGroup * C && ring_shape(r, p.T, q.n_vec, C, kY ? 512 : 768, p.columns ? parts / sms : kMaxGroups, weights, sms, s)) {
+        // The sums of a group (two float32 a column with y, else one) fit where its ring was: at least two stages of
+        // two rows or more of at least two bytes a value.
+        if (q.n_vec <= kMaxGroup * C && (!p.columns || parts >= sms) && ring_shape(r, p.T, q.n_vec, C, kY ? 512 : 768, kMaxGroups, weights, sms, s)) {
             q.group = s.group; q.rows = s.groups;
             auto kern = block_grad_ring_kernel<W, Y, C, false>;
             if constexpr (kY)
                 if (p.gate_kind == MOE_GATE_FULL) kern = block_grad_ring_kernel<W, Y, C, true>;
             cudaError_t err = allow_max_smem(kern);
             if (err != cudaSuccess) return err;
-            *groups = s.blocks * s.groups;
+            *groups = s.blocks;
             return launch_pdl(kern, dim3((unsigned)s.blocks), dim3(s.group * s.groups), s.smem, st, q, r);
         }
     }
@@ -443,11 +454,11 @@ cudaError_t launch_block_out_grad(const NormGradArgs& a, cudaStream_t st, int* l
     c.part = a.part; c.groups = groups; c.d = a.d; c.gate_kind = a.gate_kind; c.post = a.post; c.accumulate = a.accumulate;
     c.offset = a.offset; c.scale = a.scale; c.gate = a.gate; c.w_post = a.w_post;
     c.dw_next = a.dw_next; c.dw_post = a.dw_post; c.dgate = channel ? a.dgate : nullptr;
-    const dim3 grid((unsigned)((a.d + 31) / 32), a.y ? 2 : 1);
+    const dim3 grid((unsigned)((a.d + 31) / 32), a.y ? 2 : 1), block(32 * (groups >= 256 ? 32 : (groups + 7) / 8));
     *launches = 2;
-    if (!a.bf16) return launch_pdl(column_sums_kernel<float, float>, grid, dim3(256), 0, st, c);
-    return a.grads_f32 ? launch_pdl(column_sums_kernel<__nv_bfloat16, float>, grid, dim3(256), 0, st, c)
-                       : launch_pdl(column_sums_kernel<__nv_bfloat16, __nv_bfloat16>, grid, dim3(256), 0, st, c);
+    if (!a.bf16) return launch_pdl(column_sums_kernel<float, float>, grid, block, 0, st, c);
+    return a.grads_f32 ? launch_pdl(column_sums_kernel<__nv_bfloat16, float>, grid, block, 0, st, c)
+                       : launch_pdl(column_sums_kernel<__nv_bfloat16, __nv_bfloat16>, grid, block, 0, st, c);
 }
 
 }  // namespace moe
