@@ -142,6 +142,131 @@ __global__ void __launch_bounds__(kMaxGroup) block_out_kernel(const BlockOutPara
     grid_dep_launch();
 }
 
+// The same for long batches, rows coming through shared memory and the factors of
+// the columns waiting there in float32: w_post' times the gate of a channel, and
+// w_next'.
+enum { kInResidual, kInY, kInGate };
+
+template <typename W, typename Y, int C, bool FULL>
+__global__ void __launch_bounds__(768, 1)
+    block_out_ring_kernel(const __grid_constant__ BlockOutParams p, const __grid_constant__ RingParams rp) {
+    constexpr bool kY = !std::is_same_v<Y, None>;
+    constexpr int E = 16 / (int)sizeof(W), P = E / 2;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ __align__(16) float red[kMaxGroups][2][kMaxGroupWarps][4];
+    const int tid = threadIdx.x % p.group, grp = threadIdx.x / p.group;
+    Sums sums = {red[grp], p.group / 32, tid / 32, 1 + grp, p.group, 0};
+    const int groups = (int)gridDim.x * p.rows, first = (int)blockIdx.x * p.rows + grp;
+    float *f_next = reinterpret_cast<float*>(smem), *f_post = f_next + (p.next ? p.d : 0);
+    Ring ring(rp, smem, grp, p.T, first, groups);
+    if (tid == 0) ring.init();
+    fence_mbar_init();
+    grid_dep_wait();
+    __syncthreads();
+    if (tid == 0)
+        for (int s = 0; s < rp.stages; ++s) ring.issue();
+    for (int c = threadIdx.x; c < p.d; c += blockDim.x) {
+        if (p.next) put_factor<E>(f_next, p.n_vec, c, p.offset + (p.w_next ? to_f32(static_cast<const W*>(p.w_next)[c]) : 0.f));
+        if constexpr (kY) {
+            float w = p.post ? p.offset + (p.w_post ? to_f32(static_cast<const W*>(p.w_post)[c]) : 0.f) : 1.f;
+            if (p.gate_kind == MOE_GATE_CHANNEL) w *= to_f32(static_cast<const W*>(p.gate)[c]);
+            put_factor<E>(f_post, p.n_vec, c, w);
+        }
+    }
+    float gt1 = 1.f;  // a token's gate, fetched a row ahead
+    auto fetch = [&](int t) {
+        if (kY && p.gate_kind == MOE_GATE_TOKEN && t < p.T) gt1 = __ldg(static_cast<const float*>(p.gate) + t);
+    };
+    fetch(first);
+    __syncthreads();
+    int t = first;
+    for (; t < p.T; t += groups) {
+        const float gt = p.scale * gt1;
+        if (!ring.wait()) break;
+        fetch(t + groups);
+        Pair v[C][P];
+        Raw<W, E> gate[C];
+        Raw<Y, E> y[C];
+        auto each = [&](auto f) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (tid + c * p.group < p.n_vec) f(c, tid + c * p.group);
+        };
+        each([&](int c, int i) {
+            Raw<W, E> r;
+            r.load(ring.input(kInResidual), i);
+            if constexpr (kY) y[c].load(ring.input(kInY), i);
+            if constexpr (FULL) gate[c].load(ring.input(kInGate), i);
+#pragma unroll
+            for (int j = 0; j < P; ++j) v[c][j] = r.pair_of(j);
+        });
+        // the stage is free when every thread has brought its part of the row's first sum
+        bool held = true;
+        auto release = [&] {
+            if (held) {
+                if (p.group == 32) __syncwarp();
+                if (tid == 0) ring.issue();
+                ring.next();
+                held = false;
+            }
+        };
+        float a = 1.f;
+        if (kY && p.post) {
+            auto squares = [&](float k) {
+                Pair ss = 0;
+                each([&](int c, int) {
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        const Pair x = mul(y[c].pair_of(j), pair(k));
+                        ss = fma(x, x, ss);
+                    }
+                });
+                return both(ss);
+            };
+            a = rstd_of(sums, squares(1.f), p.d, p.eps, [&] { return squares(0x1p-80f); });
+            release();
+            if (tid == 0 && p.rstd_post) p.rstd_post[t] = a;
+        }
+        if constexpr (kY)
+            each([&](int c, int i) {
+                Pair w[P];
+                get_factors<E>(f_post, p.n_vec, i, w);
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    Pair b = mul(mul(y[c].pair_of(j), pair(a)), w[j]);
+                    if constexpr (FULL) b = mul(b, gate[c].pair_of(j));
+                    v[c][j] = fma(pair(gt), b, v[c][j]);
+                }
+                store<W, P>(p.out + t * p.ldo, i, v[c]);
+            });
+        if (p.next) {
+            auto squares = [&](float k) {
+                Pair ss = 0;
+                each([&](int c, int) {
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        const Pair x = mul(v[c][j], pair(k));
+                        ss = fma(x, x, ss);
+                    }
+                });
+                return both(ss);
+            };
+            const float b = rstd_of(sums, squares(1.f), p.d, p.eps, [&] { return squares(0x1p-80f); });
+            release();
+            if (tid == 0 && p.rstd_next) p.rstd_next[t] = b;
+            each([&](int c, int i) {
+                Pair w[P];
+                get_factors<E>(f_next, p.n_vec, i, w);
+#pragma unroll
+                for (int j = 0; j < P; ++j) v[c][j] = mul(mul(v[c][j], pair(b)), w[j]);
+                store<W, P>(p.next + t * p.ldn, i, v[c]);
+            });
+        }
+    }
+    if (tid == 0 && t < p.T) ring.drain(t);
+    grid_dep_launch();
+}
+
 template <typename W, typename Y, int E, int C>
 cudaError_t launch(BlockOutParams p, int sms, cudaStream_t st) {
     p.n_vec = p.d / E;
@@ -156,6 +281,33 @@ cudaError_t launch(BlockOutParams p, int sms, cudaStream_t st) {
 template <typename W, typename Y>
 cudaError_t launch_vectors(const BlockOutParams& p, int e, int sms, cudaStream_t st) {
     constexpr int kWide = 16 / (int)sizeof(W);
+    constexpr bool kY = !std::is_same_v<Y, None>;
+    if (e == kWide && (p.post || p.next)) {  // without a norm there is no sum to wait for: registers give 5.1 TB/s
+        constexpr int C = 16 / kWide;  // 16 values a thread
+        BlockOutParams q = p;
+        q.n_vec = p.d / e;
+        RingParams r = {};
+        const uint32_t row = (uint32_t)p.d * (uint32_t)sizeof(W);
+        auto input = [&](int i, const char* src, int64_t stride, uint32_t bytes) { r.src[i] = src; r.stride[i] = stride; r.bytes[i] = bytes; };
+        input(kInResidual, p.r, p.ldr, row);
+        if constexpr (kY) input(kInY, p.y, p.ldy, (uint32_t)p.d * (uint32_t)sizeof(Y));
+        if (kY && p.gate_kind == MOE_GATE_FULL) input(kInGate, static_cast<const char*>(p.gate), row, row);
+        RingShape s;
+        const uint32_t weights = ((p.next ? 1u : 0u) + (kY ? 1u : 0u)) * (uint32_t)p.d * 4;
+        // Rows of 64 vectors or fewer leave the ring's threads too few (d 256, 65536 tokens: 58 us against 30 in
+        // registers; d 512 37 against 34; d 1024 29 against 34), and so does a norm alone with one group (d 8192,
+        // 4096 tokens: 41 against 36; with a branch 74 against 88).
+        if (q.n_vec > 64 && q.n_vec <= kMaxGroup * C && ring_shape(r, p.T, q.n_vec, C, 768, kMaxGroups, weights, sms, s) &&
+            (kY || s.groups > 1)) {
+            q.group = s.group; q.rows = s.groups;
+            auto kern = block_out_ring_kernel<W, Y, C, false>;
+            if constexpr (kY)
+                if (p.gate_kind == MOE_GATE_FULL) kern = block_out_ring_kernel<W, Y, C, true>;
+            const cudaError_t err = allow_max_smem(kern);
+            if (err != cudaSuccess) return err;
+            return launch_pdl(kern, dim3((unsigned)s.blocks), dim3(s.group * s.groups), s.smem, st, q, r);
+        }
+    }
     return with_chunks<kWide>(p.d, e, [&](auto E, auto C) { return launch<W, Y, E, C>(p, sms, st); });
 }
 

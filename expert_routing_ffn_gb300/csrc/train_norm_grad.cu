@@ -161,9 +161,11 @@ __global__ void __launch_bounds__(kMaxGroup) block_grad_kernel(const BlockGradPa
 // channel.  A row's values pass through registers once; of what the sums need,
 // D without its projection (t), out and y stay.
 enum { kInDout, kInDnext, kInOut, kInY, kInGate };
+// threads of a block, by the registers that 16 values of every input take
+__host__ __device__ constexpr int ring_threads(bool branch, bool full) { return full ? 384 : branch ? 512 : 768; }
 
 template <typename W, typename Y, int C, bool FULL>
-__global__ void __launch_bounds__(std::is_same_v<Y, None> ? 768 : 512, 1)
+__global__ void __launch_bounds__(ring_threads(!std::is_same_v<Y, None>, FULL), 1)
     block_grad_ring_kernel(const __grid_constant__ BlockGradParams p, const __grid_constant__ RingParams rp) {
     constexpr bool kY = !std::is_same_v<Y, None>;
     constexpr int E = 16 / (int)sizeof(W), P = E / 2, kSums = kY ? 2 : 1;  // sums of a column
@@ -406,7 +408,7 @@ cudaError_t launch_vectors(const BlockGradParams& p, int e, int parts, int sms, 
         const uint32_t weights = ((p.dnext ? 1u : 0u) + (kY ? 1u : 0u)) * (uint32_t)p.d * 4;
         // The sums of a group (two float32 a column with y, else one) fit where its ring was: at least two stages of
         // two rows or more of at least two bytes a value.
-        if (q.n_vec <= kMaxGroup * C && (!p.columns || parts >= sms) && ring_shape(r, p.T, q.n_vec, C, kY ? 512 : 768, kMaxGroups, weights, sms, s)) {
+        if (q.n_vec <= kMaxGroup * C && (!p.columns || parts >= sms) && ring_shape(r, p.T, q.n_vec, C, ring_threads(kY, p.gate_kind == MOE_GATE_FULL), kMaxGroups, weights, sms, s)) {
             q.group = s.group; q.rows = s.groups;
             auto kern = block_grad_ring_kernel<W, Y, C, false>;
             if constexpr (kY)
