@@ -108,6 +108,7 @@ struct NormGradArgs {
     float offset, scale;
     bool bf16, grads_f32, accumulate;
     float* part;                             // workspace: norm_parts x 2 x d
+    DevError* err;
     int sms;
 };
 cudaError_t launch_block_out_grad(const NormGradArgs& a, cudaStream_t st, int* launches);

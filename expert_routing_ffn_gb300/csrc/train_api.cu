@@ -153,7 +153,7 @@ moe_status zero_columns(const moe_dims* D, std::initializer_list<void*> sums, mo
 moe_status run_norm_grad(const moe_dims* D, NormGradArgs& a, moe_dtype gtype, int accumulate, void* ws, void* stream,
                          const char* what) {
     a.bf16 = D->wtype == MOE_DTYPE_BF16; a.grads_f32 = gtype == MOE_DTYPE_F32; a.accumulate = accumulate != 0;
-    a.part = ws_at<float>(ws, train_ws(*D).norm); a.sms = device_sms();
+    a.part = ws_at<float>(ws, train_ws(*D).norm); a.err = ws_at<DevError>(ws, 0); a.sms = device_sms();
     int launches = 0;
     const cudaError_t e = launch_block_out_grad(a, S(stream), &launches);
     if (e != cudaSuccess) return cuda_failed(e, what);

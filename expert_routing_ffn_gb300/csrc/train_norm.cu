@@ -179,10 +179,9 @@ __global__ void __launch_bounds__(768, 1)
     };
     fetch(first);
     __syncthreads();
-    int t = first;
-    for (; t < p.T; t += groups) {
-        const float gt = p.scale * gt1;
-        if (!ring.wait()) break;
+    for (int t = first; t < p.T; t += groups) {
+        const float lost = ring.wait();
+        const float gt = p.scale * gt1 + lost;
         fetch(t + groups);
         Pair v[C][P];
         Raw<W, E> gate[C];
@@ -221,7 +220,7 @@ __global__ void __launch_bounds__(768, 1)
                         ss = fma(x, x, ss);
                     }
                 });
-                return both(ss);
+                return both(ss) + lost;
             };
             a = rstd_of(sums, squares(1.f), p.d, p.eps, [&] { return squares(0x1p-80f); });
             release();
@@ -249,7 +248,7 @@ __global__ void __launch_bounds__(768, 1)
                         ss = fma(x, x, ss);
                     }
                 });
-                return both(ss);
+                return both(ss) + lost;
             };
             const float b = rstd_of(sums, squares(1.f), p.d, p.eps, [&] { return squares(0x1p-80f); });
             release();
@@ -263,7 +262,7 @@ __global__ void __launch_bounds__(768, 1)
             });
         }
     }
-    if (tid == 0 && t < p.T) ring.drain(t);
+    if (tid == 0) ring.drain();
     grid_dep_launch();
 }
 

@@ -166,11 +166,12 @@ struct Ring {
     int slot, issue_slot;
     uint32_t phase;
     int64_t ahead;  // the next row to fetch
+    bool dead;      // a wait gave up
 
     __device__ __forceinline__ Ring(const RingParams& p, char* smem, int group, int64_t T, int64_t first, int64_t step)
         : p(p), base(smem + p.rings + (size_t)group * p.stages * p.stage_bytes),
           full(reinterpret_cast<uint64_t*>(smem + p.barriers) + group * kMaxStages), T(T), first(first), step(step),
-          policy(l2_evict_first_policy()), slot(0), issue_slot(0), phase(0), ahead(first) {}
+          policy(l2_evict_first_policy()), slot(0), issue_slot(0), phase(0), ahead(first), dead(false) {}
     __device__ __forceinline__ void init() {
         for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
     }
@@ -186,18 +187,24 @@ struct Ring {
         ahead += step;
         if (++issue_slot == p.stages) issue_slot = 0;
     }
-    // the current row's stage has arrived (false: given up)
-    __device__ __forceinline__ bool wait() { return mbar_wait(&full[slot], phase); }
+    // The current row's stage has arrived: 0, or NaN where the wait gave up (mbar_wait's
+    // limit).  The row's results become NaN then; the group goes on, because its
+    // threads meet at barriers, and waits no more.
+    __device__ __forceinline__ float wait() {
+        if (!dead && mbar_wait(&full[slot], phase)) return 0.f;
+        dead = true;
+        return __int_as_float(0x7fc00000);
+    }
     __device__ __forceinline__ const char* input(int i) const { return base + (size_t)slot * p.stage_bytes + p.at[i]; }
     __device__ __forceinline__ void next() {
         if (++slot == p.stages) { slot = 0; phase ^= 1; }
     }
-    // after a wait that gave up: nothing of this thread's copies may land once the block is gone
-    __device__ __forceinline__ void drain(int64_t t) {
-        for (int64_t r = t; r < ahead && r < T; r += step) {
-            (void)wait();
-            next();
-        }
+    // at the end, by the thread that issues: no copy may land once the block is gone
+    __device__ __forceinline__ void drain() {
+        if (!dead) return;
+        const int64_t rows = T > first ? (T - first + step - 1) / step : 0;
+        for (int64_t k = rows > p.stages ? rows - p.stages : 0; k < rows; ++k)
+            (void)mbar_wait(&full[k % p.stages], (uint32_t)(k / p.stages) & 1u);
     }
 };
 

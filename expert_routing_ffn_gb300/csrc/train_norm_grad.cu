@@ -30,6 +30,7 @@ struct BlockGradParams {
     int T, d, n_vec, post, group, rows, columns;     // columns: sums over the tokens are asked for
     float offset, scale, inv_d;
     float* part;                                     // [groups][2][d]
+    DevError* err;
 };
 
 // E values a vector; C > 0: a thread's C vectors of a row, and its columns' sums,
@@ -205,10 +206,8 @@ __global__ void __launch_bounds__(ring_threads(!std::is_same_v<Y, None>, FULL), 
     for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int j = 0; j < P; ++j) cn[c][j] = cp[c][j] = 0;
-    int t = first;
-    for (; t < p.T; t += groups) {
-        const float a = a1, b = b1, gt = gt1;
-        if (!ring.wait()) break;
+    for (int t = first; t < p.T; t += groups) {
+        const float lost = ring.wait(), a = a1, b = b1 + lost, gt = gt1 + lost;
         fetch(t + groups);
         Pair s0 = 0, s1 = 0, s2 = 0;
         Pair dt[C][P];  // dout + b dnext w_next'
@@ -310,7 +309,8 @@ __global__ void __launch_bounds__(ring_threads(!std::is_same_v<Y, None>, FULL), 
             }
         }
     }
-    if (tid == 0 && t < p.T) ring.drain(t);
+    if (tid == 0) ring.drain();
+    if (ring.dead) set_error(p.err, MOE_ERR_TIMEOUT, first);
     if (p.columns) {
         // the groups' sums meet in shared memory, where the rings were, and leave as one
         float* mine = reinterpret_cast<float*>(smem + rp.rings) + (size_t)grp * kSums * p.d;
@@ -439,6 +439,7 @@ cudaError_t launch_block_out_grad(const NormGradArgs& a, cudaStream_t st, int* l
     p.dgate = channel ? nullptr : a.dgate;
     p.T = a.T; p.d = a.d; p.post = a.post; p.offset = a.offset; p.scale = a.scale; p.part = a.part;
     p.inv_d = 1.f / (float)a.d;
+    p.err = a.err;
     p.columns = a.dw_post || a.dw_next || (channel && a.dgate);
     const int parts = norm_parts(a.T, a.d);
     int groups = 0;

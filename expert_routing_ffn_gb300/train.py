@@ -105,6 +105,14 @@ def _buf(dev, t, dtype, numel, name, optional=False):
 
 def _rows(dev, t, dtype, T, d, name, optional=False):
     """Address and row stride of token rows [T, d] (contiguous columns)."""
+    try:  # the common case first: a call's host time is its checks
+        if t.dtype is dtype and t.get_device() == dev:
+            rows, cols = t.shape
+            ld, inner = t.stride()
+            if cols == d and rows >= T and inner == 1 and ld >= d:
+                return t.data_ptr(), ld
+    except (AttributeError, ValueError):
+        pass
     if t is None and optional:
         return None, 0
     if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype:
@@ -420,6 +428,8 @@ def moe_pack_rows(x, q, scale, stream=None):
     """x [rows, cols] (bfloat16 or float32) to 8 bits: q int8, scale uint8 (packed_rows makes them)."""
     dev = _here()
     rows, cols, px, ldx, xtype = _plain_rows(dev, x, "x")
+    if getattr(scale, "shape", (0,))[-1] != (cols + 31) // 32:
+        raise ValueError(f"scale must be [rows, {(cols + 31) // 32}] for {cols} columns")
     pq, ps = _packed(dev, q, scale, rows, cols, "x")
     _check(lib().moe_pack_rows(rows, cols, px, ldx, xtype, pq, ps, _queue(dev, stream)), "moe_pack_rows")
 

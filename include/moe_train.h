@@ -172,7 +172,9 @@ moe_status moe_experts_down_grad(const moe_dims* dims, const void* dy_perm, cons
 /* ------------------------------------------------------------ the block around the layer
  * Norms are root mean square norms: rstd = (mean_j x_j^2 + eps)^-1/2 over a
  * row's d values, n_j = x_j rstd (weight_offset + w_j).  Squares whose sum
- * passes float32's range are summed again at a smaller scale. */
+ * passes float32's range are summed again at a smaller scale.  Long batches wait
+ * for their rows inside the kernel; a wait that gives up (about a second) makes
+ * the rows' results NaN and, in the gradients, MOE_ERR_TIMEOUT in the error word. */
 
 /* The factor on the block's output before it joins the residual. */
 typedef enum {
