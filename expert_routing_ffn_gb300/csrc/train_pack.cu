@@ -16,15 +16,18 @@ using namespace pack8;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32, kCols = 256;  // columns of a warp
 
-// A warp takes up to kPieces pieces of kCols columns of a row at a time, all
-// their loads before any use.
-constexpr int kPieces = 4;
+// A warp takes several pieces of kCols columns of a row at a time, all their loads
+// before any use; a row's pieces are split evenly.  Pack and gather of
+// 4096 tokens of 3584 values, 8 slots each, four pieces to pack: four to unpack 67
+// us, five 65, seven (half a row) 61, eight (with more registers, and seven taken)
+// 64; the gather's writes alone take 35 at the copy bandwidth.  HBM writes bound it.
+constexpr int kPackPieces = 4, kUnpackPieces = 7;
 
 struct PackParams {
     const void* x; int64_t ldx;  // elements
     int8_t* q; uint8_t* scale;
     int64_t rows;
-    int cols, nb, chunks;        // chunks of kPieces pieces in a row
+    int cols, nb, chunks, per;   // chunks of `per` pieces in a row
     const int32_t* index; int divisor;
     int64_t src_rows;
 };
@@ -46,7 +49,7 @@ __device__ __forceinline__ void each_chunk(const PackParams& p, F f) {
         c += dc;
         if (c >= p.chunks) { c -= p.chunks; ++r; }
         if (p.index && r < p.rows) index = p.index[r];
-        f(r0, c0 * kPieces * kCols, i);
+        f(r0, c0 * p.per * kCols, i);
     }
 }
 
@@ -55,12 +58,13 @@ __global__ void __launch_bounds__(kThreads) pack_rows_kernel(const PackParams p)
     const int lane = threadIdx.x & 31;
     grid_dep_wait();
     each_chunk(p, [&](int64_t r, int c0, int) {
-        float f[kPieces][8];
+        float f[kPackPieces][8];
 #pragma unroll
-        for (int u = 0; u < kPieces; ++u) load8<W, VEC>(static_cast<const W*>(p.x) + r * p.ldx, c0 + u * kCols + lane * 8, p.cols, f[u]);
+        for (int u = 0; u < kPackPieces; ++u)
+            load8<W, VEC>(static_cast<const W*>(p.x) + r * p.ldx, c0 + u * kCols + lane * 8, u < p.per ? p.cols : 0, f[u]);
 #pragma unroll
-        for (int u = 0; u < kPieces; ++u) {
-            if (c0 + u * kCols >= p.cols) break;  // the same for the warp
+        for (int u = 0; u < kPackPieces; ++u) {
+            if (u >= p.per || c0 + u * kCols >= p.cols) break;  // the same for the warp
             uint32_t m = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) m = max(m, magnitude(f[u][i]));
@@ -93,22 +97,22 @@ __global__ void __launch_bounds__(kThreads) unpack_rows_kernel(const PackParams 
     each_chunk(p, [&](int64_t r, int c0, int index) {
         const int64_t src = !p.index ? r : index < 0 ? -1 : index / p.divisor;
         const bool there = src >= 0 && src < p.src_rows;
-        uint2 w[kPieces];
-        uint32_t E[kPieces];
+        uint2 w[kUnpackPieces];
+        uint32_t E[kUnpackPieces];
 #pragma unroll
-        for (int u = 0; u < kPieces; ++u) {
+        for (int u = 0; u < kUnpackPieces; ++u) {
             const int block = (c0 + u * kCols) / 32 + lane / 4;
             w[u] = make_uint2(0, 0);
             E[u] = 0;
-            if (there && block < p.nb) {
+            if (there && u < p.per && block < p.nb) {
                 const int64_t at = src * p.nb + block;
                 w[u] = *reinterpret_cast<const uint2*>(p.q + at * 32 + (lane & 3) * 8);
                 E[u] = p.scale[at];
             }
         }
 #pragma unroll
-        for (int u = 0; u < kPieces; ++u) {
-            if (c0 + u * kCols >= p.cols) break;  // the same for the warp
+        for (int u = 0; u < kUnpackPieces; ++u) {
+            if (u >= p.per || c0 + u * kCols >= p.cols) break;  // the same for the warp
             const float s = step(E[u]);
             const uint2 v = to_columns(w[u]);
             const uint32_t lo = biased(v.x), hi = biased(v.y);
@@ -123,8 +127,10 @@ __global__ void __launch_bounds__(kThreads) unpack_rows_kernel(const PackParams 
 // ---------------------------------------------------------------- combine, gradient
 // A block takes a token at a time: dout's row, every slot's row of
 // y in 8 bits for dgate, eight slots' loads before any use and without a branch, and
-// its row of dy written.  Three blocks of eight warps an SM: 78 us for 4096 tokens of
-// 3584 values, 8 slots each; two 84, four (64 registers) 100.  A thread takes dout in two orders, by columns for dy and by the order
+// its row of dy written.  Bound: the latency of rows that lie apart, then HBM: 4096
+// tokens of 3584 values, 8 slots each: 77 us for 386 MB, 0.74 of the measured copy
+// bandwidth, with three blocks of eight warps an SM; two 84, four (64 registers) 100;
+// a branch a slot before its loads 171.  A thread takes dout in two orders, by columns for dy and by the order
 // of its two words for the products, so the words need no exchange.
 constexpr int kGradWarps = 8, kGradBlocks = 3;  // a block's warps at most; blocks an SM
 
@@ -232,6 +238,12 @@ bool vectors(const void* p, int64_t ld, int cols, bool bf16) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % n == 0 && cols % n == 0;
 }
 
+void set_chunks(PackParams& p, int most) {
+    const int pieces = (p.cols + kCols - 1) / kCols;
+    p.chunks = (pieces + most - 1) / most;
+    p.per = (pieces + p.chunks - 1) / p.chunks;
+}
+
 unsigned pack_grid(int64_t items, int sms) {
     const int64_t blocks = (items + kWarps - 1) / kWarps, most = (int64_t)sms * 8;
     return (unsigned)(blocks < most ? blocks : most);
@@ -243,7 +255,7 @@ cudaError_t launch_pack_rows(int64_t rows, int cols, const void* x, int64_t ldx,
                              int sms, cudaStream_t st) {
     PackParams p = {};
     p.x = x; p.ldx = ldx; p.q = q; p.scale = scale; p.rows = rows; p.cols = cols; p.nb = pack_blocks(cols);
-    p.chunks = (cols + kCols * kPieces - 1) / (kCols * kPieces);
+    set_chunks(p, kPackPieces);
     const dim3 grid(pack_grid(rows * p.chunks, sms)), block(kThreads);
     const bool vec = vectors(x, ldx, cols, bf16);
     if (bf16)
@@ -257,7 +269,8 @@ cudaError_t launch_unpack_rows(int64_t src_rows, int cols, const int8_t* q, cons
                                int divisor, int64_t rows, void* out, int64_t ldo, bool bf16, int sms, cudaStream_t st) {
     PackParams p = {};
     p.x = out; p.ldx = ldo; p.q = const_cast<int8_t*>(q); p.scale = const_cast<uint8_t*>(scale); p.rows = rows;
-    p.cols = cols; p.nb = pack_blocks(cols); p.chunks = (cols + kCols * kPieces - 1) / (kCols * kPieces);
+    p.cols = cols; p.nb = pack_blocks(cols);
+    set_chunks(p, kUnpackPieces);
     p.index = index; p.divisor = divisor; p.src_rows = src_rows;
     const dim3 grid(pack_grid(rows * p.chunks, sms)), block(kThreads);
     const bool vec = vectors(out, ldo, cols, bf16);

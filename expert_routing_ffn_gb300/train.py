@@ -68,6 +68,7 @@ MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_CHANNEL, MOE_GATE_FULL = range(4)
 
 _F32, _I32, _U8, _I8 = torch.float32, torch.int32, torch.uint8, torch.int8
 _WTYPE = {MOE_DTYPE_F32: torch.float32, MOE_DTYPE_BF16: torch.bfloat16}
+_CODE = {t: c for c, t in _WTYPE.items()}
 
 
 def _here():
@@ -294,7 +295,7 @@ def _branch_type(dims, t, name):
     if t is None:
         return _WTYPE[dims.wtype]
     dtype = getattr(t, "dtype", None)
-    if dtype not in (_F32, _WTYPE[dims.wtype]):
+    if dtype is not _F32 and dtype is not _WTYPE[dims.wtype]:
         raise TypeError(f"{name} has dtype {dtype}, expected {_WTYPE[dims.wtype]} or {_F32}")
     return dtype
 
@@ -368,11 +369,12 @@ def moe_block_out_grad(dims, block, dout, dnext, y, out, gate, w_post, w_next, r
     T, d, wt = dims.T, dims.d, _WTYPE[dims.wtype]
     yt = _branch_type(dims, dy if y is None else y, "dy" if y is None else "y")
     branch = dy is not None or dgate is not None or dw_post is not None
-    sums = [(t, n) for t, n in ((dw_post, "dw_post"), (dw_next, "dw_next"),
-                                (dgate if block.gate == MOE_GATE_CHANNEL else None, "dgate")) if t is not None]
-    gdtype = sums[0][0].dtype if sums else wt
-    if gdtype not in (_F32, wt):
-        raise TypeError(f"{sums[0][1]} has dtype {gdtype}, expected {wt} or {_F32}")
+    # the sums over the tokens share the first one's type
+    first, name = (dw_post, "dw_post") if dw_post is not None else (dw_next, "dw_next") if dw_next is not None else \
+        (dgate if block.gate == MOE_GATE_CHANNEL else None, "dgate")
+    gdtype = wt if first is None else getattr(first, "dtype", None)
+    if gdtype is not _F32 and gdtype is not wt:
+        raise TypeError(f"{name} has dtype {gdtype}, expected {wt} or {_F32}")
     pdo, lddo = _rows(dev, dout, wt, T, d, "dout", dnext is not None)
     pdn, lddn = _rows(dev, dnext, wt, T, d, "dnext", True)
     py, ldy = _rows(dev, y, yt, T, d, "y", not branch)
@@ -415,6 +417,14 @@ def _packed(dev, q, scale, rows, cols, name, optional=False):
 
 def _plain_rows(dev, t, name):
     """rows, cols, address, row stride and type code of a tensor [rows, cols]."""
+    try:
+        code = _CODE[t.dtype]
+        rows, cols = t.shape
+        ld, inner = t.stride()
+        if inner == 1 and ld >= cols and t.get_device() == dev:
+            return rows, cols, t.data_ptr(), ld, code
+    except (AttributeError, KeyError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise TypeError(f"{name} must be a tensor [rows, cols]")
     if t.dtype not in (torch.float32, torch.bfloat16):

@@ -84,6 +84,16 @@ def test_values_where_the_format_turns(kind):
     assert np.array_equal(host(out), ref.unpack(rq, rE, 70), equal_nan=True)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_what_was_restored_packs_to_the_same_bytes(kind):
+    x = torch.from_numpy(np.random.default_rng(3).standard_normal((300, 500)).astype(np.float32)).to(TYPES[kind]).cuda()
+    (q, e), (q2, e2) = buffers(300, 500), buffers(300, 500)
+    moe.moe_pack_rows(x, q, e)
+    moe.moe_unpack_rows(q, e, None, 1, x)
+    moe.moe_pack_rows(x, q2, e2)
+    assert torch.equal(q, q2) and torch.equal(e, e2)
+
+
 def test_gather_with_indices_that_name_no_row():
     rng = np.random.default_rng(2)
     x, xh = rnd(rng, (6, 100), "bf16")
