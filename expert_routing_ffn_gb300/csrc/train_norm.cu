@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kMaxGroup) block_out_kernel(const BlockOutPara
         if (kY && p.gate_kind == MOE_GATE_CHANNEL) gate[c].load(p.gate, i);
     };
     grid_dep_wait();
+    grid_dep_launch();
     if (C > 0) each(load_weights);
     for (int64_t t = (int64_t)blockIdx.x * p.rows + g; t < p.T; t += (int64_t)gridDim.x * p.rows) {
         auto load_row = [&](int c, int i) {
@@ -148,7 +149,6 @@ __global__ void __launch_bounds__(kMaxGroup) block_out_kernel(const BlockOutPara
                 }
             });
     }
-    grid_dep_launch();
 }
 
 // The same for long batches, rows coming through shared memory and the factors of
@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(768, 1)
     if (tid == 0) ring.init();
     fence_mbar_init();
     grid_dep_wait();
+    grid_dep_launch();
     __syncthreads();
     if (tid == 0)
         for (int s = 0; s < rp.stages; ++s) ring.issue();
@@ -272,7 +273,6 @@ __global__ void __launch_bounds__(768, 1)
         }
     }
     if (tid == 0) ring.drain();
-    grid_dep_launch();
 }
 
 template <typename W, typename Y, int E, int C>

@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kMaxGroup) block_grad_kernel(const BlockGradPa
         if (kY && p.gate_kind == MOE_GATE_CHANNEL) gate[c].load(p.gate, i);
     };
     grid_dep_wait();
+    grid_dep_launch();
     if (C > 0) each(load_weights);
     const int64_t groups = (int64_t)gridDim.x * p.rows, first = (int64_t)blockIdx.x * p.rows + grp;
     float *col_next = p.part + first * 2 * p.d, *col_post = col_next + p.d;
@@ -162,7 +163,6 @@ __global__ void __launch_bounds__(kMaxGroup) block_grad_kernel(const BlockGradPa
             store<float, E>(col_next, i, cn[c]);
             if constexpr (kY) store<float, E>(col_post, i, cp[c]);
         });
-    grid_dep_launch();
 }
 
 // The same for long batches, rows coming through shared memory.  The factors of
@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(ring_threads(!std::is_same_v<Y, None>, FULL), 
     if (tid == 0) ring.init();
     fence_mbar_init();
     grid_dep_wait();
+    grid_dep_launch();
     __syncthreads();
     if (tid == 0)
         for (int s = 0; s < rp.stages; ++s) ring.issue();
@@ -340,7 +341,6 @@ __global__ void __launch_bounds__(ring_threads(!std::is_same_v<Y, None>, FULL), 
             p.part[(int64_t)blockIdx.x * 2 * p.d + c] = v;
         }
     }
-    grid_dep_launch();
 }
 
 // The groups' sums of 32 columns, added by the block's warps, each in the groups'
@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const ColumnParams p)
     __shared__ float red[32][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, col = blockIdx.x * 32 + lane, which = blockIdx.y;
     grid_dep_wait();
+    grid_dep_launch();
     float s = 0.f;
     if (col < p.d && (which || p.dw_next))
 #pragma unroll 8
@@ -381,7 +382,6 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const ColumnParams p)
             if (p.dgate) put(p.dgate, p.post ? s * (p.offset + (p.w_post ? to_f32(static_cast<const W*>(p.w_post)[col]) : 0.f)) : s);
         }
     }
-    grid_dep_launch();
 }
 
 template <typename W, typename Y, int E, int C>

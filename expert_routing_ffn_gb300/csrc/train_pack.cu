@@ -57,6 +57,7 @@ template <typename W, bool VEC>
 __global__ void __launch_bounds__(kThreads) pack_rows_kernel(const PackParams p) {
     const int lane = threadIdx.x & 31;
     grid_dep_wait();
+    grid_dep_launch();
     each_chunk(p, [&](int64_t r, int c0, int) {
         float f[kPackPieces][8];
 #pragma unroll
@@ -87,13 +88,13 @@ __global__ void __launch_bounds__(kThreads) pack_rows_kernel(const PackParams p)
             }
         }
     });
-    grid_dep_launch();
 }
 
 template <typename W, bool VEC>
 __global__ void __launch_bounds__(kThreads) unpack_rows_kernel(const PackParams p) {
     const int lane = threadIdx.x & 31;
     grid_dep_wait();
+    grid_dep_launch();
     each_chunk(p, [&](int64_t r, int c0, int index) {
         const int64_t src = !p.index ? r : index < 0 ? -1 : index / p.divisor;
         const bool there = src >= 0 && src < p.src_rows;
@@ -121,7 +122,6 @@ __global__ void __launch_bounds__(kThreads) unpack_rows_kernel(const PackParams 
             store8<W, VEC>(static_cast<W*>(const_cast<void*>(p.x)) + r * p.ldx, c0 + u * kCols + lane * 8, p.cols, f);
         }
     });
-    grid_dep_launch();
 }
 
 // ---------------------------------------------------------------- combine, gradient
@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kGradWarps * 32, kGradBlocks) combine_grad_pac
         }
     };
     grid_dep_wait();
+    grid_dep_launch();
     fetch(blockIdx.x);
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
         if (tid < KB) {
@@ -229,7 +230,6 @@ __global__ void __launch_bounds__(kGradWarps * 32, kGradBlocks) combine_grad_pac
             p.dgate[t * p.k + tid] = row_s[tid] >= 0 ? v : 0.f;
         }
     }
-    grid_dep_launch();
 }
 
 // rows that start on 16 bytes and hold whole vectors of them
