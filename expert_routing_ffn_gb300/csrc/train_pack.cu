@@ -125,13 +125,16 @@ __global__ void __launch_bounds__(kThreads) unpack_rows_kernel(const PackParams 
 }
 
 // ---------------------------------------------------------------- combine, gradient
-// A block takes a token at a time: dout's row, every slot's row of
-// y in 8 bits for dgate, eight slots' loads before any use and without a branch, and
-// its row of dy written.  Bound: the latency of rows that lie apart, then HBM: 4096
-// tokens of 3584 values, 8 slots each: 77 us for 386 MB, 0.74 of the measured copy
-// bandwidth, with three blocks of eight warps an SM; two 84, four (64 registers) 100;
-// a branch a slot before its loads 171.  A thread takes dout in two orders, by columns for dy and by the order
-// of its two words for the products, so the words need no exchange.
+// A block takes a token at a time: dout's row, every slot's row of y in 8 bits for
+// dgate, and its row of dy written.  A thread takes dout in two orders, by columns
+// for dy and by the order of its two words for the products, so the words need no
+// exchange.  Everything is fetched ahead: a token's rows and gates two tokens, dout
+// one, the words of eight slots one piece of 256 columns.
+// Bound: HBM, two thirds of it writes: 4096 tokens of 3584 values, 8 slots each: 71 us
+// for 386 MB, 0.81 of the measured copy bandwidth, with three blocks of eight warps
+// an SM.  Without the words ahead 78, with dout from global memory 76; two blocks 87,
+// four (64 registers) 100; a branch a slot before its loads 171.  Two tokens a block
+// (1001 of 1536 values, Granite shape) take 11.3 us, 11.9 with dout from global memory.
 constexpr int kGradWarps = 8, kGradBlocks = 3;  // a block's warps at most; blocks an SM
 
 struct GradParams {
@@ -140,70 +143,108 @@ struct GradParams {
     int T, k, n_rows, d, nb;
 };
 
-template <typename W, bool VEC, int KB>
+// Eight slots' words of one piece, and their scales: lane l holds those of slot l / 4,
+// blocks 2 (l % 4) and the next.
+struct SlotWords {
+    uint2 w[8];
+    uint32_t scales;
+};
+__device__ __forceinline__ void load_slots(const GradParams& p, const int* rows, int c0, SlotWords& o) {
+    const int lane = threadIdx.x & 31, block = min(c0 / 32 + lane / 4, p.nb - 1);  // past the last block dout has zeros
+#pragma unroll
+    for (int s = 0; s < 8; ++s)  // a slot without a row reads row 0, and its sum is not used
+        o.w[s] = *reinterpret_cast<const uint2*>(p.q + ((int64_t)max(rows[s], 0) * p.nb + block) * 32 + (lane & 3) * 8);
+    const uint8_t* e = p.scale + (int64_t)max(rows[lane >> 2], 0) * p.nb;
+    const int b = c0 / 32 + (lane & 3) * 2;
+    o.scales = e[min(b, p.nb - 1)] | (uint32_t)e[min(b + 1, p.nb - 1)] << 8;
+}
+
+// STAGED (with VEC): dout comes a token ahead by asynchronous copies to shared memory
+template <typename W, bool VEC, bool STAGED, int KB>
 __global__ void __launch_bounds__(kGradWarps * 32, kGradBlocks) combine_grad_packed_kernel(const GradParams p) {
+    extern __shared__ __align__(16) unsigned char dout_s[];  // STAGED: [2][d]
     __shared__ float part[kGradWarps][KB];
-    __shared__ int row_s[KB];
-    __shared__ float gate_s[KB];
+    __shared__ int row_s[2][KB];  // this token's rows and the next one's
+    __shared__ float gate_s[2][KB];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     int next_row = -1;
     float next_gate = 1.f;
-    auto fetch = [&](int64_t t) {  // a token's rows and gates, ahead of their use
+    auto fetch = [&](int64_t t) {  // a token's rows and gates, two tokens ahead of their use
         if (tid < p.k && t < p.T) {
             const int r = p.inv[t * p.k + tid];
             next_row = r >= p.n_rows || r < -1 - p.n_rows ? -1 : r;  // out of range: no row
             if (p.gate) next_gate = p.gate[t * p.k + tid];
         }
     };
+    auto keep = [&](int buf) {
+        if (tid < KB) {
+            row_s[buf][tid] = next_row;
+            gate_s[buf][tid] = next_gate;
+        }
+    };
+    auto fetch_dout = [&](int64_t t, int to) {
+        if (STAGED && t < p.T) {
+            const char* src = reinterpret_cast<const char*>(static_cast<const W*>(p.dout) + t * p.lddout);
+            const int bytes = p.d * (int)sizeof(W);
+            const uint32_t dst = smem_u32(dout_s) + to * bytes;
+            for (int i = tid * 16; i < bytes; i += blockDim.x * 16)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i), "l"(src + i) : "memory");
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    };
     grid_dep_wait();
     grid_dep_launch();
     fetch(blockIdx.x);
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-        if (tid < KB) {
-            row_s[tid] = next_row;
-            gate_s[tid] = next_gate;
-        }
+    fetch_dout(blockIdx.x, 0);
+    keep(0);
+    fetch(blockIdx.x + gridDim.x);
+    __syncthreads();
+    SlotWords ahead;  // of the next piece, eight slots at a time
+    if (p.dgate) load_slots(p, row_s[0], warp * kCols, ahead);
+    int buf = 0;
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, buf ^= 1) {
+        keep(buf ^ 1);
+        if (STAGED) asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-        fetch(t + gridDim.x);
-        const W* dout = static_cast<const W*>(p.dout) + t * p.lddout;
+        fetch(t + 2 * gridDim.x);
+        fetch_dout(t + gridDim.x, buf ^ 1);
+        const W* dout = STAGED ? reinterpret_cast<const W*>(dout_s) + buf * p.d : static_cast<const W*>(p.dout) + t * p.lddout;
+        const int* rows = row_s[buf];
         float dot[KB];
 #pragma unroll
         for (int s = 0; s < KB; ++s) dot[s] = 0.f;
         for (int c0 = warp * kCols; c0 < p.d; c0 += warps * kCols) {
-            const int c = c0 + lane * 8, block = min(c / 32, p.nb - 1);  // past the last block dout has zeros
+            const int c = c0 + lane * 8;
             float g[8], h[8];
             load8<W, VEC>(dout, c, p.d, g);
-            load_interleaved<W, VEC>(dout, c, p.d, h);
             if (p.dgate) {
+                load_interleaved<W, VEC>(dout, c, p.d, h);
 #pragma unroll
                 for (int s0 = 0; s0 < KB; s0 += 8) {
-                    uint2 w[8];
-                    uint32_t E[8];
-#pragma unroll
-                    for (int s = 0; s < 8; ++s) {  // a slot without a row reads row 0, and its sum is not used
-                        const int64_t at = (int64_t)max(row_s[s0 + s], 0) * p.nb + block;
-                        w[s] = *reinterpret_cast<const uint2*>(p.q + at * 32 + (lane & 3) * 8);
-                        E[s] = p.scale[at];
-                    }
+                    const SlotWords now = ahead;
+                    if (s0 + 8 < KB) load_slots(p, rows + s0 + 8, c0, ahead);
+                    else if (c0 + warps * kCols < p.d) load_slots(p, rows, c0 + warps * kCols, ahead);
+                    else if (t + gridDim.x < p.T) load_slots(p, row_s[buf ^ 1], warp * kCols, ahead);
 #pragma unroll
                     for (int s = 0; s < 8; ++s) {
-                        const uint32_t lo = biased(w[s].x), hi = biased(w[s].y);
+                        const uint32_t lo = biased(now.w[s].x), hi = biased(now.w[s].y);
+                        const uint32_t E = __shfl_sync(0xffffffffu, now.scales, s * 4 + lane / 8) >> (lane & 4 ? 8 : 0) & 0xffu;
                         Pair v = mul(pair(h[0], h[1]), add(pair(raw<0>(lo), raw<0>(hi)), pair(-kRaw)));
                         v = fma(pair(h[2], h[3]), add(pair(raw<1>(lo), raw<1>(hi)), pair(-kRaw)), v);
                         v = fma(pair(h[4], h[5]), add(pair(raw<2>(lo), raw<2>(hi)), pair(-kRaw)), v);
                         v = fma(pair(h[6], h[7]), add(pair(raw<3>(lo), raw<3>(hi)), pair(-kRaw)), v);
-                        dot[s0 + s] = fmaf(both(v), step(E[s]), dot[s0 + s]);
+                        dot[s0 + s] = fmaf(both(v), step(E), dot[s0 + s]);
                     }
                 }
             }
             if (p.dy) {
 #pragma unroll
                 for (int s = 0; s < KB; ++s) {
-                    const int row = row_s[s];
+                    const int row = rows[s];
                     if (row == -1) continue;
                     float f[8] = {};
                     if (row >= 0) {
-                        const Pair a = pair(gate_s[s]);
+                        const Pair a = pair(gate_s[buf][s]);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float2 v = halves(mul(pair(g[2 * i], g[2 * i + 1]), a));
@@ -227,7 +268,7 @@ __global__ void __launch_bounds__(kGradWarps * 32, kGradBlocks) combine_grad_pac
 #pragma unroll
             for (int w = 0; w < kGradWarps; ++w)
                 if (w < warps) v += part[w][tid];
-            p.dgate[t * p.k + tid] = row_s[tid] >= 0 ? v : 0.f;
+            p.dgate[t * p.k + tid] = rows[tid] >= 0 ? v : 0.f;
         }
     }
 }
@@ -281,16 +322,17 @@ cudaError_t launch_unpack_rows(int64_t src_rows, int cols, const int8_t* q, cons
                : launch_pdl(unpack_rows_kernel<float, false>, grid, block, 0, st, p);
 }
 
-template <typename W, bool VEC>
+template <typename W, bool VEC, bool STAGED>
 static cudaError_t launch_grad(const GradParams& p, int sms, cudaStream_t st) {
     // as many warps as share a row's pieces evenly
     const int pieces = (p.d + kCols - 1) / kCols, turns = (pieces + kGradWarps - 1) / kGradWarps;
     const int warps = (pieces + turns - 1) / turns;
     const dim3 block(32 * warps);
+    const size_t smem = STAGED ? 2 * (size_t)p.d * sizeof(W) : 0;
     int most = sms * (kGradWarps * kGradBlocks / warps);
     if (most > p.T) most = p.T;
-    return p.k <= 8 ? launch_pdl(combine_grad_packed_kernel<W, VEC, 8>, dim3(most), block, 0, st, p)
-                    : launch_pdl(combine_grad_packed_kernel<W, VEC, 16>, dim3(most), block, 0, st, p);
+    return p.k <= 8 ? launch_pdl(combine_grad_packed_kernel<W, VEC, STAGED, 8>, dim3(most), block, smem, st, p)
+                    : launch_pdl(combine_grad_packed_kernel<W, VEC, STAGED, 16>, dim3(most), block, smem, st, p);
 }
 
 cudaError_t launch_combine_rows_grad_packed(const CombineRowsGradPackedArgs& a, cudaStream_t st) {
@@ -298,8 +340,15 @@ cudaError_t launch_combine_rows_grad_packed(const CombineRowsGradPackedArgs& a, 
     p.dout = a.dout; p.lddout = a.lddout; p.q = a.q; p.scale = a.scale; p.gate = a.gate; p.inv = a.inv;
     p.dy = a.dy; p.dgate = a.dgate; p.T = a.T; p.k = a.k; p.n_rows = a.T * a.k; p.d = a.d; p.nb = pack_blocks(a.d);
     const bool vec = vectors(a.dout, a.lddout, a.d, a.bf16) && (!a.dy || vectors(a.dy, a.d, a.d, a.bf16));
-    if (a.bf16) return vec ? launch_grad<__nv_bfloat16, true>(p, a.sms, st) : launch_grad<__nv_bfloat16, false>(p, a.sms, st);
-    return vec ? launch_grad<float, true>(p, a.sms, st) : launch_grad<float, false>(p, a.sms, st);
+    // two of dout's rows within the 48 KB that a block has without asking for more
+    const bool staged = vec && 2LL * a.d * (a.bf16 ? 2 : 4) <= 40960;
+    if (a.bf16)
+        return staged ? launch_grad<__nv_bfloat16, true, true>(p, a.sms, st)
+             : vec    ? launch_grad<__nv_bfloat16, true, false>(p, a.sms, st)
+                      : launch_grad<__nv_bfloat16, false, false>(p, a.sms, st);
+    return staged ? launch_grad<float, true, true>(p, a.sms, st)
+         : vec    ? launch_grad<float, true, false>(p, a.sms, st)
+                  : launch_grad<float, false, false>(p, a.sms, st);
 }
 
 }  // namespace moe

@@ -131,7 +131,8 @@ def test_offsets_past_32_bits():
 
 COMBINE = [(1, 2048, 64, 6, "all", "bf16"), (1, 7, 3, 1, "none", "f32"), (33, 250, 40, 8, "some", "bf16"), (33, 251, 40, 8, "some", "f32"),
            (257, 1000, 40, 8, "skew", "f32"), (64, 40, 300, 16, "all", "f32"), (700, 33, 512, 16, "skew", "bf16"), (129, 3584, 64, 8, "all", "bf16"),
-           (40, 1024, 8, 2, "one", "bf16"), (12, 1032, 16, 9, "some", "bf16")]
+           (40, 1024, 8, 2, "one", "bf16"), (12, 1032, 16, 9, "some", "bf16"), (2000, 264, 8, 2, "some", "f32"),
+           (1900, 768, 40, 8, "some", "bf16"), (5, 12000, 8, 2, "all", "bf16")]
 
 
 @pytest.mark.parametrize("T,d,N,k,how,kind", COMBINE)
