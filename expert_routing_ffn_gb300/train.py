@@ -95,17 +95,20 @@ def _refuse(dev, t, dtype, numel, name):
 
 def _buf(dev, t, dtype, numel, name, optional=False):
     """Address of a contiguous tensor of at least numel elements on device dev (None -> None if optional)."""
+    if t is None and optional:
+        return None
     try:
         if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= numel:
             return t.data_ptr()
     except AttributeError:
-        if t is None and optional:
-            return None
+        pass
     _refuse(dev, t, dtype, numel, name)
 
 
 def _rows(dev, t, dtype, T, d, name, optional=False):
     """Address and row stride of token rows [T, d] (contiguous columns)."""
+    if t is None and optional:
+        return None, 0
     try:  # the common case first: a call's host time is its checks
         if t.dtype is dtype and t.get_device() == dev:
             rows, cols = t.shape
@@ -114,8 +117,6 @@ def _rows(dev, t, dtype, T, d, name, optional=False):
                 return t.data_ptr(), ld
     except (AttributeError, ValueError):
         pass
-    if t is None and optional:
-        return None, 0
     if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype:
         _refuse(dev, t, dtype, T * d, name)
     shape = t.shape
