@@ -229,11 +229,14 @@ __global__ void __launch_bounds__(kGradWarps * 32, kGradBlocks) combine_grad_pac
                     for (int s = 0; s < 8; ++s) {
                         const uint32_t lo = biased(now.w[s].x), hi = biased(now.w[s].y);
                         const uint32_t E = __shfl_sync(0xffffffffu, now.scales, s * 4 + lane / 8) >> (lane & 4 ? 8 : 0) & 0xffu;
-                        Pair v = mul(pair(h[0], h[1]), add(pair(raw<0>(lo), raw<0>(hi)), pair(-kRaw)));
-                        v = fma(pair(h[2], h[3]), add(pair(raw<1>(lo), raw<1>(hi)), pair(-kRaw)), v);
-                        v = fma(pair(h[4], h[5]), add(pair(raw<2>(lo), raw<2>(hi)), pair(-kRaw)), v);
-                        v = fma(pair(h[6], h[7]), add(pair(raw<3>(lo), raw<3>(hi)), pair(-kRaw)), v);
-                        dot[s0 + s] = fmaf(both(v), step(E), dot[s0 + s]);
+                        // y itself, exact, before dout: a product of dout with whole steps can pass the range where dout y does not
+                        const Pair f = pair(step(E));
+                        auto y = [&](float a, float b) { return mul(add(pair(a, b), pair(-kRaw)), f); };
+                        Pair v = mul(pair(h[0], h[1]), y(raw<0>(lo), raw<0>(hi)));
+                        v = fma(pair(h[2], h[3]), y(raw<1>(lo), raw<1>(hi)), v);
+                        v = fma(pair(h[4], h[5]), y(raw<2>(lo), raw<2>(hi)), v);
+                        v = fma(pair(h[6], h[7]), y(raw<3>(lo), raw<3>(hi)), v);
+                        dot[s0 + s] += both(v);
                     }
                 }
             }
