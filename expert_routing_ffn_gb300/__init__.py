@@ -163,6 +163,7 @@ _PROTOS = {
     "moe_testing_fail_copies_after": ([C.c_int], None),
     "moe_testing_wait_timeout": ([C.c_void_p, C.c_size_t, C.c_void_p], C.c_int),
     "moe_testing_set_tc_pairs": ([C.c_int], None),
+    "moe_testing_lose_row": ([C.c_int], None),
 }
 
 
@@ -630,6 +631,11 @@ def moe_testing_fail_copies_after(n: int):
 def moe_testing_set_tc_pairs(mode: int):
     """-1: the prefill FFN chooses single CTAs or CTA pairs; 0 / 1: force."""
     lib().moe_testing_set_tc_pairs(int(mode))
+
+
+def moe_testing_lose_row(row: int):
+    """>= 0: the norms of long batches never receive this row, and their wait for it runs out; -1: off."""
+    lib().moe_testing_lose_row(int(row))
 
 
 def moe_testing_wait_timeout(ws, stream=None):

@@ -86,6 +86,7 @@ struct NormArgs {
     int sms;
 };
 cudaError_t launch_block_out(const NormArgs& a, cudaStream_t st);
+int lost_row();  // moe_testing_lose_row's
 
 constexpr int kNormMaxParts = 2048;              // column sums of so many row groups
 constexpr size_t kNormPartBytes = 12u << 20;     // and in so much of the workspace

@@ -1,8 +1,10 @@
 // C ABI of the training step (include/moe_train.h): argument checks,
 // workspace layout and the launches of each call.
+#include <atomic>
 #include <cmath>
 #include <initializer_list>
 
+#include "../../include/moe_testing.h"
 #include "common.cuh"
 #include "train.h"
 
@@ -10,6 +12,8 @@ using namespace moe;
 
 namespace moe {
 void note_launches(int n);
+static std::atomic<int> g_lost_row{-1};
+int lost_row() { return g_lost_row.load(std::memory_order_relaxed); }
 }
 
 namespace {
@@ -565,6 +569,8 @@ moe_status moe_combine_rows_grad_packed(const moe_dims* dims, const void* dout, 
     note_launches(1);
     return MOE_OK;
 }
+
+void moe_testing_lose_row(int row) { g_lost_row.store(row < 0 ? -1 : row); }
 
 const char* moe_experts_path(const moe_dims* dims) {
     if (check_dims(dims) != MOE_OK) return "unsupported";

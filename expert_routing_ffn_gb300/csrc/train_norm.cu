@@ -211,10 +211,10 @@ __global__ void __launch_bounds__(768, 1)
         });
         // the stage is free when every thread has brought its part of the row's first sum
         bool held = true;
-        auto release = [&] {
+        auto release = [&](float rstd) {
             if (held) {
                 if (p.group == 32) __syncwarp();
-                if (tid == 0) ring.issue();
+                if (tid == 0) ring.issue(isnan(rstd));  // a thread that gave up made the sum NaN
                 ring.next();
                 held = false;
             }
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(768, 1)
                 return both(ss) + lost;
             };
             a = rstd_of(sums, squares(1.f), p.d, p.eps, [&] { return squares(0x1p-80f); });
-            release();
+            release(a);
             if (tid == 0 && p.rstd_post) p.rstd_post[t] = a;
         }
         if constexpr (kY)
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(768, 1)
                 return both(ss) + lost;
             };
             const float b = rstd_of(sums, squares(1.f), p.d, p.eps, [&] { return squares(0x1p-80f); });
-            release();
+            release(b);
             if (tid == 0 && p.rstd_next) p.rstd_next[t] = b;
             each([&](int c, int i) {
                 Pair w[P];

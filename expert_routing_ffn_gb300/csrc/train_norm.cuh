@@ -148,6 +148,14 @@ inline Shape shape_of(int n_vec, int chunks) {
 // each stage a row of every input, brought by bulk copies that the group's first
 // thread issues `stages` rows ahead.  A group reads its row into registers, and
 // the barrier of the row's first sum tells that thread that the stage is free.
+//
+// A wait that gives up (mbar_wait's limit) is the group's matter: the thread says so in
+// the group's word before that barrier, so behind it the issuing thread knows that
+// every thread has seen the row arrive, or fetches no more.  A stage is therefore
+// never filled while a copy into it may be on its way, and the copies in flight at
+// the end are the last one of each stage, which drain waits for.  The results of that
+// row and of the group's rows after it become NaN; the group goes on, because its
+// threads meet at barriers.
 constexpr int kMaxInputs = 5, kMaxStages = 8, kMaxGroups = 12;
 struct RingParams {
     const char* src[kMaxInputs];  // rows, NULL: not there
@@ -156,43 +164,46 @@ struct RingParams {
     uint32_t stage_bytes;
     int stages;
     uint32_t rings, barriers;     // offsets in shared memory (the weights come first)
+    int lost;                     // moe_testing_lose_row's row: more is announced than comes (-1: none)
 };
+constexpr int kBarriers = kMaxStages + 1;  // of a group, and its word that a wait gave up
 struct Ring {
     const RingParams& p;
     char* base;
     uint64_t* full;
-    int64_t T, first, step;
+    int T, first, step;
     uint64_t policy;
     int slot, issue_slot;
     uint32_t phase;
-    int64_t ahead;  // the next row to fetch
-    bool dead;      // a wait gave up
+    int ahead;      // the next row to fetch
+    bool dead;      // a wait of this thread gave up
 
-    __device__ __forceinline__ Ring(const RingParams& p, char* smem, int group, int64_t T, int64_t first, int64_t step)
+    __device__ __forceinline__ Ring(const RingParams& p, char* smem, int group, int T, int first, int step)
         : p(p), base(smem + p.rings + (size_t)group * p.stages * p.stage_bytes),
-          full(reinterpret_cast<uint64_t*>(smem + p.barriers) + group * kMaxStages), T(T), first(first), step(step),
+          full(reinterpret_cast<uint64_t*>(smem + p.barriers) + group * kBarriers), T(T), first(first), step(step),
           policy(l2_evict_first_policy()), slot(0), issue_slot(0), phase(0), ahead(first), dead(false) {}
+    __device__ __forceinline__ volatile int& gave_up() const { return *reinterpret_cast<volatile int*>(full + kMaxStages); }
     __device__ __forceinline__ void init() {
         for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
+        gave_up() = 0;
     }
-    // one row more, by one thread
-    __device__ __forceinline__ void issue() {
-        if (ahead < T) {
-            mbar_arrive_expect_tx(&full[issue_slot], p.stage_bytes);
-            char* dst = base + (size_t)issue_slot * p.stage_bytes;
+    // One row more, by one thread, behind the barrier of the first sum of the row that had the
+    // stage; none once a wait has given up (look: whether one may have).
+    __device__ __forceinline__ void issue(bool look = true) {
+        if (ahead >= T || (look && gave_up())) return;
+        mbar_arrive_expect_tx(&full[issue_slot], p.stage_bytes + (ahead == p.lost ? 16u : 0u));
+        char* dst = base + (size_t)issue_slot * p.stage_bytes;
 #pragma unroll
-            for (int i = 0; i < kMaxInputs; ++i)
-                if (p.src[i]) bulk_g2s(dst + p.at[i], p.src[i] + ahead * p.stride[i], p.bytes[i], &full[issue_slot], policy);
-        }
+        for (int i = 0; i < kMaxInputs; ++i)
+            if (p.src[i]) bulk_g2s(dst + p.at[i], p.src[i] + (int64_t)ahead * p.stride[i], p.bytes[i], &full[issue_slot], policy);
         ahead += step;
         if (++issue_slot == p.stages) issue_slot = 0;
     }
-    // The current row's stage has arrived: 0, or NaN where the wait gave up (mbar_wait's
-    // limit).  The row's results become NaN then; the group goes on, because its
-    // threads meet at barriers, and waits no more.
+    // The current row's stage has arrived: 0, or NaN where this thread gave up on it or on a row before.
     __device__ __forceinline__ float wait() {
         if (!dead && mbar_wait(&full[slot], phase)) return 0.f;
         dead = true;
+        gave_up() = 1;
         return __int_as_float(0x7fc00000);
     }
     __device__ __forceinline__ const char* input(int i) const { return base + (size_t)slot * p.stage_bytes + p.at[i]; }
@@ -201,10 +212,9 @@ struct Ring {
     }
     // at the end, by the thread that issues: no copy may land once the block is gone
     __device__ __forceinline__ void drain() {
-        if (!dead) return;
-        const int64_t rows = T > first ? (T - first + step - 1) / step : 0;
-        for (int64_t k = rows > p.stages ? rows - p.stages : 0; k < rows; ++k)
-            (void)mbar_wait(&full[k % p.stages], (uint32_t)(k / p.stages) & 1u);
+        if (!gave_up()) return;  // every thread has seen every row arrive
+        const int issued = (ahead - first) / step;
+        for (int s = 0; s < p.stages && s < issued; ++s) (void)mbar_wait(&full[s], (uint32_t)((issued - 1 - s) / p.stages) & 1u);
     }
 };
 
@@ -242,8 +252,9 @@ inline bool ring_shape(RingParams& r, int T, int n_vec, int chunks, int threads,
             r.at[i] = r.stage_bytes;
             r.stage_bytes += r.bytes[i];
         }
-    const uint32_t bars = kMaxGroups * kMaxStages * 8;
+    const uint32_t bars = kMaxGroups * kBarriers * 8;
     r.rings = (weights + 127) / 128 * 128;
+    r.lost = lost_row();
     if (most > kMaxGroups) most = kMaxGroups;
     if (most > threads / s.group) most = threads / s.group;
     for (s.groups = most; s.groups > 0; --s.groups) {

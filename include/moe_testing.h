@@ -32,6 +32,12 @@ moe_status moe_testing_wait_timeout(void* ws, size_t ws_bytes, void* stream);
  * the same inputs. */
 void moe_testing_set_tc_pairs(int mode);
 
+/* The block's norms and their gradients (moe_train.h) fetch the rows of long
+ * batches by asynchronous copies.  While row >= 0, 16 bytes more are announced of
+ * that row of each such call than are copied, so the wait for it runs out (about one
+ * second), as it would for a copy that got lost.  -1 (the default): off.  Process-wide. */
+void moe_testing_lose_row(int row);
+
 #ifdef __cplusplus
 }
 #endif

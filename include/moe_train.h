@@ -173,8 +173,10 @@ moe_status moe_experts_down_grad(const moe_dims* dims, const void* dy_perm, cons
  * Norms are root mean square norms: rstd = (mean_j x_j^2 + eps)^-1/2 over a
  * row's d values, n_j = x_j rstd (weight_offset + w_j).  Squares whose sum
  * passes float32's range are summed again at a smaller scale.  Long batches wait
- * for their rows inside the kernel; a wait that gives up (about a second) makes
- * the rows' results NaN and, in the gradients, MOE_ERR_TIMEOUT in the error word. */
+ * for their rows inside the kernel.  A wait that gives up (about a second) makes
+ * that row's results NaN, those of the rows that the same threads would have taken
+ * after it, and the sums over the tokens, and gives MOE_ERR_TIMEOUT in the error
+ * word of the gradients (moe_norm_rows and moe_block_out have none). */
 
 /* The factor on the block's output before it joins the residual. */
 typedef enum {
