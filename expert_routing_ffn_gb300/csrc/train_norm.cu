@@ -34,17 +34,19 @@ struct BlockOutParams {
     float eps, offset, scale;
 };
 
-// (sum x^2 / d + eps)^-1/2; `again` sums (x 2^-80)^2, for rows whose squares pass float32's range
+// (sum x^2 / d + eps)^-1/2; `again` sums (x 2^-80)^2, for rows whose squares pass float32's range,
+// beside eps at the same scale (zero unless eps is large)
 template <typename F>
 __device__ __forceinline__ float rstd_of(Sums& sums, float ss, int d, float eps, F again) {
     float s[1] = {ss};
     sums.sum(s);
-    if (!(s[0] < INFINITY)) {  // the same for every thread of the row; NaN stays NaN
+    const float m = s[0] / (float)d + eps;
+    if (!(m < INFINITY)) {  // the same for every thread of the row; NaN stays NaN
         s[0] = again();
         sums.sum(s);
-        return 0x1p-80f / sqrtf(s[0] / (float)d);
+        return 0x1p-80f / sqrtf(s[0] / (float)d + eps * 0x1p-80f * 0x1p-80f);
     }
-    return 1.f / sqrtf(s[0] / (float)d + eps);
+    return 1.f / sqrtf(m);
 }
 
 // E values a vector; C > 0: a thread's C vectors of a row stay in registers,

@@ -172,7 +172,8 @@ moe_status moe_experts_down_grad(const moe_dims* dims, const void* dy_perm, cons
 /* ------------------------------------------------------------ the block around the layer
  * Norms are root mean square norms: rstd = (mean_j x_j^2 + eps)^-1/2 over a
  * row's d values, n_j = x_j rstd (weight_offset + w_j).  Squares whose sum
- * passes float32's range are summed again at a smaller scale.  Long batches wait
+ * passes float32's range are summed again at a smaller scale; below it they are
+ * lost beside an eps that is a normal number.  Long batches wait
  * for their rows inside the kernel.  A wait that gives up (about a second) makes
  * that row's results NaN, those of the rows that the same threads would have taken
  * after it, and the sums over the tokens, and gives MOE_ERR_TIMEOUT in the error
