@@ -106,7 +106,8 @@ def _buf(dev, t, dtype, numel, name, optional=False):
 
 
 def _rows(dev, t, dtype, T, d, name, optional=False):
-    """Address and row stride of token rows [T, d] (contiguous columns)."""
+    """Address and row stride of token rows [T, d] (contiguous columns); a single row's stride says
+    nothing, and d keeps its loads wide."""
     if t is None and optional:
         return None, 0
     try:  # the common case first: a call's host time is its checks
@@ -114,7 +115,7 @@ def _rows(dev, t, dtype, T, d, name, optional=False):
             rows, cols = t.shape
             ld, inner = t.stride()
             if cols == d and rows >= T and inner == 1 and ld >= d:
-                return t.data_ptr(), ld
+                return t.data_ptr(), ld if T > 1 else d
     except (AttributeError, ValueError):
         pass
     if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype:
@@ -423,7 +424,7 @@ def _plain_rows(dev, t, name):
         rows, cols = t.shape
         ld, inner = t.stride()
         if inner == 1 and ld >= cols and t.get_device() == dev:
-            return rows, cols, t.data_ptr(), ld, code
+            return rows, cols, t.data_ptr(), ld if rows > 1 else cols, code
     except (AttributeError, KeyError, ValueError):
         pass
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
