@@ -51,19 +51,22 @@ class TrainLayer:
         # routing
         self.topk_idx, self.topk_gate, self.prob = buf(T, k, dtype=i32), buf(T, k, dtype=f32), buf(T, N, dtype=f32)
         self.delta_hat, self.prefetch_mask = buf(T, dtype=i32), buf(T, dtype=torch.int64)
-        # rows grouped by expert, kept for the gradient
+        # rows grouped by expert
         M = T * k
-        self.x_perm, self.y_perm = buf(M, d), buf(M, d)
-        self.g, self.u, self.h = buf(M, I), buf(M, I), buf(M, I)
+        self.x_perm, self.y_perm, self.h = buf(M, d), buf(M, d), buf(M, I)
         self.offsets, self.perm, self.inv = buf(N + 1, dtype=i32), buf(M, dtype=i32), buf(M, dtype=i32)
         self.out = buf(T, d)
         if packed:
-            # kept until the backward pass: x once a token, g, u and y once a slot; the 16-bit rows
-            # above can then serve every layer of a model in turn
+            # kept until the backward pass: x once a token, g, u and y once a slot.  Nothing above is, so
+            # the 16-bit rows could serve every layer of a model in turn, and here y's serve dx's
             self.x8, self.y8 = moe.packed_rows(T, d, device), moe.packed_rows(M, d, device)
             self.g8, self.u8 = moe.packed_rows(M, I, device), moe.packed_rows(M, I, device)
+            self.dx_perm = self.y_perm
+        else:  # kept: x_perm, y_perm, h and
+            self.g, self.u = buf(M, I), buf(M, I)
+            self.dx_perm = buf(M, d)
         # gradients; the weights' in float32, so that micro-batches may add up
-        self.dy_perm, self.dx_perm, self.dx = buf(M, d), buf(M, d), buf(T, d)
+        self.dy_perm, self.dx = buf(M, d), buf(T, d)
         self.dg, self.du = buf(M, I), buf(M, I)
         self.dgate, self.dlogits, self.loss = buf(T, k, dtype=f32), buf(T, N, dtype=f32), buf(1, dtype=f32)
         self.dw_gate, self.dw_up, self.dw_down = (torch.zeros((N, I, d), dtype=f32, device=device) for _ in range(3))
