@@ -18,20 +18,18 @@ constexpr int kMaxGroup = 512, kMaxGroupWarps = kMaxGroup / 32, kBlock = 256;
 
 struct None {};  // the type of a y that is not there
 
-// E consecutive values of type W, as they lie in memory
+// E consecutive values of type W, as they lie in memory: whole 16 bytes, or one value
 template <typename W, int E>
 struct Raw {
-    static constexpr int kBytes = E * (int)sizeof(W), kVec = kBytes < 16 ? kBytes : 16, kN = kBytes / kVec;
+    static constexpr int kBytes = E * (int)sizeof(W), kN = kBytes / 16;
+    static_assert(kBytes % 16 == 0 || E == 1, "");
     uint4 v[(kBytes + 15) / 16];
     __device__ __forceinline__ void load(const void* row, int i) {
         const char* p = static_cast<const char*>(row) + (int64_t)i * kBytes;
-        if constexpr (kVec == 16) {
+        if constexpr (kN > 0) {
 #pragma unroll
             for (int j = 0; j < kN; ++j) v[j] = reinterpret_cast<const uint4*>(p)[j];
-        } else if constexpr (kVec == 8) {
-            const uint2 t = *reinterpret_cast<const uint2*>(p);
-            v[0].x = t.x; v[0].y = t.y;
-        } else if constexpr (kVec == 4) v[0].x = *reinterpret_cast<const uint32_t*>(p);
+        } else if constexpr (kBytes == 4) v[0].x = *reinterpret_cast<const uint32_t*>(p);
         else v[0].x = *reinterpret_cast<const uint16_t*>(p);
     }
     __device__ __forceinline__ void zero() {
@@ -63,14 +61,14 @@ struct Raw<None, E> {
 template <typename W, int E>
 __device__ __forceinline__ void store(void* row, int i, const float (&f)[E]) {
     if constexpr (!std::is_same_v<W, None>) {
+        static_assert(E * sizeof(W) % 16 == 0 || E == 1, "");
         char* p = static_cast<char*>(row) + (int64_t)i * E * (int)sizeof(W);
         if constexpr (sizeof(W) == 4) {
             if constexpr (E % 4 == 0) {
 #pragma unroll
                 for (int j = 0; j < E / 4; ++j)
                     reinterpret_cast<float4*>(p)[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
-            } else if constexpr (E == 2) *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
-            else *reinterpret_cast<float*>(p) = f[0];
+            } else *reinterpret_cast<float*>(p) = f[0];
         } else {
             uint32_t w[(E + 1) / 2];
 #pragma unroll
@@ -79,7 +77,6 @@ __device__ __forceinline__ void store(void* row, int i, const float (&f)[E]) {
                 w[j / 2] = *reinterpret_cast<const uint32_t*>(&b);
             }
             if constexpr (E == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-            else if constexpr (E == 2) *reinterpret_cast<uint32_t*>(p) = w[0];
             else *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
         }
     }
