@@ -149,7 +149,8 @@ __device__ __forceinline__ void load_interleaved(const W* row, int c, int cols, 
     }
 }
 
-// one value of packed rows of nb blocks
+// one value of packed rows of nb blocks: a byte and a scale fetched for each (down gradient on the CUDA cores, 128
+// float32 rows an expert, d 256, I 512: 33 us against 27 from g and u in float32; 256 rows, d 1024: 141 against 131)
 __device__ __forceinline__ float value_at(const int8_t* q, const uint8_t* scale, int64_t row, int col, int nb) {
     const int64_t block = row * nb + col / 32;
     const int c = col & 31;

@@ -7,14 +7,21 @@
 // algebra that would give both at once, sum (r + a v)^2 from three sums, cancels
 // where the branch undoes the residual, and is not used.
 //
-// Bound: HBM for long batches, the call's host time for a few tokens.  Three forms:
+// Bound: a row's chain of waits for long batches, the call's host time for a few
+// tokens.  Three forms (figures of long runs over changing inputs):
 //   ring       long batches: 8192 tokens of 3584 bf16 values, a gate a token: 51 us
 //              for 235 MB, 0.68 of the measured copy bandwidth (registers: 77);
-//              a norm alone 29 us, 0.60
+//              a norm alone 29 us, 0.60.  Three rows are in work on an SM there, one
+//              at 4096 tokens of 8192 (73 us, 0.54; 36, 0.55), and each goes through
+//              wait, squares, barrier, root and stores on its own: 1.5 us.  Rows of
+//              float32 have more bytes a step: 8192 tokens of 2048, 47 us, 0.84
 //   registers  a thread's 16 values stay; 8 tokens of 4096: 5 us on the device
-//   C = 0      rows beyond that (d above 8192, odd d above 4096), read three times
-// Rows of odd length or address are read value by value (8192 tokens of 2001: 80 us,
-// 0.24): a vector that straddled two rows would need the neighbour's values.
+//   C = 0      rows beyond that (d above 8192; value by value above 4096), read three
+//              times: 256 tokens of 65536, a norm alone 23 us, 0.42
+// Rows whose length, stride or address is not of whole 16-byte vectors (8 bf16 or 4
+// float32 values) are read value by value (8192 tokens of 2001: 80 us, 0.24): a vector
+// across the end of an odd row would hold the neighbour's values, and narrower
+// vectors for even rows are not built.
 #include "train_norm.cuh"
 
 namespace moe {

@@ -234,8 +234,9 @@ __device__ __forceinline__ void get_factors(const float* f, int n_vec, int i, Pa
 // Whether a batch takes the ring, and its geometry: `groups` rows at a time of
 // `group` threads each, at most `threads` and `most` groups in all; at least
 // four rows a group.  More groups of two stages beat fewer of three: norm gradient
-// of 16384 tokens, d 1536, eight against six 38 -> 35 us; 8192 float32 tokens, d 2048,
-// 70 -> 57, block gradient 87 -> 77; nothing measured got slower.
+// of 16384 tokens, d 1536, eight against six 38 -> 35 us with warm caches, 41 -> 40 on
+// inputs that change; of 8192 float32 tokens, d 2048, on inputs that change 70 -> 57,
+// block gradient 87 -> 77; nothing measured got slower.
 struct RingShape {
     int group, groups, blocks;
     uint32_t smem;

@@ -10,15 +10,24 @@
 // Sums over the tokens: a group of threads that owns a row's columns takes
 // many rows and keeps two sums a column, of dnext xo and of D v without the
 // weights; dgate of a channel and dw_post are both multiples of the latter.
-// A second launch adds the groups' sums in their order (3 us for the 152 blocks of
-// a long batch).
+// A second launch adds the groups' sums in their order (8 us for the 152 blocks of
+// a long batch, 3 in long runs).
 //
 // Bound: HBM beside the issue rate (53 % of the slots, DRAM at 0.72 of copy).  8192
-// tokens of 3584 bf16 values, a gate a token: 75 us for 352 MB, both launches; rows
-// from global memory to registers took 133, the ring without pairs and with a row's
-// rstd fetched when it is needed 90.  16384 tokens of 1536, a norm alone: 40 us for
-// 201 MB (its first launch 33.5, 0.88 of copy).  Eight values a thread instead of
-// 16, 1024 threads of 64 registers: 105 us and 45.
+// tokens of 3584 bf16 values, a gate a token: 75 us for 352 MB, both launches, on
+// inputs that change (71 in long runs); rows from global memory to registers took 133,
+// the ring without pairs and with a row's rstd fetched when it is needed 90.  16384
+// tokens of 1536, a norm alone: 39 us for 201 MB (32 in long runs).  Eight values a
+// thread instead of 16, 1024 threads of 64 registers: 105 us and 45.
+//
+// What does not take the ring is slower by far: rows whose inputs leave it no room, as
+// 4096 tokens of 8192 with a float32 branch (245 us, 0.32 of copy; with a full gate,
+// which also leaves the threads too few, 265, 0.37), for the register form spills there
+// (92 and 132 bytes at two bf16 vectors a thread, 992 at four of float32: 300 tokens of
+// 8192 33 us, 0.26); rows above 8192 (256 of 65536: 526 us, for 12 MB hold the column
+// sums of 24 groups); value by value (8192 of 2001: 114 us, 0.25).  Many short rows
+// leave most of the ring's threads without work: 65536 tokens of 256, a norm alone, 38 us,
+// 0.39.
 #include "train_norm.cuh"
 
 namespace moe {

@@ -17,10 +17,14 @@ using namespace pack8;
 constexpr int kThreads = 256, kWarps = kThreads / 32, kCols = 256;  // columns of a warp
 
 // A warp takes several pieces of kCols columns of a row at a time, all their loads
-// before any use; a row's pieces are split evenly.  Pack and gather of
-// 4096 tokens of 3584 values, 8 slots each, four pieces to pack: four to unpack 67
-// us, five 65, seven (half a row) 61, eight (with more registers, and seven taken)
-// 64; the gather's writes alone take 35 at the copy bandwidth.  HBM writes bound it.
+// before any use; a row's pieces are split evenly.  Gather of 4096 tokens, 8 slots
+// each, in long runs over changing inputs, with at most four, five, seven, eight pieces:
+// d 3584 56, 52, 49, 50 us; d 1536 26, 27, 23, 24; d 4096 59, 62, 60, 55; of 6 slots, d
+// 2048, 25, 25, 27, 23.  Seven is half a row of 3584 and was taken there; it splits
+// 2048 and 4096 into more turns than eight does.  At d 3584 the packing before it takes
+// 12 us and the gather's bytes 37 at the copy bandwidth.
+// The issue rate bounds the gather (74 % of the slots, DRAM at 0.58 of copy): a token is
+// restored anew for each of its slots.
 constexpr int kPackPieces = 4, kUnpackPieces = 7;
 
 struct PackParams {
@@ -135,6 +139,8 @@ __global__ void __launch_bounds__(kThreads) unpack_rows_kernel(const PackParams 
 // an SM.  Without the words ahead 78, with dout from global memory 76; two blocks 87,
 // four (64 registers) 100; a branch a slot before its loads 171.  Two tokens a block
 // (1001 of 1536 values, Granite shape) take 11.3 us, 11.9 with dout from global memory.
+// Beyond eight slots 16 sums spill (170 to 220 bytes): 2048 tokens of 1536, 16 slots, 37
+// us, 0.63.
 constexpr int kGradWarps = 8, kGradBlocks = 3;  // a block's warps at most; blocks an SM
 
 struct GradParams {

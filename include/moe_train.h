@@ -77,7 +77,9 @@
 extern "C" {
 #endif
 
-/* Device workspace for the calls below with these dims (at most 16 MiB).
+/* Device workspace for the calls below with these dims (at most 16 MiB; 12 of it
+ * hold the sums over the tokens of moe_norm_rows_grad and moe_block_out_grad, and
+ * the other calls take a workspace without them).
  * Zero-fill it once before first use.  Its error word sits where moe_check()
  * looks for it. */
 moe_status moe_train_workspace_size(const moe_dims* dims, size_t* bytes);
